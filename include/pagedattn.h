@@ -475,6 +475,207 @@ PA_API int pa_gather_kv(void* k_out, void* v_out, uint8_t* mask, const pa_pool* 
                  int batch, int max_len, pa_stream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * Several new tokens per sequence: norm, rotation and append; attention.
+ *
+ * Both calls take the batch's new tokens packed: rows query_starts[b] ..
+ * query_starts[b + 1] - 1 of q (and k, v) are sequence b's n_b new tokens, the
+ * last n_b of its context_lens[b]; the i-th stands at position
+ * context_lens[b] - n_b + i.  query_starts: device int32 [batch + 1], from 0,
+ * not decreasing, at most num_tokens at the end (n_b = 0 is fine).  Rows
+ * behind the last sequence are neither read nor written.  A sequence with
+ * n_b > context_lens[b] or a length past its table sets PA_STATUS_BAD_LENGTH
+ * and its output rows are zero; starts that break the rule above set it too,
+ * and the rows they bound are unspecified.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary frequencies: a host object that holds no device memory. */
+typedef struct pa_rope pa_rope;
+
+enum {
+    PA_ROPE_PLAIN = 0,   /* f_j = base^(-2 j / rotary_dim) */
+    PA_ROPE_LINEAR = 1,  /* f_j / factor (positions interpolated) */
+    PA_ROPE_NTK = 2,     /* base * factor^(rotary_dim / (rotary_dim - 2)) in place of base */
+    PA_ROPE_PARTS = 3    /* by wavelength: with r = original_len * f_j / (2 pi) turns over the
+                          * trained length and g = clamp((r - low) / (high - low), 0, 1),
+                          * f_j * ((1 - g) / factor + g) */
+};
+
+/*
+ * The rotary_dim / 2 frequencies (radians per position) of a scaling rule into
+ * the host array `frequencies`.  rotary_dim: a positive multiple of 16; base >
+ * 1; factor > 0 (not used by PA_ROPE_PLAIN); original_len > 0 and low < high
+ * for PA_ROPE_PARTS (not used by the others).
+ * Cites: no counterpart on the pages (they show no model around the cache).
+ */
+PA_API int pa_rope_frequencies(double* frequencies, int rotary_dim, double base, int scaling,
+                               double factor, double original_len, double low, double high);
+
+/*
+ * A rotation of the first rotary_dim elements of a head: pair j turns by
+ * position * frequencies[j] and is scaled by `amplitude` (1 for none).
+ * interleaved != 0: the pairs are (2 j, 2 j + 1); 0: (j, j + rotary_dim / 2).
+ * rotary_dim: a multiple of 16, 16 .. 128; frequencies: host, each in
+ * [0, 2 pi).  They are kept as 64-bit fractions of a turn, so that far
+ * positions lose nothing.
+ * Cites: no counterpart on the pages (they show no model around the cache).
+ */
+PA_API int pa_rope_create(pa_rope** out, int rotary_dim, int interleaved,
+                          const double* frequencies, double amplitude);
+
+/* NULL is accepted.
+ * Cites: no counterpart on the pages (see pa_rope_create). */
+PA_API int pa_rope_destroy(pa_rope* rope);
+
+/*
+ * For every new token, in one pass: the RMS norm of each query and key head
+ * (x * rsqrt(mean(x^2) + eps) * weight, in fp32), the rotation of `rope` at the
+ * token's position, the query to q_out and the key and value to the token's
+ * slot of the cache (as pa_write_kv).  One rounding, at the store; values are
+ * copied bit for bit.
+ *   q_out         device [num_tokens, num_heads, head_dim] of the pool dtype,
+ *                 contiguous, 16-byte aligned.  May be q itself (same stride);
+ *                 must not overlap the inputs otherwise.
+ *   q, k, v       device rows of num_heads / num_kv_heads / num_kv_heads heads
+ *                 of the pool dtype; *_stride elements from token to token (at
+ *                 least the row, a multiple of 16 bytes), 16-byte aligned: the
+ *                 slices of one packed projection will do.
+ *   rope          NULL: no rotation; rotary_dim <= head_dim.
+ *   q_weight, k_weight  device [head_dim] of the pool dtype, 16-byte aligned;
+ *                 both NULL: no norm (eps is not used).
+ *   context_lens  device int32 [batch], the new tokens included.
+ *   query_starts  as above; NULL: one new token per sequence (num_tokens ==
+ *                 batch).
+ * Only the table entries of the new tokens' blocks are read.  A bad one sets
+ * PA_STATUS_BAD_BLOCK_ID and those K and V rows are not stored.  No two
+ * sequences may append to the same block.  head_dim 64 or 128.
+ * Cites: the append as pa_write_kv; the norm and the rotation have no
+ * counterpart on the pages.
+ */
+PA_API int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const void* q,
+                                 int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const pa_rope* rope,
+                                 const void* q_weight, const void* k_weight, float eps,
+                                 const int* block_tables, int max_blocks_per_seq,
+                                 const int* context_lens, const int* query_starts, int batch,
+                                 int num_tokens, int num_heads, pa_stream_t stream);
+
+/*
+ * Causal attention of the new tokens over the cache, which holds them already
+ * (prompts, chunks of prompts behind a cached prefix, a few tokens to verify):
+ *   out[t][h] = softmax_s(scale * q[t][h] . K_s) V_s over s <= position of t,
+ * rows resolved through the block table as in pa_decode_attention, fp32 scores
+ * and sums.  What lies in the cache at positions a row does not see (future
+ * tokens, rows past the context), be it NaN, does not reach that row.
+ *   out, q        device [num_tokens, num_heads, head_dim] of the pool dtype,
+ *                 contiguous, 16-byte aligned; they must not overlap.
+ *   workspace     at least pa_prefill_workspace_size() bytes, 256-byte aligned
+ *                 (may be NULL when that is 0); concurrent calls need separate
+ *                 ones.
+ * head_dim 64 or 128, block_size 16 or 32, any GQA group.  A bad table entry
+ * sets PA_STATUS_BAD_BLOCK_ID and its tokens get no weight (none left: a zero
+ * row).
+ * Cites: as pa_decode_attention ("vllmini", "The CUDA Block Kernel"), for more
+ * than one query per sequence, which the pages do not show.
+ */
+PA_API int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int layer,
+                                const int* block_tables, int max_blocks_per_seq,
+                                const int* context_lens, const int* query_starts, int batch,
+                                int num_tokens, int num_heads, float scale, void* workspace,
+                                size_t workspace_bytes, pa_stream_t stream);
+
+/* Workspace bytes of pa_prefill_attention for these sizes on the current
+ * device (0 when nothing is split).
+ * Cites: no counterpart on the pages (the scratch of split contexts). */
+PA_API int pa_prefill_workspace_size(const pa_pool* pool, int batch, int num_tokens,
+                                     int num_heads, int max_blocks_per_seq, size_t* bytes);
+
+/* ----------------------------------------------------------------------------
+ * Pages: copies, sequences that share pages, compaction.
+ *
+ * `shares` is a caller-owned device int32 array [num_blocks]: the owners of a
+ * page beyond the first.  Zeros describe a pool in which nothing is shared, so
+ * it starts as zeros, and pa_device_alloc_blocks (whose pages have one owner)
+ * needs no word of it; rows that may share pages are freed by
+ * pa_device_free_shared instead of pa_device_free_blocks.  dev_stack is the
+ * device stack of pa_device_stack_upload.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Copy page src_ids[i] to page dst_ids[i] (every layer and KV head, K and V,
+ * bit for bit), i < n.  Both device int32 [n].  The copies run in no order: no
+ * destination may be another pair's source or destination (the page's contents
+ * are unspecified then).  A pair with an id outside the pool is skipped and
+ * flagged (PA_STATUS_BAD_BLOCK_ID).
+ * Cites: no counterpart on the pages (they move no blocks).
+ */
+PA_API int pa_copy_blocks(pa_pool* pool, const int* src_ids, const int* dst_ids, int n,
+                          pa_stream_t stream);
+
+/*
+ * Rows children[i] of the tables become continuations of rows parents[i],
+ * i < n: the full pages are shared (shares += 1), the partial last one, if any,
+ * is copied (its live rows) into a page from the stack's top, in increasing i,
+ * the rest of the row is -1, and context_lens[child] = context_lens[parent].
+ * Parent and child then append independently.  The children's rows must hold no
+ * pages (free them first), be distinct, and not be parents in the same call.
+ *   block_tables  device int32 [batch, max_blocks_per_seq]; context_lens [batch].
+ * When the stack runs dry, the entries of the pages that were not to be had
+ * are -1 (PA_STATUS_NO_FREE_BLOCKS).  Pairs with rows outside [0, batch), a row
+ * as its own parent or a bad parent length are skipped (PA_STATUS_BAD_LENGTH).
+ * Cites: no counterpart on the pages (their tables share no blocks); new pages
+ * come from the free list as in mini-infer, "Python Implementation: Physical
+ * Block Pool".
+ */
+PA_API int pa_device_fork_sequences(pa_pool* pool, void* dev_stack, int* shares,
+                                    int* block_tables, int max_blocks_per_seq, int* context_lens,
+                                    int batch, const int* parents, const int* children, int n,
+                                    pa_stream_t stream);
+
+/*
+ * pa_device_free_blocks for rows that may share pages: every entry of a
+ * finished row gives up one ownership (shares -= 1), and a page that no one
+ * owns any more is pushed, in row and table order of the last owner that gave
+ * it up here.  Without sharing it does what pa_device_free_blocks does.  A page
+ * listed more often than it has owners is pushed once.
+ * batch * max_blocks_per_seq <= 2^30.
+ * Cites: mini-infer, "Python Implementation: Physical Block Pool" (free_block,
+ * once per block no sequence uses any more).
+ */
+PA_API int pa_device_free_shared(pa_pool* pool, void* dev_stack, int* shares, int* block_tables,
+                                 int max_blocks_per_seq, const int* context_lens,
+                                 const uint8_t* finished, int batch, pa_stream_t stream);
+
+/*
+ * Defragment: the pages in use (all that are not on the stack) move to the ids
+ * [0, live).  The i-th smallest used id >= live goes to the i-th smallest free
+ * id below it; the others stay.  Written are
+ *   out_stack     the new stack, num_blocks + 1 entries: the lowest free id on
+ *                 top, -1 above the height;
+ *   out_tables    block_tables with the used entries renumbered (entries past
+ *                 ceil(context_lens[b] / B) as they are); may be block_tables;
+ *   out_shares    shares by new id (NULL with shares NULL);
+ *   remap         [num_blocks], the new id of each used page, -1 for free ones,
+ *                 for page ids held elsewhere.
+ * out_stack, out_shares and remap must not be (or overlap) the inputs.  The
+ * pages that moved keep their old bytes too, so work in flight on the old
+ * tables is not disturbed as long as it appends nothing.  Used entries outside
+ * the pool or on the stack become -1 (PA_STATUS_BAD_BLOCK_ID).
+ * workspace: pa_compact_workspace_size() bytes, 256-byte aligned.  Pools of up
+ * to 786,432 blocks (PA_ERR_UNSUPPORTED above).
+ * Cites: no counterpart on the pages (blocks of a fixed size need no
+ * defragmentation to be used; this makes the upper part of a pool free).
+ */
+PA_API int pa_device_compact_blocks(pa_pool* pool, const void* dev_stack, const int* shares,
+                                    const int* block_tables, int max_blocks_per_seq,
+                                    const int* context_lens, int batch, void* out_stack,
+                                    int* out_shares, int* out_tables, int* remap, void* workspace,
+                                    size_t workspace_bytes, pa_stream_t stream);
+
+/* Workspace bytes of pa_device_compact_blocks.
+ * Cites: no counterpart on the pages (as pa_device_compact_blocks). */
+PA_API int pa_compact_workspace_size(const pa_pool* pool, size_t* bytes);
+
+/* ----------------------------------------------------------------------------
  * Device status.
  * ------------------------------------------------------------------------- */
 

@@ -31,6 +31,11 @@ PA_DECODE_TCGEN05 = 3
 PA_DTYPE_F32 = 0
 PA_DTYPE_BF16 = 1
 
+PA_ROPE_PLAIN = 0
+PA_ROPE_LINEAR = 1
+PA_ROPE_NTK = 2
+PA_ROPE_PARTS = 3
+
 PA_STATUS_BAD_BLOCK_ID = 0x1
 PA_STATUS_BAD_LENGTH = 0x2
 PA_STATUS_TIMEOUT = 0x4
@@ -72,6 +77,8 @@ _F = ctypes.c_float
 _PI = ctypes.POINTER(ctypes.c_int)
 _PSZ = ctypes.POINTER(ctypes.c_size_t)
 _PU = ctypes.POINTER(ctypes.c_uint)
+_L = ctypes.c_int64
+_D = ctypes.c_double
 
 _SIGNATURES = {
     "pa_last_error_string": ([], ctypes.c_char_p),
@@ -103,6 +110,18 @@ _SIGNATURES = {
     "pa_decode_attention_noalloc": (
         [_P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P], _I),
     "pa_gather_kv": ([_P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _P], _I),
+    "pa_rope_frequencies": ([_P, _I, _D, _I, _D, _D, _D, _D], _I),
+    "pa_rope_create": ([ctypes.POINTER(_P), _I, _I, _P, _D], _I),
+    "pa_rope_destroy": ([_P], _I),
+    "pa_norm_rope_write_kv": ([_P, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _F, _P, _I, _P, _P,
+                               _I, _I, _I, _P], _I),
+    "pa_prefill_attention": ([_P, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _F, _P, _SZ, _P], _I),
+    "pa_prefill_workspace_size": ([_P, _I, _I, _I, _I, _PSZ], _I),
+    "pa_copy_blocks": ([_P, _P, _P, _I, _P], _I),
+    "pa_device_fork_sequences": ([_P, _P, _P, _P, _I, _P, _I, _P, _P, _I, _P], _I),
+    "pa_device_free_shared": ([_P, _P, _P, _P, _I, _P, _P, _I, _P], _I),
+    "pa_device_compact_blocks": ([_P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "pa_compact_workspace_size": ([_P, _PSZ], _I),
     "pa_get_status": ([_PU, _P], _I),
     "pa_selftest_wait_timeout": ([_P], _I),
 }
@@ -373,6 +392,101 @@ def pa_gather_kv(k_out, v_out, mask, pool: int, layer: int, block_tables, max_bl
     _check(lib().pa_gather_kv(_ptr(k_out), _ptr(v_out), _ptr(mask), pool, layer,
                               _ptr(block_tables), max_blocks_per_seq, _ptr(context_lens), batch,
                               max_len, _stream(stream)), "pa_gather_kv")
+
+
+# --------------------------------------- several new tokens per sequence
+
+
+def pa_rope_frequencies(rotary_dim: int, base: float, scaling: int = PA_ROPE_PLAIN,
+                        factor: float = 1.0, original_len: float = 0.0, low: float = 0.0,
+                        high: float = 0.0) -> list:
+    out = (_D * max(1, rotary_dim // 2))()
+    _check(lib().pa_rope_frequencies(ctypes.cast(out, _P), rotary_dim, base, scaling, factor,
+                                     original_len, low, high), "pa_rope_frequencies")
+    return list(out)
+
+
+def pa_rope_create(rotary_dim: int, interleaved: bool, frequencies, amplitude: float = 1.0) -> int:
+    if rotary_dim > 0 and len(frequencies) != rotary_dim // 2:
+        raise ValueError(f"{rotary_dim // 2} frequencies expected, got {len(frequencies)}")
+    arr = (_D * max(1, len(frequencies)))(*[float(f) for f in frequencies])
+    h = _P()
+    _check(lib().pa_rope_create(ctypes.byref(h), rotary_dim, int(bool(interleaved)),
+                                ctypes.cast(arr, _P), amplitude), "pa_rope_create")
+    return h.value
+
+
+def pa_rope_destroy(rope: int) -> None:
+    _check(lib().pa_rope_destroy(rope), "pa_rope_destroy")
+
+
+def pa_norm_rope_write_kv(pool: int, layer: int, q_out, q, q_stride: int, k, k_stride: int, v,
+                          v_stride: int, rope, q_weight, k_weight, eps: float, block_tables,
+                          max_blocks_per_seq: int, context_lens, query_starts, batch: int,
+                          num_tokens: int, num_heads: int, stream=None) -> None:
+    _check(lib().pa_norm_rope_write_kv(
+        pool, layer, _ptr(q_out), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, rope,
+        _ptr(q_weight), _ptr(k_weight), eps, _ptr(block_tables), max_blocks_per_seq,
+        _ptr(context_lens), _ptr(query_starts), batch, num_tokens, num_heads, _stream(stream)),
+        "pa_norm_rope_write_kv")
+
+
+def pa_prefill_attention(out, q, pool: int, layer: int, block_tables, max_blocks_per_seq: int,
+                         context_lens, query_starts, batch: int, num_tokens: int, num_heads: int,
+                         scale: float, workspace=None, workspace_bytes: int = 0,
+                         stream=None) -> None:
+    _check(lib().pa_prefill_attention(
+        _ptr(out), _ptr(q), pool, layer, _ptr(block_tables), max_blocks_per_seq,
+        _ptr(context_lens), _ptr(query_starts), batch, num_tokens, num_heads, scale,
+        _ptr(workspace), workspace_bytes, _stream(stream)), "pa_prefill_attention")
+
+
+def pa_prefill_workspace_size(pool: int, batch: int, num_tokens: int, num_heads: int,
+                              max_blocks_per_seq: int) -> int:
+    v = _SZ()
+    _check(lib().pa_prefill_workspace_size(pool, batch, num_tokens, num_heads, max_blocks_per_seq,
+                                           ctypes.byref(v)), "pa_prefill_workspace_size")
+    return v.value
+
+
+# ------------------------------------------------------------------- pages
+
+
+def pa_copy_blocks(pool: int, src_ids, dst_ids, n: int, stream=None) -> None:
+    _check(lib().pa_copy_blocks(pool, _ptr(src_ids), _ptr(dst_ids), n, _stream(stream)),
+           "pa_copy_blocks")
+
+
+def pa_device_fork_sequences(pool: int, dev_stack, shares, block_tables, max_blocks_per_seq: int,
+                             context_lens, batch: int, parents, children, n: int,
+                             stream=None) -> None:
+    _check(lib().pa_device_fork_sequences(
+        pool, _ptr(dev_stack), _ptr(shares), _ptr(block_tables), max_blocks_per_seq,
+        _ptr(context_lens), batch, _ptr(parents), _ptr(children), n, _stream(stream)),
+        "pa_device_fork_sequences")
+
+
+def pa_device_free_shared(pool: int, dev_stack, shares, block_tables, max_blocks_per_seq: int,
+                          context_lens, finished, batch: int, stream=None) -> None:
+    _check(lib().pa_device_free_shared(
+        pool, _ptr(dev_stack), _ptr(shares), _ptr(block_tables), max_blocks_per_seq,
+        _ptr(context_lens), _ptr(finished), batch, _stream(stream)), "pa_device_free_shared")
+
+
+def pa_device_compact_blocks(pool: int, dev_stack, shares, block_tables, max_blocks_per_seq: int,
+                             context_lens, batch: int, out_stack, out_shares, out_tables, remap,
+                             workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().pa_device_compact_blocks(
+        pool, _ptr(dev_stack), _ptr(shares), _ptr(block_tables), max_blocks_per_seq,
+        _ptr(context_lens), batch, _ptr(out_stack), _ptr(out_shares), _ptr(out_tables),
+        _ptr(remap), _ptr(workspace), workspace_bytes, _stream(stream)),
+        "pa_device_compact_blocks")
+
+
+def pa_compact_workspace_size(pool: int) -> int:
+    v = _SZ()
+    _check(lib().pa_compact_workspace_size(pool, ctypes.byref(v)), "pa_compact_workspace_size")
+    return v.value
 
 
 def pa_get_status(stream=None) -> int:

@@ -31,6 +31,12 @@ struct pa_pool {
     mutable std::mutex mu;
 };
 
+struct pa_rope {
+    int rotary_dim, interleaved;
+    float amplitude;
+    unsigned long long freq[pa::kMaxRotaryPairs];  // turns per position, in 2^-64
+};
+
 namespace {
 
 thread_local std::string t_last_error;
@@ -861,6 +867,424 @@ int pa_gather_kv(void* k_out, void* v_out, uint8_t* mask, const pa_pool* pool, i
     if (e != cudaSuccess) return cuda_fail(e, "pa_gather_kv launch");
     return PA_OK;
 }
+
+}  // extern "C"
+
+// ------------------------------------------- several new tokens per sequence
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925;
+
+// The device addresses of a table, its lengths and an optional index array.
+int check_tables(const int* block_tables, int maxb, int block_size, const int* context_lens,
+                 int batch) {
+    if (batch < 0) return fail(PA_ERR_INVALID_ARG, "batch %d < 0", batch);
+    if (maxb <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq %d <= 0", maxb);
+    if ((long long)maxb * block_size > INT_MAX)
+        return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq * block_size overflows int");
+    if (batch == 0) return PA_OK;
+    if (!block_tables || !context_lens || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return fail(PA_ERR_INVALID_ARG,
+                    "block_tables and context_lens must be non-NULL and 4-byte aligned");
+    return PA_OK;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const char* x = static_cast<const char*>(a);
+    const char* y = static_cast<const char*>(b);
+    return na && nb && x < y + nb && y < x + na;
+}
+
+int page_geom(const pa_pool* pool, pa::PageGeom* out) {
+    unsigned* status = nullptr;
+    cudaError_t e = pa::status_word(&status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    const pa::PoolGeom& g = pool->g;
+    *out = pa::PageGeom{g.k_base, g.v_base, g.s_blk, g.s_layer,     g.s_head, g.num_blocks,
+                        g.L,      g.Hkv,    g.B,     g.elt, g.B * g.D * g.elt, status};
+    return PA_OK;
+}
+
+int check_stack(const void* dev_stack) {
+    if (!dev_stack || !aligned(dev_stack, 4))
+        return fail(PA_ERR_INVALID_ARG, "dev_stack must be non-NULL and 4-byte aligned");
+    return PA_OK;
+}
+
+// What both prefill calls need of the sizes.
+int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads, int maxb,
+                  int* splits, size_t* ws_bytes) {
+    const pa::PoolGeom& g = pool->g;
+    if (batch < 0 || num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "batch (%d) and num_tokens (%d) must be >= 0", batch,
+                    num_tokens);
+    if (num_heads <= 0 || num_heads % g.Hkv != 0)
+        return fail(PA_ERR_INVALID_ARG, "num_heads %d is not a positive multiple of num_kv_heads %d",
+                    num_heads, g.Hkv);
+    if (maxb <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq %d <= 0", maxb);
+    if ((long long)maxb * g.B > INT_MAX)
+        return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq * block_size overflows int");
+    if ((long long)num_tokens * num_heads > INT_MAX)
+        return fail(PA_ERR_INVALID_ARG, "num_tokens * num_heads overflows int");
+    if (!pa::prefill_supported(g.dtype, g.D, g.B))
+        return fail(PA_ERR_UNSUPPORTED,
+                    "no prefill kernel for dtype=%d head_dim=%d block_size=%d (built: head_dim "
+                    "64/128, block_size 16/32)",
+                    g.dtype, g.D, g.B);
+    *splits = 1, *ws_bytes = 0;
+    if (batch == 0 || num_tokens == 0) return PA_OK;
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    *splits = pa::prefill_splits(g.dtype, g.D, num_heads / g.Hkv, g.Hkv, batch, num_tokens, maxb,
+                                 g.B, sms);
+    *ws_bytes = pa::prefill_workspace_bytes(g.dtype, g.D, num_heads, num_tokens, *splits);
+    return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pa_rope_frequencies(double* frequencies, int rotary_dim, double base, int scaling,
+                        double factor, double original_len, double low, double high) {
+    if (!frequencies) return fail(PA_ERR_INVALID_ARG, "frequencies is NULL");
+    if (rotary_dim <= 0 || rotary_dim % 16 != 0)
+        return fail(PA_ERR_INVALID_ARG, "rotary_dim %d is not a positive multiple of 16", rotary_dim);
+    if (!(base > 1.0) || !std::isfinite(base))
+        return fail(PA_ERR_INVALID_ARG, "base must be finite and above 1");
+    if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_PARTS)
+        return fail(PA_ERR_INVALID_ARG, "unknown scaling %d", scaling);
+    if (scaling != PA_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor)))
+        return fail(PA_ERR_INVALID_ARG, "factor must be finite and positive");
+    if (scaling == PA_ROPE_PARTS &&
+        (!(original_len > 0.0) || !std::isfinite(original_len) || !(low < high) ||
+         !std::isfinite(low) || !std::isfinite(high)))
+        return fail(PA_ERR_INVALID_ARG, "parts: original_len > 0 and low < high, all finite");
+    const double r = rotary_dim;
+    if (scaling == PA_ROPE_NTK) base *= std::pow(factor, r / (r - 2.0));
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        double f = std::pow(base, -2.0 * j / r);
+        if (scaling == PA_ROPE_LINEAR) f /= factor;
+        if (scaling == PA_ROPE_PARTS) {
+            const double turns = original_len * f / kTwoPi;
+            const double g = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+            f = f * (1.0 - g) / factor + f * g;
+        }
+        frequencies[j] = f;
+    }
+    return PA_OK;
+}
+
+int pa_rope_create(pa_rope** out, int rotary_dim, int interleaved, const double* frequencies,
+                   double amplitude) {
+    if (!out) return fail(PA_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    if (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > 2 * pa::kMaxRotaryPairs)
+        return fail(PA_ERR_INVALID_ARG, "rotary_dim %d is not a multiple of 16 in 16 .. %d",
+                    rotary_dim, 2 * pa::kMaxRotaryPairs);
+    if (!frequencies) return fail(PA_ERR_INVALID_ARG, "frequencies is NULL");
+    if (!std::isfinite(amplitude) || !std::isfinite((float)amplitude))
+        return fail(PA_ERR_INVALID_ARG, "amplitude is not finite");
+    pa_rope* r = new (std::nothrow) pa_rope();
+    if (!r) return fail(PA_ERR_INVALID_ARG, "host allocation failed");
+    r->rotary_dim = rotary_dim;
+    r->interleaved = interleaved != 0;
+    r->amplitude = (float)amplitude;
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        const double turns = frequencies[j] / kTwoPi;
+        // (rounds to below 1: the largest double below it is 1 - 2^-53)
+        if (!(turns >= 0.0 && turns < 1.0)) {
+            delete r;
+            return fail(PA_ERR_INVALID_ARG, "frequencies[%d] is outside [0, 2 pi)", j);
+        }
+        r->freq[j] = (unsigned long long)std::ldexp(turns, 64);
+    }
+    *out = r;
+    return PA_OK;
+}
+
+int pa_rope_destroy(pa_rope* rope) {
+    delete rope;
+    return PA_OK;
+}
+
+int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const pa_rope* rope, const void* q_weight, const void* k_weight,
+                          float eps, const int* block_tables, int max_blocks_per_seq,
+                          const int* context_lens, const int* query_starts, int batch,
+                          int num_tokens, int num_heads, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_layer(pool, layer)) return rc;
+    const pa::PoolGeom& g = pool->g;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+    if (!query_starts && num_tokens != batch)
+        return fail(PA_ERR_INVALID_ARG, "without query_starts num_tokens (%d) must be batch (%d)",
+                    num_tokens, batch);
+    if (num_heads <= 0 || num_heads % g.Hkv != 0)
+        return fail(PA_ERR_INVALID_ARG, "num_heads %d is not a positive multiple of num_kv_heads %d",
+                    num_heads, g.Hkv);
+    if (g.D != 64 && g.D != 128)
+        return fail(PA_ERR_UNSUPPORTED, "norm and rotation are built for head_dim 64 and 128, not %d",
+                    g.D);
+    if (rope && rope->rotary_dim > g.D)
+        return fail(PA_ERR_INVALID_ARG, "rotary_dim %d is above head_dim %d", rope->rotary_dim, g.D);
+    if (!q_weight != !k_weight)
+        return fail(PA_ERR_INVALID_ARG, "q_weight and k_weight: both or neither");
+    if (q_weight && !(eps >= 0.f && std::isfinite(eps)))
+        return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (batch == 0 || num_tokens == 0) return PA_OK;
+    if (!q_out || !q || !k || !v || !aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) ||
+        !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+        return fail(PA_ERR_INVALID_ARG,
+                    "q_out, q, k, v must be non-NULL and, as the weights, 16-byte aligned");
+    if (query_starts && !aligned(query_starts, 4))
+        return fail(PA_ERR_INVALID_ARG, "query_starts must be 4-byte aligned");
+    const struct {
+        int64_t stride;
+        int heads;
+        const void* at;
+        const char* name;
+    } in[3] = {{q_stride, num_heads, q, "q"}, {k_stride, g.Hkv, k, "k"}, {v_stride, g.Hkv, v, "v"}};
+    const size_t out_bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
+    for (const auto& x : in) {
+        const int64_t row = (int64_t)x.heads * g.D;
+        if (x.stride < row || x.stride * g.elt % 16 != 0 || x.stride > (int64_t)1 << 40)
+            return fail(PA_ERR_INVALID_ARG,
+                        "%s_stride %lld: at least the row (%lld elements), a multiple of 16 bytes",
+                        x.name, (long long)x.stride, (long long)row);
+        if (x.at == q_out && x.at == q && q_stride == row) continue;  // in place
+        const size_t bytes = ((size_t)(num_tokens - 1) * x.stride + row) * g.elt;
+        if (overlap(q_out, out_bytes, x.at, bytes))
+            return fail(PA_ERR_INVALID_ARG, "q_out overlaps %s", x.name);
+    }
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    pa::NormRopeParams p{};
+    cudaError_t e = pa::status_word(&p.status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    p.q_out = q_out;
+    p.q = q, p.k = k, p.v = v;
+    p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+    p.q_weight = q_weight, p.k_weight = k_weight;
+    p.eps = eps;
+    p.k_base = g.k_base, p.v_base = g.v_base;
+    p.s_blk = g.s_blk, p.tile_off = layer * g.s_layer, p.s_head = g.s_head;
+    p.num_blocks = g.num_blocks;
+    p.H = num_heads, p.Hkv = g.Hkv, p.B = g.B;
+    p.bt = block_tables, p.maxb = max_blocks_per_seq;
+    p.lens = context_lens, p.starts = query_starts;
+    p.batch = batch, p.num_tokens = num_tokens;
+    p.amplitude = 1.f;
+    if (rope) {
+        p.rotary = rope->rotary_dim;
+        p.interleaved = rope->interleaved;
+        p.amplitude = rope->amplitude;
+        std::copy(rope->freq, rope->freq + rope->rotary_dim / 2, p.freq);
+    }
+    e = pa::launch_norm_rope(p, g.dtype, g.D, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_norm_rope_write_kv launch");
+    return PA_OK;
+}
+
+int pa_prefill_workspace_size(const pa_pool* pool, int batch, int num_tokens, int num_heads,
+                              int max_blocks_per_seq, size_t* bytes) {
+    if (int rc = check_pool(pool)) return rc;
+    if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes is NULL");
+    int splits = 1;
+    return prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &splits, bytes);
+}
+
+int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int layer,
+                         const int* block_tables, int max_blocks_per_seq, const int* context_lens,
+                         const int* query_starts, int batch, int num_tokens, int num_heads,
+                         float scale, void* workspace, size_t workspace_bytes,
+                         pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_layer(pool, layer)) return rc;
+    const pa::PoolGeom& g = pool->g;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
+    if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
+    int splits = 1;
+    size_t need = 0;
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &splits,
+                               &need))
+        return rc;
+    if (batch == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !aligned(out, 16) || !aligned(q, 16))
+        return fail(PA_ERR_INVALID_ARG, "out and q must be non-NULL and 16-byte aligned");
+    if (!query_starts || !aligned(query_starts, 4))
+        return fail(PA_ERR_INVALID_ARG, "query_starts must be non-NULL and 4-byte aligned");
+    const size_t bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
+    if (overlap(out, bytes, q, bytes)) return fail(PA_ERR_INVALID_ARG, "out overlaps q");
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return fail(PA_ERR_WORKSPACE,
+                    "workspace must be 256-byte aligned and hold %zu bytes (got %p, %zu)", need,
+                    workspace, workspace_bytes);
+    pa::PrefillParams p{};
+    cudaError_t e = pa::status_word(&p.status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    p.out = out;
+    p.q = q;
+    p.k_base = g.k_base, p.v_base = g.v_base;
+    p.s_blk = g.s_blk, p.tile_off = layer * g.s_layer, p.s_head = g.s_head;
+    p.num_blocks = g.num_blocks;
+    p.H = num_heads, p.Hkv = g.Hkv, p.G = num_heads / g.Hkv, p.layer = layer;
+    p.bt = block_tables, p.maxb = max_blocks_per_seq;
+    p.lens = context_lens, p.starts = query_starts;
+    p.batch = batch, p.num_tokens = num_tokens;
+    p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax evaluated with exp2
+    p.splits = splits;
+    if (need) {
+        p.part_o = static_cast<float*>(workspace);
+        p.part_ml = p.part_o + (size_t)splits * num_tokens * num_heads * g.D;
+    }
+    e = pa::launch_prefill(p, g.dtype, g.D, g.B, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
+    return PA_OK;
+}
+
+// --------------------------------------------------------------------- pages
+
+int pa_copy_blocks(pa_pool* pool, const int* src_ids, const int* dst_ids, int n,
+                   pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (n < 0) return fail(PA_ERR_INVALID_ARG, "n %d < 0", n);
+    if (n == 0) return PA_OK;
+    if (!src_ids || !dst_ids || !aligned(src_ids, 4) || !aligned(dst_ids, 4))
+        return fail(PA_ERR_INVALID_ARG, "src_ids and dst_ids must be non-NULL and 4-byte aligned");
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    pa::PageGeom g{};
+    if (int rc = page_geom(pool, &g)) return rc;
+    cudaError_t e = pa::launch_copy_blocks(g, src_ids, dst_ids, n, sms,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_copy_blocks launch");
+    return PA_OK;
+}
+
+int pa_device_fork_sequences(pa_pool* pool, void* dev_stack, int* shares, int* block_tables,
+                             int max_blocks_per_seq, int* context_lens, int batch,
+                             const int* parents, const int* children, int n, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
+        return rc;
+    if (n < 0 || n > batch)
+        return fail(PA_ERR_INVALID_ARG, "n %d outside [0, batch]: the children are distinct rows", n);
+    if (n == 0) return PA_OK;
+    if (int rc = check_stack(dev_stack)) return rc;
+    if (!shares || !parents || !children || !aligned(shares, 4) || !aligned(parents, 4) ||
+        !aligned(children, 4))
+        return fail(PA_ERR_INVALID_ARG,
+                    "shares, parents and children must be non-NULL and 4-byte aligned");
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    pa::ForkParams p{};
+    if (int rc = page_geom(pool, &p.g)) return rc;
+    p.stack = static_cast<int*>(dev_stack);
+    p.shares = shares, p.bt = block_tables, p.lens = context_lens;
+    p.maxb = max_blocks_per_seq, p.batch = batch;
+    p.parents = parents, p.children = children, p.n = n;
+    cudaError_t e = pa::launch_fork(p, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_device_fork_sequences launch");
+    return PA_OK;
+}
+
+int pa_device_free_shared(pa_pool* pool, void* dev_stack, int* shares, int* block_tables,
+                          int max_blocks_per_seq, const int* context_lens, const uint8_t* finished,
+                          int batch, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
+        return rc;
+    if ((long long)batch * max_blocks_per_seq > 1 << 30)
+        return fail(PA_ERR_INVALID_ARG, "batch * max_blocks_per_seq is above 2^30");
+    if (batch == 0) return PA_OK;
+    if (int rc = check_stack(dev_stack)) return rc;
+    if (!shares || !finished || !aligned(shares, 4))
+        return fail(PA_ERR_INVALID_ARG,
+                    "shares (4-byte aligned) and finished must be non-NULL");
+    pa::PageGeom g{};
+    if (int rc = page_geom(pool, &g)) return rc;
+    const pa::FreeSharedParams p{static_cast<int*>(dev_stack), shares, block_tables, context_lens,
+                                 finished, max_blocks_per_seq, batch, g.B, g.num_blocks, g.status};
+    cudaError_t e = pa::launch_free_shared(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_device_free_shared launch");
+    return PA_OK;
+}
+
+int pa_compact_workspace_size(const pa_pool* pool, size_t* bytes) {
+    if (int rc = check_pool(pool)) return rc;
+    if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes is NULL");
+    // a count, then the sources and destinations of at most half the pages
+    *bytes = 256 + 2 * align256((size_t)(pool->g.num_blocks / 2 + 1) * sizeof(int));
+    return PA_OK;
+}
+
+int pa_device_compact_blocks(pa_pool* pool, const void* dev_stack, const int* shares,
+                             const int* block_tables, int max_blocks_per_seq,
+                             const int* context_lens, int batch, void* out_stack, int* out_shares,
+                             int* out_tables, int* remap, void* workspace, size_t workspace_bytes,
+                             pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
+        return rc;
+    const long long nb = pool->g.num_blocks;
+    if (nb > 786432)
+        return fail(PA_ERR_UNSUPPORTED, "compaction is built for up to 786432 blocks, not %lld", nb);
+    if (int rc = check_stack(dev_stack)) return rc;
+    if (!out_stack || !remap || !aligned(out_stack, 4) || !aligned(remap, 4) ||
+        !aligned(shares, 4) || !aligned(out_shares, 4) || !aligned(out_tables, 4))
+        return fail(PA_ERR_INVALID_ARG,
+                    "out_stack and remap must be non-NULL; all arrays 4-byte aligned");
+    if (batch > 0 && !out_tables) return fail(PA_ERR_INVALID_ARG, "out_tables is NULL");
+    if (!shares != !out_shares)
+        return fail(PA_ERR_INVALID_ARG, "shares and out_shares: both or neither");
+    const size_t ints = (size_t)nb * sizeof(int), table = (size_t)batch * max_blocks_per_seq * 4;
+    const struct {
+        const void* at;
+        size_t bytes;
+    } in[4] = {{dev_stack, ints + 4}, {shares, shares ? ints : 0}, {block_tables, table},
+               {context_lens, (size_t)batch * 4}},
+      out[4] = {{out_stack, ints + 4}, {out_shares, shares ? ints : 0}, {remap, ints},
+                {out_tables, table}};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 4; ++i)
+            if (!(o == 3 && i == 2 && out_tables == block_tables) &&
+                overlap(out[o].at, out[o].bytes, in[i].at, in[i].bytes))
+                return fail(PA_ERR_INVALID_ARG, "an output overlaps an input (only out_tables may "
+                                                "be block_tables)");
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o].at, out[o].bytes, out[i].at, out[i].bytes))
+                return fail(PA_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    size_t need = 0;
+    if (int rc = pa_compact_workspace_size(pool, &need)) return rc;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+        return fail(PA_ERR_WORKSPACE,
+                    "workspace must be 256-byte aligned and hold %zu bytes (got %p, %zu)", need,
+                    workspace, workspace_bytes);
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    pa::CompactParams p{};
+    if (int rc = page_geom(pool, &p.g)) return rc;
+    p.stack = static_cast<const int*>(dev_stack);
+    p.shares = shares, p.bt = block_tables, p.lens = context_lens;
+    p.maxb = max_blocks_per_seq, p.batch = batch;
+    p.out_stack = static_cast<int*>(out_stack);
+    p.out_shares = out_shares, p.out_bt = out_tables, p.remap = remap;
+    p.move_count = static_cast<int*>(workspace);
+    p.move_src = p.move_count + 64;
+    p.move_dst = p.move_src + align256((size_t)(nb / 2 + 1) * sizeof(int)) / sizeof(int);
+    cudaError_t e = pa::launch_compact(p, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_device_compact_blocks launch");
+    return PA_OK;
+}
+
+}  // extern "C"
+
+extern "C" {
 
 int pa_selftest_wait_timeout(pa_stream_t stream) {
     unsigned* status = nullptr;

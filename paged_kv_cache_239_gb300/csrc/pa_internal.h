@@ -104,6 +104,95 @@ struct GatherParams {
     unsigned* status;
 };
 
+// Norm + rotation + append of new tokens (see pa_rope.cu).
+constexpr int kMaxRotaryPairs = 64;
+struct NormRopeParams {
+    void* q_out;             // [num_tokens, H, D]
+    const void *q, *k, *v;   // rows of heads; strides between tokens in elements
+    long long q_stride, k_stride, v_stride;
+    const void *q_weight, *k_weight;  // [D], both or neither
+    float eps, amplitude;
+    void *k_base, *v_base;
+    long long s_blk, tile_off, s_head;  // elements; tile_off = layer * s_layer
+    long long num_blocks;
+    int H, Hkv, B;
+    const int* bt;
+    int maxb;
+    const int* lens;
+    const int* starts;       // [batch + 1], or null: token t is sequence t
+    int batch, num_tokens, splits;
+    int rotary, interleaved;
+    unsigned* status;
+    unsigned long long freq[kMaxRotaryPairs];  // turns per position, as fractions of 2^64
+};
+
+// Attention of several new tokens per sequence (see pa_prefill_f32.cuh).
+struct PrefillParams {
+    void* out;               // [num_tokens, H, D], pool dtype
+    const void* q;           // [num_tokens, H, D], pool dtype
+    const void *k_base, *v_base;
+    long long s_blk, tile_off, s_head;  // elements; tile_off = layer * s_layer
+    long long num_blocks;
+    int H, Hkv, G, layer;
+    const int* bt;
+    int maxb;
+    const int* lens;
+    const int* starts;       // [batch + 1]
+    int batch, num_tokens;
+    float qscale;            // softmax scale * log2(e)
+    int splits;
+    float *part_o, *part_ml;
+    unsigned* status;
+};
+
+// The pages of a pool (see pa_pages.cu).
+struct PageGeom {
+    void *k_base, *v_base;
+    long long s_blk, s_layer, s_head;  // elements
+    long long num_blocks;
+    int L, Hkv, B, elt, tile_bytes;
+    unsigned* status;
+};
+struct ForkParams {
+    PageGeom g;
+    int *stack, *shares, *bt, *lens;
+    int maxb, batch;
+    const int *parents, *children;
+    int n;
+};
+struct FreeSharedParams {
+    int *stack, *shares, *bt;
+    const int* lens;
+    const uint8_t* finished;
+    int maxb, batch, B;
+    long long num_blocks;
+    unsigned* status;
+};
+struct CompactParams {
+    PageGeom g;
+    const int *stack, *shares, *bt, *lens;
+    int maxb, batch;
+    int *out_stack, *out_shares, *out_bt, *remap;
+    int *move_src, *move_dst, *move_count;
+};
+
+cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, int D, int num_sms,
+                             cudaStream_t s);
+bool prefill_supported(int dtype, int D, int B);
+// Rows (token, head of a group) per tile, and the splits of the contexts that
+// a call's size asks for.
+int prefill_splits(int dtype, int D, int G, int Hkv, int batch, int num_tokens, int maxb, int B,
+                   int num_sms);
+size_t prefill_workspace_bytes(int dtype, int D, int H, int num_tokens, int splits);
+cudaError_t launch_prefill(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s);
+
+cudaError_t launch_copy_blocks(const PageGeom& g, const int* src, const int* dst, int n,
+                               int num_sms, cudaStream_t s);
+cudaError_t launch_fork(const ForkParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_free_shared(const FreeSharedParams& p, cudaStream_t s);
+size_t compact_smem_bytes(long long num_blocks);
+cudaError_t launch_compact(const CompactParams& p, int num_sms, cudaStream_t s);
+
 // Returns cudaErrorNotSupported (without launching) when no kernel is built
 // for (dtype, D, B, G).
 cudaError_t launch_decode_bf16(const DecodeParams& p, int D, int B, int G, cudaStream_t s);

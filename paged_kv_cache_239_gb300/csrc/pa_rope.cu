@@ -1,0 +1,225 @@
+// pa_rope.cu -- new tokens on their way into the cache: per-head RMS norm of
+// queries and keys, rotary position embedding, and the append of K and V, in
+// one pass over the projections' output.
+//
+// Token t of sequence b (n_b new ones, this the i-th) stands at position
+// p = context_lens[b] - n_b + i.  For a query or key head x of D elements
+//   y_d = x_d * rsqrt(mean(x^2) + eps) * w_d                  (w given; else y = x)
+//   (y_a, y_b) -> A (y_a cos(p f_j) - y_b sin(p f_j), y_a sin(p f_j) + y_b cos(p f_j))
+// for the pairs j < r/2 of the first r elements: (a, b) = (2j, 2j + 1) when
+// interleaved, (j, j + r/2) in halves.  Everything is fp32 from the load to the
+// one rounding at the store.
+//
+// The angle: p f_j / 2 pi in turns is only needed modulo 1, so f_j / 2 pi is
+// kept as a 64-bit binary fraction and multiplied by p in wrapping integer
+// arithmetic: exact modulo 1 up to p * 2^-64 turns plus the fraction's own
+// rounding, where an fp32 product would be off by p f_j 2^-24 radians (0.008 at
+// p = 131072).  The top 32 bits, as a signed fraction of half a turn, go to
+// sincospif.
+//
+// What bounds it: bytes, (H + 2 Hkv) rows read and written per token.  A row
+// is read in 16-byte chunks, LPR lanes to a row, and stays in registers; a
+// lane's partner elements come by shuffle.  A warp serves one token and a share
+// of its rows, so it computes its lanes' sines once for all of them.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRopeThreads = 128;
+
+template <typename T>
+struct Chunk;  // 16 bytes of a row as floats
+
+template <>
+struct Chunk<float> {
+    static constexpr int E = 4;
+    static __device__ __forceinline__ void unpack(const uint4& w, float* x) {
+        x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float* x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+    }
+};
+
+template <>
+struct Chunk<__nv_bfloat16> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ void unpack(const uint4& w, float* x) {
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = bf16x2_to_float2(v[k]);
+            x[2 * k] = f.x, x[2 * k + 1] = f.y;
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float* x) {
+        uint32_t v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+            v[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+};
+
+// The number of starts[1 .. batch] that are <= t: the sequence of token t
+// (batch for a token behind the last sequence).  The whole warp counts, each
+// lane a 32nd of the array.
+__device__ __forceinline__ int find_sequence(const int* starts, int batch, int t, int lane) {
+    int n = 0;
+    for (int b = lane; b < batch; b += 32) n += ld_dep(starts + 1 + b) <= t ? 1 : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kFullMask, n, o);
+    return n;
+}
+
+template <typename T, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+    pdl_trigger();
+    pdl_wait();
+    using C = Chunk<T>;
+    constexpr int E = C::E;
+    constexpr int LPR = D / E;       // lanes per row
+    constexpr int RPW = 32 / LPR;    // rows per warp and pass
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(w / p.splits);
+    const int split = (int)(w % p.splits);
+    if (t >= p.num_tokens) return;
+    const int c = lane % LPR;        // this lane's chunk of its row
+    const int sub = lane / LPR;
+
+    // ---- where the token stands ----
+    int b = t, s0 = t, n_new = 1;
+    if (p.starts != nullptr) {
+        b = find_sequence(p.starts, p.batch, t, lane);
+        if (b >= p.batch) return;    // behind the last sequence: left as it is
+        s0 = ld_dep(p.starts + b);
+        n_new = ld_dep(p.starts + b + 1) - s0;
+    }
+    const int n = ld_dep(p.lens + b);
+    const int i = t - s0;
+    const bool good = n >= 0 && n <= p.maxb * p.B && i >= 0 && i < n_new && n_new <= n;
+    if (!good && split == 0 && lane == 0) atomicOr(p.status, kStatusBadLength);
+    const int pos = good ? n - n_new + i : 0;
+    int blk = good ? ld_dep(p.bt + (long long)b * p.maxb + pos / p.B) : -1;
+    if (good && (blk < 0 || blk >= p.num_blocks)) {
+        if (split == 0 && lane == 0) atomicOr(p.status, kStatusBadBlock);
+        blk = -1;
+    }
+
+    // ---- this lane's sines ----
+    constexpr int NF = INTERLEAVED ? E / 2 : E;
+    const int rc = p.rotary / E;     // chunks that turn
+    const bool turns = c < rc;
+    float cs[NF], sn[NF];
+    if (turns) {
+        const int f0 = INTERLEAVED ? c * (E / 2) : (c % (rc / 2)) * E;
+#pragma unroll
+        for (int k = 0; k < NF; ++k) {
+            const unsigned long long x = (unsigned long long)pos * p.freq[f0 + k];
+            const float half_turns = (float)(int)(x >> 32) * 4.656612873077393e-10f;  // 2^-31
+            sincospif(half_turns, &sn[k], &cs[k]);
+            sn[k] *= p.amplitude, cs[k] *= p.amplitude;
+        }
+    }
+    // halves: the partner chunk, and the sign of its sine's term
+    const int partner = turns ? (c < rc / 2 ? lane + rc / 2 : lane - rc / 2) : lane;
+    const bool low = c < rc / 2;
+
+    const int rows = p.H + 2 * p.Hkv;
+    for (int r0 = split * RPW; r0 < rows; r0 += p.splits * RPW) {
+        const int r = r0 + sub;
+        const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.Hkv;
+        const bool live = r < rows;
+        const int h = is_q ? r : is_k ? r - p.H : r - p.H - p.Hkv;
+        const T* src = static_cast<const T*>(is_q ? p.q : is_k ? p.k : p.v) +
+                       (long long)t * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) +
+                       (long long)h * D;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (live) raw = ld_dep(reinterpret_cast<const uint4*>(src) + c);
+        const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+        float x[E];
+        C::unpack(raw, x);
+        if (p.q_weight != nullptr) {
+            float ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < E; ++k) ss += x[k] * x[k];
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+            const float rs = rsqrtf(ss * (1.f / D) + p.eps);
+            float wv[E];
+            C::unpack(ld_dep(reinterpret_cast<const uint4*>(weight) + c), wv);
+#pragma unroll
+            for (int k = 0; k < E; ++k) x[k] = x[k] * rs * wv[k];
+        }
+        if constexpr (INTERLEAVED) {
+            if (turns) {
+#pragma unroll
+                for (int k = 0; k < NF; ++k) {
+                    const float a = x[2 * k], d = x[2 * k + 1];
+                    x[2 * k] = a * cs[k] - d * sn[k];
+                    x[2 * k + 1] = a * sn[k] + d * cs[k];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float o = __shfl_sync(kFullMask, x[k], partner);
+                if (turns) x[k] = low ? x[k] * cs[k] - o * sn[k] : o * sn[k] + x[k] * cs[k];
+            }
+        }
+        if (!live) continue;
+        if (is_q) {
+            uint4 y = good ? C::pack(x) : make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) +
+                                     ((long long)t * p.H + h) * D)[c] = y;
+        } else if (blk >= 0) {
+            const uint4 y = is_k ? C::pack(x) : raw;
+            T* dst = static_cast<T*>(is_k ? p.k_base : p.v_base) + (long long)blk * p.s_blk +
+                     p.tile_off + (long long)h * p.s_head + (long long)(pos % p.B) * D;
+            reinterpret_cast<uint4*>(dst)[c] = y;
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const NormRopeParams& p, int grid, cudaStream_t s) {
+    return p.interleaved
+               ? launch_pdl(pa_norm_rope_kernel<T, D, true>, dim3(grid), dim3(kRopeThreads), 0, s, p)
+               : launch_pdl(pa_norm_rope_kernel<T, D, false>, dim3(grid), dim3(kRopeThreads), 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope(const NormRopeParams& p_in, int dtype, int D, int num_sms,
+                             cudaStream_t s) {
+    NormRopeParams p = p_in;
+    const int elt = dtype == 1 ? 2 : 4;
+    const int rpw = 32 / (D * elt / 16);
+    const long long groups = (p.H + 2LL * p.Hkv + rpw - 1) / rpw;
+    // warps per token: one, unless that leaves SMs without eight warps
+    long long splits = (8LL * num_sms + p.num_tokens - 1) / p.num_tokens;
+    if (splits > groups) splits = groups;
+    p.splits = (int)splits;
+    const long long warps = splits * p.num_tokens;
+    const long long grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (dtype == 1 && D == 64) return launch_d<__nv_bfloat16, 64>(p, (int)grid, s);
+    if (dtype == 1 && D == 128) return launch_d<__nv_bfloat16, 128>(p, (int)grid, s);
+    if (dtype == 0 && D == 64) return launch_d<float, 64>(p, (int)grid, s);
+    if (dtype == 0 && D == 128) return launch_d<float, 128>(p, (int)grid, s);
+    return cudaErrorNotSupported;
+}
+
+}  // namespace pa

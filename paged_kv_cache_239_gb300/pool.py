@@ -150,6 +150,181 @@ class BlockPool:
                        context_lens, batch, max_len, stream)
         return k, v, mask.bool()
 
+    # -- several new tokens per sequence ------------------------------------
+    def norm_rope_write_kv(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           rope=None, q_weight: Optional[torch.Tensor] = None,
+                           k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                           query_starts: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """RMS norm of query and key heads (with weights), rotation (with a
+        ``Rope``) and append of the new tokens: returns the queries, stores the
+        keys and values.  q, k, v: [tokens, heads, head_dim], any stride between
+        tokens (slices of one packed projection); context_lens include the new
+        tokens; query_starts [batch + 1] says which rows are whose (None: one
+        token per sequence).  ``out`` may be q itself when q is contiguous."""
+        tokens, num_heads = q.shape[0], q.shape[1]
+        self._check_rows(q, tokens, num_heads, "q")
+        self._check_rows(k, tokens, self.num_kv_heads, "k")
+        self._check_rows(v, tokens, self.num_kv_heads, "v")
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                self._check_dense(w, (self.head_dim,), self.dtype, name)
+        batch, maxb = self._check_batch(block_tables, context_lens, query_starts)
+        if out is None:
+            out = self._empty(q.shape, self.dtype, stream)
+        else:
+            self._check_dense(out, (tokens, num_heads, self.head_dim), self.dtype, "out")
+        B.pa_norm_rope_write_kv(self.handle, layer, out, q, q.stride(0) if tokens > 1 else
+                                num_heads * self.head_dim, k, k.stride(0) if tokens > 1 else
+                                self.num_kv_heads * self.head_dim, v, v.stride(0) if tokens > 1
+                                else self.num_kv_heads * self.head_dim,
+                                None if rope is None else rope.handle, q_weight, k_weight, eps,
+                                block_tables, maxb, context_lens, query_starts, batch, tokens,
+                                num_heads, stream)
+        return out
+
+    def prefill_workspace_size(self, batch: int, num_tokens: int, num_heads: int,
+                               max_blocks_per_seq: int) -> int:
+        return B.pa_prefill_workspace_size(self.handle, batch, num_tokens, num_heads,
+                                           max_blocks_per_seq)
+
+    def prefill_attention(self, q: torch.Tensor, layer: int, block_tables: torch.Tensor,
+                          context_lens: torch.Tensor, query_starts: torch.Tensor, scale: float,
+                          out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Causal attention of the new tokens (rows query_starts[b] ..
+        query_starts[b + 1] of q, the last of sequence b's context_lens[b]) over
+        the cache, which holds them already.  q and out: [tokens, num_heads,
+        head_dim], contiguous, the pool's dtype."""
+        tokens, num_heads = q.shape[0], q.shape[1]
+        shape = (tokens, num_heads, self.head_dim)
+        self._check_dense(q, shape, self.dtype, "q")
+        batch, maxb = self._check_batch(block_tables, context_lens, query_starts)
+        if out is None:
+            out = self._empty(shape, self.dtype, stream)
+        else:
+            self._check_dense(out, shape, self.dtype, "out")
+        need = self.prefill_workspace_size(batch, tokens, num_heads, maxb)
+        if need and workspace is None:
+            workspace = self._empty((need,), torch.uint8, stream)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        B.pa_prefill_attention(out, q, self.handle, layer, block_tables, maxb, context_lens,
+                               query_starts, batch, tokens, num_heads, scale, workspace, wbytes,
+                               stream)
+        return out
+
+    # -- pages --------------------------------------------------------------
+    def copy_blocks(self, src_ids: torch.Tensor, dst_ids: torch.Tensor, stream=None) -> None:
+        """Page src_ids[i] to page dst_ids[i] (int32), all layers."""
+        n = src_ids.shape[0]
+        self._check_dense(src_ids, (n,), torch.int32, "src_ids")
+        self._check_dense(dst_ids, (n,), torch.int32, "dst_ids")
+        B.pa_copy_blocks(self.handle, src_ids, dst_ids, n, stream)
+
+    def page_shares(self) -> torch.Tensor:
+        """A new array of page shares (owners beyond the first): nothing shared."""
+        return torch.zeros(self.num_blocks, dtype=torch.int32, device=self.pool.device)
+
+    def device_fork_sequences(self, stack: torch.Tensor, shares: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor,
+                              parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
+        """Rows children[i] continue rows parents[i]: full pages shared, the
+        partial last page copied into one from the device stack."""
+        n = parents.shape[0]
+        batch, maxb = self._check_batch(block_tables, context_lens)
+        self._check_pages(stack, shares)
+        self._check_dense(parents, (n,), torch.int32, "parents")
+        self._check_dense(children, (n,), torch.int32, "children")
+        B.pa_device_fork_sequences(self.handle, stack, shares, block_tables, maxb, context_lens,
+                                   batch, parents, children, n, stream)
+
+    def device_free_shared(self, stack: torch.Tensor, shares: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           finished: torch.Tensor, stream=None) -> None:
+        """device_free_blocks for rows that may share pages."""
+        batch, maxb = self._check_batch(block_tables, context_lens)
+        self._check_pages(stack, shares)
+        self._check_dense(finished, (batch,), (torch.uint8, torch.bool), "finished")
+        B.pa_device_free_shared(self.handle, stack, shares, block_tables, maxb, context_lens,
+                                finished, batch, stream)
+
+    def compact_workspace_size(self) -> int:
+        return B.pa_compact_workspace_size(self.handle)
+
+    def device_compact_blocks(self, stack: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, shares: Optional[torch.Tensor] = None,
+                              out_stack: Optional[torch.Tensor] = None,
+                              out_tables: Optional[torch.Tensor] = None,
+                              out_shares: Optional[torch.Tensor] = None,
+                              remap: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, stream=None):
+        """Moves the pages in use to the lowest ids.  Returns the new (stack,
+        tables, shares, remap); remap[old id] is a page's new id."""
+        batch, maxb = self._check_batch(block_tables, context_lens)
+        self._check_pages(stack, shares)
+        new = lambda like: self._empty(like.shape, torch.int32, stream)  # noqa: E731
+        out_stack = new(stack) if out_stack is None else out_stack
+        out_tables = new(block_tables) if out_tables is None else out_tables
+        if shares is not None and out_shares is None:
+            out_shares = new(shares)
+        remap = self._empty((self.num_blocks,), torch.int32, stream) if remap is None else remap
+        self._check_pages(out_stack, out_shares)
+        self._check_dense(out_tables, tuple(block_tables.shape), torch.int32, "out_tables")
+        self._check_dense(remap, (self.num_blocks,), torch.int32, "remap")
+        if workspace is None:
+            workspace = self._empty((self.compact_workspace_size(),), torch.uint8, stream)
+        B.pa_device_compact_blocks(self.handle, stack, shares, block_tables, maxb, context_lens,
+                                   batch, out_stack, out_shares, out_tables, remap, workspace,
+                                   workspace.numel() * workspace.element_size(), stream)
+        return out_stack, out_tables, out_shares, remap
+
+    # -- checks of what only the tensors know --------------------------------
+    def _empty(self, shape, dtype, stream) -> torch.Tensor:
+        """A tensor that `stream` may write at once (torch reuses memory in the
+        order of the stream it was allocated on)."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.pool.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.pool.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.pool.device)
+
+    def _check_dense(self, t: torch.Tensor, shape, dtype, name: str) -> None:
+        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, "
+                             f"not {tuple(t.shape)}")
+        if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.device != self.pool.device:
+            raise ValueError(f"{name} is on {t.device}, the pool on {self.pool.device}")
+
+    def _check_rows(self, t: torch.Tensor, tokens: int, heads: int, name: str) -> None:
+        d = self.head_dim
+        if tuple(t.shape) != (tokens, heads, d) or t.dtype != self.dtype:
+            raise ValueError(f"{name} must be {self.dtype} [{tokens}, {heads}, {d}], "
+                             f"not {t.dtype} {tuple(t.shape)}")
+        if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if t.device != self.pool.device:
+            raise ValueError(f"{name} is on {t.device}, the pool on {self.pool.device}")
+
+    def _check_batch(self, block_tables, context_lens, query_starts=None):
+        batch = context_lens.shape[0]
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+        self._check_dense(block_tables, (batch, block_tables.shape[1]), torch.int32,
+                          "block_tables")
+        self._check_dense(context_lens, (batch,), torch.int32, "context_lens")
+        if query_starts is not None:
+            self._check_dense(query_starts, (batch + 1,), torch.int32, "query_starts")
+        return batch, block_tables.shape[1]
+
+    def _check_pages(self, stack, shares) -> None:
+        self._check_dense(stack, (self.num_blocks + 1,), torch.int32, "stack")
+        if shares is not None:
+            self._check_dense(shares, (self.num_blocks,), torch.int32, "shares")
+
     def close(self) -> None:
         if getattr(self, "handle", None):
             B.pa_pool_destroy(self.handle)
