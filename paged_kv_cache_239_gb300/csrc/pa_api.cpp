@@ -672,6 +672,17 @@ int pa_decode_workspace_size(const pa_pool* pool, int batch, int num_heads,
 
 namespace {
 
+// Encodes the pool's tensor maps on first use.
+int pool_tmaps(const pa_pool* pool) {
+    std::lock_guard<std::mutex> lock(pool->mu);
+    if (pool->tmaps_ready) return PA_OK;
+    const cudaError_t e = pa::encode_pool_tmaps(pool->g, pool->tmaps, &pool->tma_slots[0],
+                                                &pool->tma_slots[1], &pool->tma_slots[2]);
+    if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
+    pool->tmaps_ready = true;
+    return PA_OK;
+}
+
 // Decode attention; with new_k/new_v/positions non-null the append of one
 // token per sequence is fused into the decode kernel.
 int decode_impl(float* out, const void* q, const pa_pool* pool, int layer,
@@ -762,15 +773,7 @@ int decode_impl(float* out, const void* q, const pa_pool* pool, int layer,
         sh.wide = wide_fits(pool, sh.G, batch, max_blocks_per_seq, sms);
     }
     if (sh.kernel != Kernel::CudaCores) {
-        {
-            std::lock_guard<std::mutex> lock(pool->mu);
-            if (!pool->tmaps_ready) {
-                e = pa::encode_pool_tmaps(g, pool->tmaps, &pool->tma_slots[0],
-                                          &pool->tma_slots[1], &pool->tma_slots[2]);
-                if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
-                pool->tmaps_ready = true;
-            }
-        }
+        if (int rc = pool_tmaps(pool)) return rc;
         p.tma_slot_blk = pool->tma_slots[0];
         p.tma_slot_layer = pool->tma_slots[1];
         p.tma_slot_head = pool->tma_slots[2];
@@ -912,9 +915,14 @@ int check_stack(const void* dev_stack) {
     return PA_OK;
 }
 
-// What both prefill calls need of the sizes.
+// What both prefill calls need of the sizes: how the work is split, and where
+// the workspace holds what.
+struct PrefillShape {
+    int splits = 1, grid = 0;
+    size_t ml_off = 0, cut_off = 0, ws_bytes = 0;
+};
 int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads, int maxb,
-                  int* splits, size_t* ws_bytes) {
+                  PrefillShape* sh) {
     const pa::PoolGeom& g = pool->g;
     if (batch < 0 || num_tokens < 0)
         return fail(PA_ERR_INVALID_ARG, "batch (%d) and num_tokens (%d) must be >= 0", batch,
@@ -932,13 +940,23 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
                     "no prefill kernel for dtype=%d head_dim=%d block_size=%d (built: head_dim "
                     "64/128, block_size 16/32)",
                     g.dtype, g.D, g.B);
-    *splits = 1, *ws_bytes = 0;
+    *sh = PrefillShape();
     if (batch == 0 || num_tokens == 0) return PA_OK;
     int sms = 0;
     if (int rc = num_sms_current(&sms)) return rc;
-    *splits = pa::prefill_splits(g.dtype, g.D, num_heads / g.Hkv, g.Hkv, batch, num_tokens, maxb,
-                                 g.B, sms);
-    *ws_bytes = pa::prefill_workspace_bytes(g.dtype, g.D, num_heads, num_tokens, *splits);
+    const int G = num_heads / g.Hkv;
+    size_t rows = 0;  // rows of partials
+    if (g.dtype == 1) {
+        sh->grid = pa::prefill_umma_grid(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
+        if (sh->grid > 1) rows = (size_t)sh->grid * 2 * 256;
+    } else {
+        sh->splits = pa::prefill_simt_splits(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
+        if (sh->splits > 1) rows = (size_t)sh->splits * num_tokens * num_heads;
+    }
+    if (rows == 0) return PA_OK;
+    sh->ml_off = align256(rows * g.D * sizeof(float));
+    sh->cut_off = sh->ml_off + align256(rows * 2 * sizeof(float));
+    sh->ws_bytes = sh->cut_off + (size_t)sh->grid * 2 * sizeof(int4);
     return PA_OK;
 }
 
@@ -1093,8 +1111,11 @@ int pa_prefill_workspace_size(const pa_pool* pool, int batch, int num_tokens, in
                               int max_blocks_per_seq, size_t* bytes) {
     if (int rc = check_pool(pool)) return rc;
     if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes is NULL");
-    int splits = 1;
-    return prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &splits, bytes);
+    PrefillShape sh;
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
+        return rc;
+    *bytes = sh.ws_bytes;
+    return PA_OK;
 }
 
 int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int layer,
@@ -1107,10 +1128,8 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
     const pa::PoolGeom& g = pool->g;
     if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
     if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
-    int splits = 1;
-    size_t need = 0;
-    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &splits,
-                               &need))
+    PrefillShape sh;
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
         return rc;
     if (batch == 0 || num_tokens == 0) return PA_OK;
     if (!out || !q || !aligned(out, 16) || !aligned(q, 16))
@@ -1119,10 +1138,11 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
         return fail(PA_ERR_INVALID_ARG, "query_starts must be non-NULL and 4-byte aligned");
     const size_t bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
     if (overlap(out, bytes, q, bytes)) return fail(PA_ERR_INVALID_ARG, "out overlaps q");
-    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    if (sh.ws_bytes &&
+        (!workspace || workspace_bytes < sh.ws_bytes || !aligned(workspace, 256)))
         return fail(PA_ERR_WORKSPACE,
-                    "workspace must be 256-byte aligned and hold %zu bytes (got %p, %zu)", need,
-                    workspace, workspace_bytes);
+                    "workspace must be 256-byte aligned and hold %zu bytes (got %p, %zu)",
+                    sh.ws_bytes, workspace, workspace_bytes);
     pa::PrefillParams p{};
     cudaError_t e = pa::status_word(&p.status);
     if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
@@ -1136,12 +1156,23 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
     p.lens = context_lens, p.starts = query_starts;
     p.batch = batch, p.num_tokens = num_tokens;
     p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax evaluated with exp2
-    p.splits = splits;
-    if (need) {
-        p.part_o = static_cast<float*>(workspace);
-        p.part_ml = p.part_o + (size_t)splits * num_tokens * num_heads * g.D;
+    p.splits = sh.splits;
+    p.grid = sh.grid;
+    if (sh.ws_bytes) {
+        char* ws = static_cast<char*>(workspace);
+        p.part_o = reinterpret_cast<float*>(ws);
+        p.part_ml = reinterpret_cast<float*>(ws + sh.ml_off);
+        if (sh.grid) p.cut = reinterpret_cast<int4*>(ws + sh.cut_off);
     }
-    e = pa::launch_prefill(p, g.dtype, g.D, g.B, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (g.dtype == 1) {
+        if (int rc = pool_tmaps(pool)) return rc;
+        p.slot_blk = pool->tma_slots[0];
+        p.slot_layer = pool->tma_slots[1];
+        e = pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
+    } else {
+        e = pa::launch_prefill_simt(p, g.D, g.B, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
     return PA_OK;
 }

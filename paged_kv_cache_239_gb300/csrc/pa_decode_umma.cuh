@@ -63,149 +63,9 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_schedule.cuh"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
-
-// ---------------------------------------------------------------- tcgen05 --
-
-// Shared-memory matrix descriptor: start address, leading / stride byte
-// offsets (all >> 4), the fixed version field (bits 46-48 = 0b001) and the
-// 128-byte swizzle (layout type 2 in bits 61-63).  K-major operands: SBO is the
-// distance between 8-row groups, LBO unused.  MN-major operands: LBO is the
-// distance between 64-element column blocks, SBO between 8-row (K) groups.
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
-// Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B,
-// operand majors (0 = K-major, 1 = MN-major), N >> 3 and M >> 4.
-__host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N, int a_mn, int b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// D (TMEM) = A . B (+ D if accumulate), issued by one thread.
-__device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// D (TMEM) = A . B (+ D), A read from tensor memory (M rows on the lanes, two
-// 16-bit K elements per 32-bit column, the first in the low half), B from
-// shared memory.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                             uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// The mbarrier receives one arrival once every tcgen05 operation this thread
-// issued before has completed.
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_alloc(uint32_t slot_addr, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     slot_addr),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// 16 consecutive 32-bit TMEM columns of this thread's lane (32x32b shape: lane
-// 32 * (warp % 4) + laneid of the warp's quarter).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-            taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-        : "memory");
-}
-
-// N (8 or a multiple of 16) consecutive columns of this thread's lane.
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-    if constexpr (N == 8) {
-        tmem_ld8(taddr, r);
-    } else {
-#pragma unroll
-        for (int c = 0; c < N; c += 16)
-            tmem_ld16(taddr + c, *reinterpret_cast<uint32_t(*)[16]>(r + c));
-    }
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t* r) {
-    if constexpr (N == 8) {
-        tmem_st8(taddr, r);
-    } else {
-#pragma unroll
-        for (int c = 0; c < N; c += 16)
-            tmem_st16(taddr + c, *reinterpret_cast<const uint32_t(*)[16]>(r + c));
-    }
-}
-
-__device__ __forceinline__ void tmem_wait_ld() {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
 
 // Named barriers over the 128 softmax threads of one head part (four warps,
 // one per TMEM lane quarter): id 1 + 2 * part plain, 2 + 2 * part with an OR
@@ -350,55 +210,6 @@ __device__ __forceinline__ bool umma_walk_next(const DecodeParams& p, UWalk& w, 
     return sched_walk_next<B, 128, kUmmaPieceUnits<G>, G>(p, w, it);
 }
 
-// Non-blocking test of an mbarrier phase (try_wait may suspend the thread for
-// a while; a thread that polls several barriers must not be parked on one).
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Waits for an mbarrier phase, suspending the thread (no issue slots used)
-// until the phase completes or about `ns` nanoseconds have passed.
-__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
-}
-
-// Bounded wait that also gives up when another role has aborted.
-__device__ __forceinline__ bool umma_wait(uint32_t bar, uint32_t parity, volatile int* abort_all,
-                                          unsigned* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    for (uint32_t it = 0; it < (1u << 30); ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_all) return false;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
-    }
-    *abort_all = 1;
-    atomicOr(status, kStatusTimeout);
-    return false;
-}
-
-// Byte offset of 16-byte chunk j of row r in a 1024-byte-aligned stack of
-// 128-byte rows with the 128-byte swizzle.
-__device__ __forceinline__ uint32_t sw128(int r, int j) {
-    return (uint32_t)(r * 128 + (((j & 7) ^ (r & 7)) << 4));
-}
-
 // Max (or sum) of v[j] over the warp's 32 lanes for each of N = 2^k values,
 // as a reduce-scatter butterfly: at each step a lane sends the half of its
 // values it does not keep, so N + N/2 + ... shuffles become N - 1 + 5 - log2 N
@@ -429,11 +240,6 @@ __device__ __forceinline__ float warp_scatter_reduce(const float (&in)[N], int l
         r = MAX ? fmaxf(r, got) : r + got;
     }
     return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <int B, int G>

@@ -126,7 +126,8 @@ struct NormRopeParams {
     unsigned long long freq[kMaxRotaryPairs];  // turns per position, as fractions of 2^64
 };
 
-// Attention of several new tokens per sequence (see pa_prefill_f32.cuh).
+// Attention of several new tokens per sequence (see pa_prefill_umma.cuh for
+// bf16 pools, pa_prefill_simt.cu for fp32).
 struct PrefillParams {
     void* out;               // [num_tokens, H, D], pool dtype
     const void* q;           // [num_tokens, H, D], pool dtype
@@ -140,9 +141,12 @@ struct PrefillParams {
     const int* starts;       // [batch + 1]
     int batch, num_tokens;
     float qscale;            // softmax scale * log2(e)
-    int splits;
     float *part_o, *part_ml;
     unsigned* status;
+    int splits;              // fp32: parts of each context
+    int grid;                // bf16: persistent CTAs, and per CTA two int4: the
+    int4* cut;               // pair whose first part it holds while others go on
+    int slot_blk, slot_layer;  // tensor-map dimensions of the pool's axes
 };
 
 // The pages of a pool (see pa_pages.cu).
@@ -179,12 +183,13 @@ struct CompactParams {
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, int D, int num_sms,
                              cudaStream_t s);
 bool prefill_supported(int dtype, int D, int B);
-// Rows (token, head of a group) per tile, and the splits of the contexts that
-// a call's size asks for.
-int prefill_splits(int dtype, int D, int G, int Hkv, int batch, int num_tokens, int maxb, int B,
-                   int num_sms);
-size_t prefill_workspace_bytes(int dtype, int D, int H, int num_tokens, int splits);
-cudaError_t launch_prefill(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s);
+// fp32: the splits of the contexts that a call's size asks for.
+int prefill_simt_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms);
+cudaError_t launch_prefill_simt(const PrefillParams& p, int D, int B, cudaStream_t s);
+// bf16: the persistent grid; `tmaps` points to the pool's two CUtensorMap.
+int prefill_umma_grid(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms);
+cudaError_t launch_prefill_umma(const PrefillParams& p, const void* tmaps, int D, int B,
+                                cudaStream_t s);
 
 cudaError_t launch_copy_blocks(const PageGeom& g, const int* src, const int* dst, int n,
                                int num_sms, cudaStream_t s);

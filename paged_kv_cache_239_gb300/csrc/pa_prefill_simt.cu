@@ -1,5 +1,5 @@
 // pa_prefill_simt.cu -- attention of several new tokens per sequence over the
-// paged cache, on the CUDA cores.
+// fp32 paged cache, on the CUDA cores.
 //
 //   out_t = sum_{s <= p_t} softmax_s(scale q_t . k_s) v_s,
 //   p_t = context_lens[b] - n_b + i for the i-th of sequence b's n_b new tokens.
@@ -10,12 +10,9 @@
 // the tile's q in shared memory and streams 64 keys and values at a time; each
 // thread accumulates 4 x 4 scores and 4 rows x D / 16 outputs in registers,
 // with the running maximum and sum of each row (one pass over the keys).
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-
-#include <mutex>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -36,19 +33,9 @@ struct SimtCfg {
 __device__ __forceinline__ float4 load4(const float* p) {
     return ld_dep(reinterpret_cast<const float4*>(p));
 }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 w = ld_dep(reinterpret_cast<const uint2*>(p));
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&b));
-}
 
-template <typename T, int D, int B>
+template <int D, int B>
 __global__ void __launch_bounds__(kThreads) pa_prefill_simt_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
@@ -113,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) pa_prefill_simt_kernel(const Prefill
     const int per = (key_tiles + p.splits - 1) / p.splits;
     const int kt0 = min((int)blockIdx.z * per, key_tiles), kt1 = min(kt0 + per, key_tiles);
 
-    const T* q = static_cast<const T*>(p.q);
+    const float* q = static_cast<const float*>(p.q);
     for (int x = tid; x < BM * (D / 4); x += kThreads) {
         const int r = x / (D / 4), c = (x % (D / 4)) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -135,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) pa_prefill_simt_kernel(const Prefill
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
     }
-    const T* kb = static_cast<const T*>(p.k_base) + p.tile_off + (long long)kvh * p.s_head;
-    const T* vb = static_cast<const T*>(p.v_base) + p.tile_off + (long long)kvh * p.s_head;
+    const float* kb = static_cast<const float*>(p.k_base) + p.tile_off + (long long)kvh * p.s_head;
+    const float* vb = static_cast<const float*>(p.v_base) + p.tile_off + (long long)kvh * p.s_head;
 
     for (int kt = kt0; kt < kt1; ++kt) {
         const int t0 = kt * BN;
@@ -264,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) pa_prefill_simt_kernel(const Prefill
             const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
-                store4(static_cast<T*>(p.out) + orow * D + 4 * tx + 64 * j,
+                store4(static_cast<float*>(p.out) + orow * D + 4 * tx + 64 * j,
                        make_float4(o[i][4 * j] * inv, o[i][4 * j + 1] * inv, o[i][4 * j + 2] * inv,
                                    o[i][4 * j + 3] * inv));
         } else {
@@ -279,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) pa_prefill_simt_kernel(const Prefill
 }
 
 // Joins the splits of every row before the last sequence's end: a warp a row.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) pa_prefill_join_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
@@ -300,14 +287,14 @@ __global__ void __launch_bounds__(kThreads) pa_prefill_join_kernel(const Prefill
             o[j] = fmaf(w, ld_dep(p.part_o + (z * all + row) * D + lane * (D / 32) + j), o[j]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* out = static_cast<T*>(p.out) + row * D + lane * (D / 32);
+    float* out = static_cast<float*>(p.out) + row * D + lane * (D / 32);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) out[j] = static_cast<T>(o[j] * inv);
+    for (int j = 0; j < D / 32; ++j) out[j] = o[j] * inv;
 }
 
-template <typename T, int D, int B>
+template <int D, int B>
 cudaError_t launch_simt(const PrefillParams& p, cudaStream_t s) {
-    auto kern = pa_prefill_simt_kernel<T, D, B>;
+    auto kern = pa_prefill_simt_kernel<D, B>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          SimtCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
@@ -317,17 +304,8 @@ cudaError_t launch_simt(const PrefillParams& p, cudaStream_t s) {
                    s, p);
     if (e != cudaSuccess || p.splits == 1) return e;
     const long long rows = (long long)p.num_tokens * p.H;
-    return launch_pdl(pa_prefill_join_kernel<T, D>, dim3((unsigned)((rows + 7) / 8)), dim3(kThreads),
+    return launch_pdl(pa_prefill_join_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(kThreads),
                       0, s, p);
-}
-
-template <typename T>
-cudaError_t launch_t(const PrefillParams& p, int D, int B, cudaStream_t s) {
-    if (D == 64 && B == 16) return launch_simt<T, 64, 16>(p, s);
-    if (D == 64 && B == 32) return launch_simt<T, 64, 32>(p, s);
-    if (D == 128 && B == 16) return launch_simt<T, 128, 16>(p, s);
-    if (D == 128 && B == 32) return launch_simt<T, 128, 32>(p, s);
-    return cudaErrorNotSupported;
 }
 
 }  // namespace
@@ -336,8 +314,7 @@ bool prefill_supported(int dtype, int D, int B) {
     return (dtype == 0 || dtype == 1) && (D == 64 || D == 128) && (B == 16 || B == 32);
 }
 
-int prefill_splits(int, int, int G, int Hkv, int batch, int num_tokens, int maxb, int B,
-                   int num_sms) {
+int prefill_simt_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms) {
     const long long tiles = ((long long)num_tokens * G / BM + batch) * Hkv;
     const long long want = 2LL * num_sms / (tiles > 0 ? tiles : 1);
     const long long most = ((long long)maxb * B + 255) / 256;  // four key tiles at least
@@ -345,12 +322,12 @@ int prefill_splits(int, int, int G, int Hkv, int batch, int num_tokens, int maxb
     return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 
-size_t prefill_workspace_bytes(int, int D, int H, int num_tokens, int splits) {
-    return splits > 1 ? (size_t)splits * num_tokens * H * (D + 2) * sizeof(float) : 0;
-}
-
-cudaError_t launch_prefill(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s) {
-    return dtype == 1 ? launch_t<__nv_bfloat16>(p, D, B, s) : launch_t<float>(p, D, B, s);
+cudaError_t launch_prefill_simt(const PrefillParams& p, int D, int B, cudaStream_t s) {
+    if (D == 64 && B == 16) return launch_simt<64, 16>(p, s);
+    if (D == 64 && B == 32) return launch_simt<64, 32>(p, s);
+    if (D == 128 && B == 16) return launch_simt<128, 16>(p, s);
+    if (D == 128 && B == 32) return launch_simt<128, 32>(p, s);
+    return cudaErrorNotSupported;
 }
 
 }  // namespace pa

@@ -1,0 +1,856 @@
+// pa_prefill_umma.cuh -- attention of several new tokens per sequence over a
+// bf16 paged cache on the 5th-generation tensor cores.
+//
+//   out_t = sum_{s <= p_t} softmax_s(scale q_t . k_s) v_s,
+//   p_t = context_lens[b] - n_b + i for the i-th of sequence b's n_b new tokens.
+//
+// The query heads of a KV head's group share its keys, so the rows of a tile
+// are (token, head of the group) in that order, flattened: row r is token r / G,
+// head r % G, whatever G is.  A pair is 256 consecutive rows of one (sequence,
+// KV head): two row tiles of 128, the M of tcgen05.mma, that run against the
+// same stream of 128-key tiles.
+//
+// Schedule: the work is all pairs' key tiles in order of sequence, KV head and
+// rows (a pair is charged kPairUnits more for its fixed cost), and each of the
+// persistent CTAs, one per SM, takes an equal contiguous share of it.  Prompts
+// of any mix of lengths and a few rows over a long context alike fill the GPU;
+// a pair that the shares cut leaves unnormalised partials that the join kernel
+// merges.
+//
+// Roles, connected by mbarriers:
+//  * warp 0: K and V tiles into one ring of stages, K(0) V(0) K(1) V(1) ..., by
+//    5-D tensor-map TMA, a 16-row box per lane, pages from the block table;
+//  * warp 1: tensor memory, and one thread issuing for each key tile i and row
+//    tile j  O_j += P_j(i) V(i), then S_j(i + 1) = Q_j K(i + 1)^T: the softmax of
+//    one row tile runs under the products of the other;
+//  * warps 2, 3: Q of the next pair, gathered by rows (cp.async) into the
+//    swizzled layout;
+//  * warps 4-7 and 8-11: softmax of row tile 0 and 1, one row per thread, so no
+//    exchange between threads: S from tensor memory, running maximum (raised,
+//    and O rescaled, only when a score exceeds it by more than 2^8: any
+//    reference point gives the same normalised result), P as bf16 over S's own
+//    columns, sums in fp32, and at the end of a piece O / l to the output.
+// P in bf16: its rounding (2^-9 relative on average over many keys) is of the
+// size of the output's own; the sum l takes the weights before that rounding.
+//
+// What a row does not see must not reach it even through 0 * NaN: in tiles that
+// reach past the pair's first row, the context's end or a bad page, the rows of
+// V outside the context are zeroed in shared memory, and values that are not
+// finite are zeroed and remembered by column and position, to be put back into
+// the rows that see them at the output.
+#pragma once
+
+#include <cfloat>
+#include <climits>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+
+template <int D_, int B_>
+struct PrefillCfg {
+    static constexpr int D = D_, B = B_;
+    static constexpr int TT = 128;                 // keys per tile
+    static constexpr int ROWS = 256;               // rows per pair (two tiles of 128)
+    static constexpr int NH = D / 64;              // 64-column halves
+    static constexpr int HALF = 128 * 128;         // one half of a 128-row tile (bytes)
+    static constexpr int TILE = NH * HALF;
+    static constexpr int NS = D == 128 ? 5 : 10;   // K/V stages
+    static constexpr int OFF_Q = NS * TILE;
+    static constexpr int OFF_CTRL = OFF_Q + 2 * TILE;
+    // ctrl (bytes): barriers | TMEM address, abort, mark_piece, wg1_done |
+    // box bits per stage | schedule | scan scratch | marks [3][D]
+    static constexpr int TMEM_SLOT = 256, ABORT = 260, MARK_PIECE = 264, WG1_DONE = 268,
+                         BITS = 272, SCHED = 320, SCAN = 384, MARKS = 512;
+    static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 3 * 128 * 4 + 1024;
+    static constexpr int THREADS = 384;
+    // TMEM: S_0, S_1 (P in their first 64 columns), O_0, O_1
+    static constexpr int O_COL = 256;
+    static constexpr int TMEM_COLS = 512;
+    // barriers
+    static constexpr int KV_FULL = 0, KV_EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
+                         S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
+                         FINAL = Q_FULL + 10, NBAR = Q_FULL + 11;
+    static_assert(NBAR * 8 <= TMEM_SLOT && NS <= 12, "ctrl layout");
+    static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+constexpr int kPairUnits = 2;
+
+// A sequence as the schedule sees it.
+struct PfSeq {
+    int start, n_new, n, first_pos, rows, tiles;
+};
+
+template <int B>
+__device__ __forceinline__ PfSeq pf_sequence(const PrefillParams& p, int b, bool* bad) {
+    PfSeq s{0, 0, 0, 0, 0, 0};
+    *bad = false;
+    if (b >= p.batch) return s;
+    const int s0 = ld_dep(p.starts + b), s1 = ld_dep(p.starts + b + 1);
+    const int n = ld_dep(p.lens + b);
+    if (s0 < 0 || s1 < s0 || s1 > p.num_tokens) {
+        *bad = true;
+        return s;
+    }
+    s.start = s0, s.n_new = s1 - s0, s.n = n;
+    if (n < s.n_new || n > p.maxb * B || n < 0) {
+        *bad = true;
+        s.n = 0;  // no key is seen: zero rows
+    }
+    s.first_pos = s.n - s.n_new;
+    s.rows = s.n_new * p.G;
+    s.tiles = (s.rows + 255) / 256;
+    return s;
+}
+
+// Key tiles of pair i of a sequence (at least one: the pair owes its output).
+__device__ __forceinline__ int pf_key_tiles(const PfSeq& s, int i, int G) {
+    const int last = min(s.rows, 256 * (i + 1)) - 1;
+    const int see = s.first_pos + last / G + 1;
+    return see > 128 ? (see + 127) >> 7 : 1;
+}
+
+// A piece: key tiles [kt0, kt1) of one pair.
+struct PfPiece {
+    int b, kvh, i, kt0, kt1, kvt;
+    PfSeq s;
+    long long gpos;   // global unit of the pair's first key tile
+    bool whole, first;
+    int nj, row0;     // row tiles (1 or 2), first row of the pair
+};
+
+struct PfWalk {
+    int b, kvh, i, count;
+    long long left, off, gpos;
+    PfSeq s;
+};
+
+// Units of sequence b0 + lane (all lanes of the warp take part).
+template <int B>
+__device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b, int lane,
+                                                  bool report) {
+    bool bad;
+    const PfSeq s = pf_sequence<B>(p, b, &bad);
+    if (bad && report) atomicOr(p.status, kStatusBadLength);
+    long long u = 0;
+    if (s.tiles <= 8)
+        for (int i = 0; i < s.tiles; ++i) u += kPairUnits + pf_key_tiles(s, i, p.G);
+    unsigned big = __ballot_sync(kFullMask, s.tiles > 8);
+    while (big) {
+        const int f = __ffs(big) - 1;
+        big &= big - 1;
+        PfSeq o;
+        o.first_pos = __shfl_sync(kFullMask, s.first_pos, f);
+        o.rows = __shfl_sync(kFullMask, s.rows, f);
+        o.tiles = __shfl_sync(kFullMask, s.tiles, f);
+        long long v = 0;
+        for (int i = lane; i < o.tiles; i += 32) v += kPairUnits + pf_key_tiles(o, i, p.G);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(kFullMask, v, x);
+        if (lane == f) u = v;
+    }
+    return u;
+}
+
+// The CTA's range of the T units, into `sched`: [0] T, [8] first unit, [16]
+// units, [24] offset within the pair, [32] b, [36] KV head, [40] pair.
+template <typename C>
+__device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned char* ctrl) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int NW = C::THREADS / 32;
+    long long* sums = reinterpret_cast<long long*>(ctrl + C::SCAN);
+    long long* out = reinterpret_cast<long long*>(ctrl + C::SCHED);
+    int* outi = reinterpret_cast<int*>(ctrl + C::SCHED + 32);
+    long long u = 0, mine = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += C::THREADS) {
+        u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, blockIdx.x == 0);
+        mine += u;
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mine += __shfl_xor_sync(kFullMask, mine, x);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    long long T = 0;
+    for (int w = 0; w < NW; ++w) T += sums[w];
+    T *= p.Hkv;
+    // (no more shares than units: an empty one inside a cut pair would be taken
+    // for a part of it)
+    const long long grid = min((long long)gridDim.x, T);
+    const long long j = blockIdx.x;
+    long long lo = 0, hi = 0;
+    if (j < grid) {
+        lo = (j * T + grid - 1) / grid;
+        hi = ((j + 1) * T + grid - 1) / grid;
+    }
+    long long before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += C::THREADS) {
+        if (p.batch > C::THREADS) u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, false);
+        long long incl = u * p.Hkv;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const long long v = __shfl_up_sync(kFullMask, incl, x);
+            if (lane >= x) incl += v;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        long long base = before;
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) base += sums[w];
+            before += sums[w];
+        }
+        const long long at = base + incl - u * p.Hkv;
+        if (lo >= at && lo < at + u * p.Hkv && hi > lo) {
+            outi[0] = b0 + threadIdx.x;
+            outi[1] = (int)((lo - at) / u);
+            out[3] = (lo - at) % u;
+        }
+    }
+    __syncthreads();
+    if (warp == 0 && hi > lo) {
+        // the pair within the sequence and KV head
+        bool bad;
+        const PfSeq s = pf_sequence<C::B>(p, outi[0], &bad);
+        long long off = out[3];
+        int i = 0;
+        for (int i0 = 0; i0 < s.tiles; i0 += 32) {
+            const int c = i0 + lane < s.tiles ? kPairUnits + pf_key_tiles(s, i0 + lane, p.G) : 0;
+            long long incl = c;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const long long v = __shfl_up_sync(kFullMask, incl, x);
+                if (lane >= x) incl += v;
+            }
+            const unsigned hit = __ballot_sync(kFullMask, off >= incl - c && off < incl);
+            if (hit) {
+                const int f = __ffs(hit) - 1;
+                i = i0 + f;
+                off -= __shfl_sync(kFullMask, incl, f) - __shfl_sync(kFullMask, c, f);
+                break;
+            }
+            off -= __shfl_sync(kFullMask, incl, 31);
+        }
+        __syncwarp();
+        if (lane == 0) out[3] = off, outi[2] = i;
+    }
+    if (threadIdx.x == 0) out[0] = T, out[1] = lo, out[2] = hi - lo;
+}
+
+template <typename C>
+__device__ __forceinline__ void pf_walk_begin(const PrefillParams& p, const unsigned char* ctrl,
+                                              PfWalk& w) {
+    const long long* in = reinterpret_cast<const long long*>(ctrl + C::SCHED);
+    const int* ini = reinterpret_cast<const int*>(ctrl + C::SCHED + 32);
+    w.left = in[2], w.count = 0;
+    if (w.left <= 0) return;
+    w.off = in[3], w.gpos = in[1] - in[3];
+    w.b = ini[0], w.kvh = ini[1], w.i = ini[2];
+    bool bad;
+    w.s = pf_sequence<C::B>(p, w.b, &bad);
+}
+
+template <typename C>
+__device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, PfPiece& pc) {
+    while (w.left > 0) {
+        const int kvt = pf_key_tiles(w.s, w.i, p.G);
+        const long long c = kPairUnits + kvt;
+        const long long take = min(c - w.off, w.left);
+        const int u0 = (int)max(w.off - kPairUnits, 0LL), u1 = (int)(w.off + take - kPairUnits);
+        pc.b = w.b, pc.kvh = w.kvh, pc.i = w.i, pc.kt0 = u0, pc.kt1 = u1, pc.kvt = kvt;
+        pc.s = w.s, pc.gpos = w.gpos + kPairUnits, pc.whole = u0 == 0 && u1 == kvt;
+        pc.first = w.count == 0;
+        pc.row0 = 256 * w.i;
+        pc.nj = w.s.rows - pc.row0 > 128 ? 2 : 1;
+        w.left -= take;
+        if (w.off + take == c) {  // on to the next pair
+            w.off = 0, w.gpos += c;
+            if (++w.i == w.s.tiles) {
+                w.i = 0;
+                if (++w.kvh == p.Hkv) {
+                    w.kvh = 0;
+                    while (w.left > 0 && ++w.b < p.batch) {
+                        bool bad;
+                        w.s = pf_sequence<C::B>(p, w.b, &bad);
+                        if (w.s.tiles > 0) break;
+                    }
+                    if (w.b >= p.batch) w.left = 0;
+                }
+            }
+        } else {
+            w.off += take;
+        }
+        if (u1 > u0) {
+            ++w.count;
+            return true;
+        }
+    }
+    return false;
+}
+
+// 32 consecutive columns of this thread's lane; the values may be used after
+// tmem_loaded32 (which names them, so that no use is moved ahead of the wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]),
+          "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]),
+          "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_loaded32(float (&r)[32]) {
+    asm volatile(""
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                   "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                   "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]),
+                   "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                   "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                   "+f"(r[30]), "+f"(r[31]));
+}
+
+// Packed pairs of fp32 (one instruction each).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// cp.async of one 16-byte chunk (zeros when !valid).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Barrier over the 128 threads of softmax group 0 with an OR of `v`.
+__device__ __forceinline__ bool wg0_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+// True where either bf16 of the word is infinite or NaN.
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// What a column's remembered values (first positions of a NaN, +inf, -inf) add
+// to the output of a row at `pos`.
+__device__ __forceinline__ float poison(const int* marks, int D, int d, int pos) {
+    const bool n = marks[d] <= pos, a = marks[D + d] <= pos, b = marks[2 * D + d] <= pos;
+    return n || (a && b) ? NAN : a ? INFINITY : b ? -INFINITY : 0.f;
+}
+
+template <int D, int B>
+__global__ void __launch_bounds__(384, 1)
+    pa_prefill_umma_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                           const __grid_constant__ CUtensorMap tmv) {
+    pdl_trigger();
+    using C = PrefillCfg<D, B>;
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
+    unsigned char* smem = smem_raw + (sbase - raw_addr);
+    unsigned char* ctrl = smem + C::OFF_CTRL;
+    const uint32_t bar0 = sbase + C::OFF_CTRL;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + C::TMEM_SLOT);
+    volatile int* abort_all = reinterpret_cast<volatile int*>(ctrl + C::ABORT);
+    volatile int* mark_piece = reinterpret_cast<volatile int*>(ctrl + C::MARK_PIECE);
+    volatile int* wg1_done = reinterpret_cast<volatile int*>(ctrl + C::WG1_DONE);
+    volatile int* box_bits = reinterpret_cast<volatile int*>(ctrl + C::BITS);
+    int* marks = reinterpret_cast<int*>(ctrl + C::MARKS);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NBAR; ++i) {
+            const bool p_full = i == C::P_FULL || i == C::P_FULL + 1;
+            const bool q_full = i == C::Q_FULL || i == C::Q_FULL + 1;
+            mbar_init(bar0 + 8 * i, p_full ? 4 : q_full ? 2 : 1);
+        }
+        *abort_all = 0, *mark_piece = -1, *wg1_done = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
+    pdl_wait();
+    pf_schedule<C>(p, ctrl);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](int bar, uint32_t parity) {
+        return umma_wait(bar0 + 8 * bar, parity, abort_all, p.status);
+    };
+    PfWalk w;
+    pf_walk_begin<C>(p, ctrl, w);
+    PfPiece pc;
+
+    if (warp < 4) {
+        regs_dec<104>();
+        if (warp == 0) {
+            // ===================================================== K and V tiles
+            int seq = 0;  // stages filled so far
+            bool aborted = false;
+            const uint64_t pol = l2_policy_evict_normal();
+            if (lane == 0 && p.cut != nullptr)
+                p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);  // (no cut pair yet)
+            while (!aborted && pf_walk_next<C>(p, w, pc)) {
+                if (lane == 0 && p.cut != nullptr && !pc.whole && pc.kt0 == 0) {
+                    // this CTA holds the first part of a pair that others go on with
+                    const long long T = *reinterpret_cast<const long long*>(ctrl + C::SCHED);
+                    const long long last = (pc.gpos + pc.kvt - 1) * min((long long)gridDim.x, T) / T;
+                    p.cut[2 * blockIdx.x] = make_int4(pc.b, pc.kvh, pc.i, pc.s.start);
+                    p.cut[2 * blockIdx.x + 1] =
+                        make_int4((int)(last - blockIdx.x) + 1, pc.first ? 0 : 1, pc.s.rows, 0);
+                }
+                auto box_block = [&](int kt) {
+                    const int tok = kt * C::TT + 16 * lane;
+                    return (kt < pc.kt1 && lane < 8 && tok < pc.s.n)
+                               ? ld_dep(p.bt + (long long)pc.b * p.maxb + tok / B)
+                               : -1;
+                };
+                int blk_next = box_block(pc.kt0);
+                for (int kt = pc.kt0; kt < pc.kt1 && !aborted; ++kt) {
+                    const int tok = kt * C::TT + 16 * lane;
+                    const int blk = blk_next;
+                    blk_next = box_block(kt + 1);
+                    const bool inside = lane < 8 && tok < pc.s.n;
+                    const bool valid = inside && blk >= 0 && blk < p.num_blocks;
+                    const unsigned vmask = __ballot_sync(kFullMask, valid);
+                    if (inside && !valid) atomicOr(p.status, kStatusBadBlock);
+                    for (int kv = 0; kv < 2; ++kv, ++seq) {
+                        const int stage = seq % C::NS;
+                        if (seq >= C::NS &&
+                            !__all_sync(kFullMask, wait(C::KV_EMPTY + stage, (seq / C::NS - 1) & 1))) {
+                            aborted = true;
+                            break;
+                        }
+                        const uint32_t fb = bar0 + 8 * (C::KV_FULL + stage);
+                        if (lane == 0) {
+                            box_bits[stage] = (int)vmask;
+                            mbar_arrive_expect_tx(fb, (uint32_t)__popc(vmask) * C::NH * 2048u);
+                        }
+                        __syncwarp();
+                        if (valid) {
+                            const int row0 = tok % B;
+                            const int o2 = p.slot_blk == 2 ? blk : (p.slot_layer == 2 ? p.layer : pc.kvh);
+                            const int o3 = p.slot_blk == 3 ? blk : (p.slot_layer == 3 ? p.layer : pc.kvh);
+                            const int o4 = p.slot_blk == 4 ? blk : (p.slot_layer == 4 ? p.layer : pc.kvh);
+                            const uint32_t dst = sbase + stage * C::TILE + lane * 2048;
+                            tma_load_5d(dst, kv ? &tmv : &tmk, fb, 0, row0, o2, o3, o4, pol);
+                            if constexpr (C::NH == 2)
+                                tma_load_5d(dst + C::HALF, kv ? &tmv : &tmk, fb, 64, row0, o2, o3, o4, pol);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (aborted || *abort_all)  // copies in flight land before the CTA can exit
+                for (int k = seq > C::NS ? seq - C::NS : 0; k < seq; ++k)
+                    (void)mbar_wait_bounded(bar0 + 8 * (C::KV_FULL + k % C::NS), (k / C::NS) & 1);
+        } else if (warp == 1) {
+            // ======================================================= MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t IDS = umma_idesc_bf16(128, C::TT, 0, 0);
+                constexpr uint32_t IDV = umma_idesc_bf16(128, D, 0, 1);
+                const uint64_t dK = umma_desc_sw128(sbase, 0, 1024);
+                const uint64_t dV = umma_desc_sw128(sbase, C::HALF, 1024);
+                const uint64_t dQ = umma_desc_sw128(sbase + C::OFF_Q, 0, 1024);
+                int seq = 0, np[2] = {0, 0}, nqj[2] = {0, 0};
+                bool ok = true;
+                auto stage_full = [&](int s) { return wait(C::KV_FULL + s % C::NS, (s / C::NS) & 1); };
+                auto score = [&](int j, int s) {  // S_j = Q_j K^T, K in stage s
+                    const uint64_t a = dQ + (uint64_t)((j * C::TILE) >> 4);
+                    const uint64_t b = dK + (uint64_t)(((s % C::NS) * C::TILE) >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = (uint64_t)(((k >> 2) * C::HALF + (k & 3) * 32) >> 4);
+                        umma_bf16(tmem + j * 128, a + o, b + o, IDS, k > 0 ? 1u : 0u);
+                    }
+                    umma_commit(bar0 + 8 * (C::S_FULL + j));
+                };
+                while (ok && pf_walk_next<C>(p, w, pc)) {
+                    const int nk = pc.kt1 - pc.kt0;
+                    for (int j = 0; j < pc.nj && ok; ++j) {
+                        ok = wait(C::Q_FULL + j, nqj[j] & 1);
+                        ++nqj[j];
+                    }
+                    if (!ok || !(ok = stage_full(seq))) break;
+                    tc_fence_after();
+                    for (int j = 0; j < pc.nj; ++j) {
+                        score(j, seq);
+                        if (nk == 1) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
+                    }
+                    umma_commit(bar0 + 8 * (C::KV_EMPTY + seq % C::NS));
+                    for (int i = 0; i < nk && ok; ++i, seq += 2) {
+                        const uint64_t v = dV + (uint64_t)((((seq + 1) % C::NS) * C::TILE) >> 4);
+                        for (int j = 0; j < pc.nj && ok; ++j) {
+                            ok = wait(C::P_FULL + j, np[j] & 1) && (j > 0 || stage_full(seq + 1));
+                            if (!ok) break;
+                            ++np[j];
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
+                                             v + (uint64_t)(k * (2048 >> 4)), IDV,
+                                             (i > 0 || k > 0) ? 1u : 0u);
+                            umma_commit(bar0 + 8 * (C::PV_DONE + j));
+                            if (j == pc.nj - 1)
+                                umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 1) % C::NS));
+                            if (i + 1 < nk) {
+                                if (j == 0 && !(ok = stage_full(seq + 2))) break;
+                                tc_fence_after();
+                                score(j, seq + 2);
+                                if (i + 2 == nk) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
+                                if (j == pc.nj - 1)
+                                    umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 2) % C::NS));
+                            }
+                        }
+                    }
+                }
+                // every MMA issued so far completes before TMEM is released
+                umma_commit(bar0 + 8 * C::FINAL);
+                (void)mbar_wait_bounded(bar0 + 8 * C::FINAL, 0);
+            }
+            __syncwarp();
+        } else {
+            // ============================================== Q rows (warps 2, 3)
+            constexpr int CPR = D / 8;               // 16-byte chunks per row
+            constexpr int RPI = 64 / CPR;            // rows per pass of the two warps
+            const int t = threadIdx.x - 64;
+            const int c = t % CPR;
+            int nqj[2] = {0, 0};
+            bool ok = true;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+            while (ok && pf_walk_next<C>(p, w, pc)) {
+                for (int j = 0; j < pc.nj && ok; ++j) {
+                    if (nqj[j] > 0)
+                        ok = __all_sync(kFullMask, wait(C::Q_EMPTY + j, (nqj[j] - 1) & 1));
+                    if (!ok) break;
+                    ++nqj[j];
+                    const uint32_t dst = sbase + C::OFF_Q + j * C::TILE + (c >> 3) * C::HALF;
+#pragma unroll 4
+                    for (int r = t / CPR; r < 128; r += RPI) {
+                        const int f = pc.row0 + 128 * j + r;
+                        const bool live = f < pc.s.rows;
+                        const int tok = live ? f / p.G : 0, g = live ? f - tok * p.G : 0;
+                        cp_async16(dst + sw128(r, c),
+                                   q + ((long long)(pc.s.start + tok) * p.H + pc.kvh * p.G + g) * D + 8 * c,
+                                   live);
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar0 + 8 * (C::Q_FULL + j));
+                }
+            }
+        }
+    } else {
+        // ============================================================ softmax
+        regs_inc<200>();
+        const int j = (warp - 4) >> 2;             // row tile
+        const int r = threadIdx.x - 128 - 128 * j; // row within it (TMEM lane)
+        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_col = trow + j * 128, o_col = trow + C::O_COL + j * D;
+        const float qs = p.qscale;
+        const bool neg = qs < 0.f;
+        int seq = 0, ns = 0;                       // V stage; tiles of this row tile so far
+        int piece = 0;
+        bool ok = true;
+        while (ok && pf_walk_next<C>(p, w, pc)) {
+            ++piece;
+            const int nk = pc.kt1 - pc.kt0;
+            if (j >= pc.nj) {
+                seq += 2 * nk;
+                if (r == 0) *wg1_done = piece;
+                continue;
+            }
+            const int f = pc.row0 + 128 * j + r;
+            const bool live = f < pc.s.rows;
+            const int tok = f / p.G;
+            const int pos = live ? pc.s.first_pos + tok : -1;
+            const int pair_pos = pc.s.first_pos + pc.row0 / p.G;   // the pair's first row's
+            float m = -FLT_MAX;   // reference point of the exponentials (scaled, base 2)
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int i = 0; i < nk; ++i, seq += 2, ++ns) {
+                const int t0 = (pc.kt0 + i) * C::TT;
+                const int vstage = (seq + 1) % C::NS;
+                // (V's arrival carries the tile's box bits)
+                ok = wait(C::KV_FULL + vstage, ((seq + 1) / C::NS) & 1) && wait(C::S_FULL + j, ns & 1);
+                ok = __all_sync(kFullMask, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const unsigned bits = (unsigned)box_bits[vstage] & 0xffu;
+                float x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x[c]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_loaded32(x[c]);
+                // keys 0 .. lim of the tile are the row's, in pages that are there
+                const int lim = pos - t0;
+                const bool masked = __any_sync(kFullMask, lim < 127) || bits != 0xffu;
+                if (masked) {
+                    const float off = neg ? INFINITY : -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int key = 32 * c + k;
+                            if (key > lim || !((bits >> (key >> 4)) & 1u)) x[c][k] = off;
+                        }
+                }
+                float mt;
+                if (!neg) {
+                    float a[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        a[c] = x[c][0];
+#pragma unroll
+                        for (int k = 1; k < 32; ++k) a[c] = fmaxf(a[c], x[c][k]);
+                    }
+                    mt = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                } else {
+                    float a[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        a[c] = x[c][0];
+#pragma unroll
+                        for (int k = 1; k < 32; ++k) a[c] = fminf(a[c], x[c][k]);
+                    }
+                    mt = fminf(fminf(a[0], a[1]), fminf(a[2], a[3]));
+                }
+                mt = fmaxf(mt * qs, -FLT_MAX);   // (no key seen, or 0 * inf: the floor)
+                if (i == 0) {
+                    m = mt;
+                } else if (__any_sync(kFullMask, mt > m + 8.f)) {
+                    const bool up = mt > m + 8.f;
+                    const float alpha = up ? ex2_approx(m - mt) : 1.f;
+                    if (up) m = mt;
+                    l2.x *= alpha, l2.y *= alpha;
+                    ok = __all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_col + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            asm volatile("" : "+r"(o[k]));
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        }
+                        tmem_st16(o_col + c, o);
+                    }
+                }
+                const float2 qq = make_float2(qs, qs), mm = make_float2(-m, -m);
+                // P over the row's own S columns, 16 columns (32 keys) at a time
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), qq, mm);
+                        float2 pv = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                        if (masked) {
+                            const int key = 32 * c + 2 * k;
+                            const bool in = (bits >> (key >> 4)) & 1u;
+                            if (key > lim || !in) pv.x = 0.f;
+                            if (key + 1 > lim || !in) pv.y = 0.f;
+                        }
+                        l2 = add2(l2, pv);
+                        pk[k] = pack_bf16x2(pv.x, pv.y);
+                    }
+                    tmem_st16(s_col + 16 * c, pk);
+                }
+                // V's rows that some row of the pair must not see
+                if (j == 0 && (bits != 0xffu || t0 + C::TT - 1 > pair_pos)) {
+                    unsigned char* vrow = smem + vstage * C::TILE + r * 128;
+                    const bool in = t0 + r < pc.s.n && ((bits >> (r >> 4)) & 1u);
+                    bool found = false;
+#pragma unroll
+                    for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint4* at = reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
+                            if (!in) {
+                                *at = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 v = *at;
+                                found = found || nonfinite2(v.x) || nonfinite2(v.y) ||
+                                        nonfinite2(v.z) || nonfinite2(v.w);
+                            }
+                        }
+                    if (wg0_or(found)) {
+                        if (*mark_piece != piece) {
+                            // group 1 may still be reading the marks of its last piece
+                            for (int n = 0; *wg1_done < piece - 1 && !*abort_all && n < (1 << 24); ++n)
+                                __nanosleep(100);
+                            wg0_or(false);   // (all have read mark_piece)
+                            for (int k = r; k < 3 * D; k += 128) marks[k] = INT_MAX;
+                            *mark_piece = piece;
+                            wg0_or(false);
+                        }
+                        if (found) {
+                            for (int h = 0; h < C::NH; ++h)
+                                for (int k = 0; k < 8; ++k) {
+                                    __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(
+                                        vrow + h * C::HALF + k * 16);
+                                    for (int e = 0; e < 8; ++e) {
+                                        const float v = __bfloat162float(at[e]);
+                                        if (isfinite(v)) continue;
+                                        const int d = h * 64 + (k ^ (r & 7)) * 8 + e;
+                                        atomicMin(marks + (v != v ? 0 : v > 0.f ? D : 2 * D) + d, t0 + r);
+                                        at[e] = __float2bfloat16(0.f);
+                                    }
+                                }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar0 + 8 * (C::P_FULL + j));
+            }
+            if (!ok) break;
+            // ------------------------------------------------ the piece's output
+            ok = __all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const float l = l2.x + l2.y;
+            const bool marked = *mark_piece == piece;
+            const float inv = pc.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const long long orow =
+                live ? (long long)(pc.s.start + tok) * p.H + pc.kvh * p.G + (f - tok * p.G) : 0;
+            const long long slot = ((long long)blockIdx.x * 2 + (pc.first ? 0 : 1)) * C::ROWS + 128 * j + r;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o_col + c, o);
+                tmem_wait_ld();
+                tmem_loaded32(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= inv;
+                if (marked) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] += poison(marks, D, c + k, pos);
+                }
+                if (!live) continue;
+                if (pc.whole) {
+                    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        out[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]),
+                                            pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                            pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
+                                            pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                } else {
+                    float4* out = reinterpret_cast<float4*>(p.part_o + slot * D + c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        out[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            if (!pc.whole && live) p.part_ml[2 * slot] = m, p.part_ml[2 * slot + 1] = l;
+            if (j == 1) {
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                if (r == 0) *wg1_done = piece;
+            }
+        }
+        if (!ok) *abort_all = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// Joins the parts of the pairs that the CTAs' shares cut: one group of CTAs per
+// main CTA, a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const PrefillParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int4 a = ld_dep(p.cut + 2 * blockIdx.x);
+    const int4 e = ld_dep(p.cut + 2 * blockIdx.x + 1);
+    const int pieces = e.x;
+    if (pieces <= 1) return;
+    const int row0 = 256 * a.z;
+    constexpr int V = D / 32;
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 256; r += gridDim.y * 8) {
+        const int f = row0 + r;
+        if (f >= e.z) return;
+        auto slot = [&](int k) {
+            return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? e.y : 0)) * 256 + r;
+        };
+        float m = -FLT_MAX;
+        for (int k = lane; k < pieces; k += 32) m = fmaxf(m, ld_dep(p.part_ml + 2 * slot(k)));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
+        float l = 0.f, o[V] = {};
+        for (int k = 0; k < pieces; ++k) {
+            const float2 ml = ld_dep(reinterpret_cast<const float2*>(p.part_ml) + slot(k));
+            if (ml.y == 0.f) continue;
+            const float w = ex2_approx(ml.x - m);
+            l = fmaf(w, ml.y, l);
+            const float* src = p.part_o + slot(k) * D + lane * V;
+#pragma unroll
+            for (int v = 0; v < V; v += 2) {
+                const float2 x = ld_dep(reinterpret_cast<const float2*>(src + v));
+                o[v] = fmaf(w, x.x, o[v]), o[v + 1] = fmaf(w, x.y, o[v + 1]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int tok = f / p.G;
+        const long long orow = (long long)(a.w + tok) * p.H + a.y * p.G + (f - tok * p.G);
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + lane * V);
+#pragma unroll
+        for (int v = 0; v < V; v += 2) out[v / 2] = pack_bf16x2(o[v] * inv, o[v + 1] * inv);
+    }
+}
+
+}  // namespace pa
