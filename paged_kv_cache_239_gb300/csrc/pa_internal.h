@@ -236,6 +236,11 @@ cudaError_t encode_pool_tmaps(const PoolGeom& g, void* tmaps, int* slot_blk, int
 // columns x box_rows rows, 128-byte swizzle) into one CUtensorMap at tmap.
 cudaError_t encode_rows_tmap(void* tmap, const void* base, long long rows, int box_rows);
 
+// Encodes a 3-D tensor map over bf16 [tokens][heads][D], contiguous (boxes of 64
+// columns x box_heads heads x box_tokens tokens, 128-byte swizzle).
+cudaError_t encode_heads_tmap(void* tmap, const void* base, int D, int heads, int tokens,
+                              int box_heads, int box_tokens);
+
 // tcgen05 kernel for bf16 pools, head_dim 128, groups that are multiples of
 // 16 (chunks of 64, 32 or 16 heads; decode_umma_chunk gives the chunk, 0 if
 // none); persistent, one CTA per SM.

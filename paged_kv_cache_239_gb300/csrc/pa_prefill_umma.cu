@@ -29,7 +29,12 @@ cudaError_t launch_inst(const PrefillParams& p, const CUtensorMap* tm, cudaStrea
             done_mask |= bit;
         }
     }
-    e = launch_pdl(kern, dim3((unsigned)p.grid), dim3(C::THREADS), C::SMEM_BYTES, s, p, tm[0], tm[1]);
+    CUtensorMap tq{};  // (not used for groups that do not divide 128)
+    if (128 % p.G == 0) {
+        e = encode_heads_tmap(&tq, p.q, D, p.H, p.num_tokens, p.G, 128 / p.G);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(kern, dim3((unsigned)p.grid), dim3(C::THREADS), C::SMEM_BYTES, s, p, tm[0], tm[1], tq);
     if (e != cudaSuccess || p.grid == 1) return e;
     return launch_pdl(pa_prefill_umma_join_kernel<D>, dim3((unsigned)p.grid, 8), dim3(256), 0, s, p);
 }

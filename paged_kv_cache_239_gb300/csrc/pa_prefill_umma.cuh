@@ -18,13 +18,12 @@
 // merges.
 //
 // Roles, connected by mbarriers:
-//  * warp 0: K and V tiles into one ring of stages, K(0) V(0) K(1) V(1) ..., by
-//    5-D tensor-map TMA, a 16-row box per lane, pages from the block table;
+//  * warps 0 and 3: K and V tiles into one ring of stages, K(0) V(0) K(1) V(1)
+//    ..., in 16-row boxes by 5-D tensor-map TMA, pages from the block table;
 //  * warp 1: tensor memory, and one thread issuing for each key tile i and row
 //    tile j  O_j += P_j(i) V(i), then S_j(i + 1) = Q_j K(i + 1)^T: the softmax of
 //    one row tile runs under the products of the other;
-//  * warps 2, 3: Q of the next pair, gathered by rows (cp.async) into the
-//    swizzled layout;
+//  * warp 2: Q of the next pair, by tensor map or row by row (cp.async);
 //  * warps 4-7 and 8-11: softmax of row tile 0 and 1, one row per thread, so no
 //    exchange between threads: S from tensor memory, running maximum (raised,
 //    and O rescaled, only when a score exceeds it by more than 2^8: any
@@ -62,13 +61,14 @@ struct PrefillCfg {
     static constexpr int NH = D / 64;              // 64-column halves
     static constexpr int HALF = 128 * 128;         // one half of a 128-row tile (bytes)
     static constexpr int TILE = NH * HALF;
-    static constexpr int NS = D == 128 ? 5 : 10;   // K/V stages
+    static constexpr int NS = D == 128 ? 5 : 9;   // K/V stages
     static constexpr int OFF_Q = NS * TILE;
     static constexpr int OFF_CTRL = OFF_Q + 2 * TILE;
     // ctrl (bytes): barriers | TMEM address, abort, mark_piece, wg1_done |
-    // box bits per stage | schedule | scan scratch | marks [3][D]
+    // box bits per stage | schedule | scan scratch, then the producers' page ids |
+    // marks [3][D]
     static constexpr int TMEM_SLOT = 256, ABORT = 260, MARK_PIECE = 264, WG1_DONE = 268,
-                         BITS = 272, SCHED = 320, SCAN = 384, MARKS = 512;
+                         BITS = 272, SCHED = 320, SCAN = 384, BLOCKS = SCAN, MARKS = 512;
     static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 3 * 128 * 4 + 1024;
     static constexpr int THREADS = 384;
     // TMEM: S_0, S_1 (P in their first 64 columns), O_0, O_1
@@ -76,13 +76,13 @@ struct PrefillCfg {
     static constexpr int TMEM_COLS = 512;
     // barriers
     static constexpr int KV_FULL = 0, KV_EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
-                         S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6, PV_DONE = Q_FULL + 8,
-                         FINAL = Q_FULL + 10, NBAR = Q_FULL + 11;
+                         S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6, P_HALF = Q_FULL + 8,
+                         PV_DONE = Q_FULL + 10, FINAL = Q_FULL + 12, NBAR = Q_FULL + 13;
     static_assert(NBAR * 8 <= TMEM_SLOT && NS <= 12, "ctrl layout");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
-constexpr int kPairUnits = 2;
+constexpr int kPairUnits = 3;
 
 // A sequence as the schedule sees it.
 struct PfSeq {
@@ -339,6 +339,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0;
+}
+
 // cp.async of one 16-byte chunk (zeros when !valid).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -355,6 +363,31 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// umma_wait for waits that are on the critical path: the timer and the abort
+// flag are looked at once in 64 tries.
+__device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, volatile int* abort_all,
+                                        unsigned* status) {
+    for (int it = 0; it < 64; ++it)
+        if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t it = 0; it < (1u << 30); ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) != 63) continue;
+        if (*abort_all) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+    }
+    *abort_all = 1;
+    atomicOr(status, kStatusTimeout);
+    return false;
+}
+
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store32(void* at, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Barrier over the 128 threads of softmax group 0 with an OR of `v`.
 __device__ __forceinline__ bool wg0_or(bool v) {
     uint32_t r;
@@ -367,9 +400,60 @@ __device__ __forceinline__ bool wg0_or(bool v) {
     return r != 0;
 }
 
-// True where either bf16 of the word is infinite or NaN.
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Bit 15 or 31 set where a bf16 of the word is infinite or NaN (its exponent,
+// all ones, carries into the sign's place).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+    return (w & 0x7f807f80u) + 0x00800080u;
+}
+
+// One row's part of a key tile: reads S (128 columns at s_col), lets `raise`
+// settle the row's reference point m (false: stop), and writes P over S's first
+// 64 columns, its sum added to l2.  With `masked`, only the keys whose bits are
+// set in vis (32 to a word) have weight: the others' scores become -inf and
+// their weights 0 (qs > 0, and m is never -inf).
+template <typename Raise, typename Ready>
+__device__ __forceinline__ bool pf_softmax_tile(uint32_t s_col, float qs, bool masked,
+                                                const uint32_t (&vis)[4], float& m, float2& l2,
+                                                Raise raise, Ready ready) {
+    float x[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x[c]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_loaded32(x[c]);
+    if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (!((vis[c] >> k) & 1u)) x[c][k] = -INFINITY;
+    }
+    float a[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        a[c] = x[c >> 1][16 * (c & 1)];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) a[c] = fmaxf(a[c], x[c >> 1][16 * (c & 1) + k]);
+    }
+    const float mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])),
+                           fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
+    // (no key seen: the finite floor)
+    if (!raise(fmaxf(mx * qs, -FLT_MAX))) return false;
+    const float2 qq = make_float2(qs, qs), mm = make_float2(-m, -m);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), qq, mm);
+            const float2 pv = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            l2 = add2(l2, pv);
+            pk[k] = pack_bf16x2(pv.x, pv.y);
+        }
+        tmem_st16(s_col + 16 * c, pk);
+        if (c & 1) ready(c >> 1);
+    }
+    return true;
 }
 
 // What a column's remembered values (first positions of a NaN, +inf, -inf) add
@@ -382,7 +466,8 @@ __device__ __forceinline__ float poison(const int* marks, int D, int d, int pos)
 template <int D, int B>
 __global__ void __launch_bounds__(384, 1)
     pa_prefill_umma_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
-                           const __grid_constant__ CUtensorMap tmv) {
+                           const __grid_constant__ CUtensorMap tmv,
+                           const __grid_constant__ CUtensorMap tmq) {
     pdl_trigger();
     using C = PrefillCfg<D, B>;
     extern __shared__ unsigned char smem_raw[];
@@ -402,9 +487,8 @@ __global__ void __launch_bounds__(384, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) {
-            const bool p_full = i == C::P_FULL || i == C::P_FULL + 1;
-            const bool q_full = i == C::Q_FULL || i == C::Q_FULL + 1;
-            mbar_init(bar0 + 8 * i, p_full ? 4 : q_full ? 2 : 1);
+            const bool p_full = i >= C::P_FULL && i < C::P_FULL + 4;  // (and P_HALF)
+            mbar_init(bar0 + 8 * i, p_full ? 4 : 1);
         }
         *abort_all = 0, *mark_piece = -1, *wg1_done = 0;
         fence_mbar_init();
@@ -413,6 +497,7 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
+        prefetch_tensormap(&tmq);
     }
     pdl_wait();
     pf_schedule<C>(p, ctrl);
@@ -421,7 +506,7 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](int bar, uint32_t parity) {
-        return umma_wait(bar0 + 8 * bar, parity, abort_all, p.status);
+        return pf_wait(bar0 + 8 * bar, parity, abort_all, p.status);
     };
     PfWalk w;
     pf_walk_begin<C>(p, ctrl, w);
@@ -429,15 +514,18 @@ __global__ void __launch_bounds__(384, 1)
 
     if (warp < 4) {
         regs_dec<104>();
-        if (warp == 0) {
-            // ===================================================== K and V tiles
-            int seq = 0;  // stages filled so far
+        if (warp == 0 || warp == 3) {
+            // ====================================== K tiles (warp 0), V tiles (warp 3)
+            const int kv = warp == 0 ? 0 : 1;
+            const CUtensorMap* tm = kv ? &tmv : &tmk;
+            int* blocks = reinterpret_cast<int*>(ctrl + C::BLOCKS) + 8 * kv;
+            int seq = kv;  // the next stage of the ring (K the even, V the odd ones)
             bool aborted = false;
             const uint64_t pol = l2_policy_evict_normal();
-            if (lane == 0 && p.cut != nullptr)
+            if (kv == 0 && lane == 0 && p.cut != nullptr)
                 p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);  // (no cut pair yet)
             while (!aborted && pf_walk_next<C>(p, w, pc)) {
-                if (lane == 0 && p.cut != nullptr && !pc.whole && pc.kt0 == 0) {
+                if (kv == 0 && lane == 0 && p.cut != nullptr && !pc.whole && pc.kt0 == 0) {
                     // this CTA holds the first part of a pair that others go on with
                     const long long T = *reinterpret_cast<const long long*>(ctrl + C::SCHED);
                     const long long last = (pc.gpos + pc.kvt - 1) * min((long long)gridDim.x, T) / T;
@@ -452,47 +540,58 @@ __global__ void __launch_bounds__(384, 1)
                                : -1;
                 };
                 int blk_next = box_block(pc.kt0);
-                for (int kt = pc.kt0; kt < pc.kt1 && !aborted; ++kt) {
+                for (int kt = pc.kt0; kt < pc.kt1; ++kt, seq += 2) {
                     const int tok = kt * C::TT + 16 * lane;
                     const int blk = blk_next;
                     blk_next = box_block(kt + 1);
                     const bool inside = lane < 8 && tok < pc.s.n;
                     const bool valid = inside && blk >= 0 && blk < p.num_blocks;
                     const unsigned vmask = __ballot_sync(kFullMask, valid);
-                    if (inside && !valid) atomicOr(p.status, kStatusBadBlock);
-                    for (int kv = 0; kv < 2; ++kv, ++seq) {
-                        const int stage = seq % C::NS;
-                        if (seq >= C::NS &&
-                            !__all_sync(kFullMask, wait(C::KV_EMPTY + stage, (seq / C::NS - 1) & 1))) {
-                            aborted = true;
-                            break;
-                        }
-                        const uint32_t fb = bar0 + 8 * (C::KV_FULL + stage);
-                        if (lane == 0) {
-                            box_bits[stage] = (int)vmask;
-                            mbar_arrive_expect_tx(fb, (uint32_t)__popc(vmask) * C::NH * 2048u);
-                        }
-                        __syncwarp();
-                        if (valid) {
-                            const int row0 = tok % B;
-                            const int o2 = p.slot_blk == 2 ? blk : (p.slot_layer == 2 ? p.layer : pc.kvh);
-                            const int o3 = p.slot_blk == 3 ? blk : (p.slot_layer == 3 ? p.layer : pc.kvh);
-                            const int o4 = p.slot_blk == 4 ? blk : (p.slot_layer == 4 ? p.layer : pc.kvh);
-                            const uint32_t dst = sbase + stage * C::TILE + lane * 2048;
-                            tma_load_5d(dst, kv ? &tmv : &tmk, fb, 0, row0, o2, o3, o4, pol);
-                            if constexpr (C::NH == 2)
-                                tma_load_5d(dst + C::HALF, kv ? &tmv : &tmk, fb, 64, row0, o2, o3, o4, pol);
-                        }
-                        __syncwarp();
+                    if (kv && inside && !valid) atomicOr(p.status, kStatusBadBlock);
+                    const int stage = seq % C::NS;
+                    if (lane < 8) blocks[lane] = blk;
+                    if (seq >= C::NS &&
+                        !__all_sync(kFullMask, wait(C::KV_EMPTY + stage, (seq / C::NS - 1) & 1))) {
+                        aborted = true;
+                        break;
                     }
+                    __syncwarp();
+                    // (one thread issues all boxes: eight lanes taking turns at it
+                    // cost the warp several times the instructions)
+                    if (elect_one()) {
+                        const uint32_t fb = bar0 + 8 * (C::KV_FULL + stage);
+                        if (kv) box_bits[stage] = (int)vmask;
+                        mbar_arrive_expect_tx(fb, (uint32_t)__popc(vmask) * C::NH * 2048u);
+                        const int4 lo = *reinterpret_cast<const int4*>(blocks);
+                        const int4 hi = *reinterpret_cast<const int4*>(blocks + 4);
+                        const int id[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        const uint32_t dst = sbase + stage * C::TILE;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            if (!((vmask >> r) & 1u)) continue;
+                            const int row0 = (16 * r) % B;
+                            const int o2 = p.slot_blk == 2 ? id[r] : (p.slot_layer == 2 ? p.layer : pc.kvh);
+                            const int o3 = p.slot_blk == 3 ? id[r] : (p.slot_layer == 3 ? p.layer : pc.kvh);
+                            const int o4 = p.slot_blk == 4 ? id[r] : (p.slot_layer == 4 ? p.layer : pc.kvh);
+#pragma unroll
+                            for (int h = 0; h < C::NH; ++h)
+                                tma_load_5d(dst + r * 2048 + h * C::HALF, tm, fb, 64 * h, row0, o2, o3, o4, pol);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             if (aborted || *abort_all)  // copies in flight land before the CTA can exit
-                for (int k = seq > C::NS ? seq - C::NS : 0; k < seq; ++k)
+                for (int k = seq - 2; k >= 0 && k >= seq - C::NS; k -= 2)
                     (void)mbar_wait_bounded(bar0 + 8 * (C::KV_FULL + k % C::NS), (k / C::NS) & 1);
+            __syncwarp();
         } else if (warp == 1) {
             // ======================================================= MMA issuer
-            if (lane == 0) {
+            // (elect.sync, not lane == 0: ptxas then knows that one thread runs the
+            // region and keeps the descriptors in uniform registers.  Beside warps
+            // that fill the issue slots a 128 x 128 x 16 MMA is issued every 66
+            // cycles, 64 being the pipe's rate; under lane == 0 every 242.)
+            if (elect_one()) {
                 constexpr uint32_t IDS = umma_idesc_bf16(128, C::TT, 0, 0);
                 constexpr uint32_t IDV = umma_idesc_bf16(128, D, 0, 1);
                 const uint64_t dK = umma_desc_sw128(sbase, 0, 1024);
@@ -527,15 +626,23 @@ __global__ void __launch_bounds__(384, 1)
                     for (int i = 0; i < nk && ok; ++i, seq += 2) {
                         const uint64_t v = dV + (uint64_t)((((seq + 1) % C::NS) * C::TILE) >> 4);
                         for (int j = 0; j < pc.nj && ok; ++j) {
-                            ok = wait(C::P_FULL + j, np[j] & 1) && (j > 0 || stage_full(seq + 1));
+                            // the first half of the keys while the exponentials of
+                            // the second are still under way
+                            ok = wait(C::P_HALF + j, np[j] & 1) && (j > 0 || stage_full(seq + 1));
                             if (!ok) break;
-                            ++np[j];
                             tc_fence_after();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
+                            for (int k = 0; k < 4; ++k)
                                 umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
                                              v + (uint64_t)(k * (2048 >> 4)), IDV,
                                              (i > 0 || k > 0) ? 1u : 0u);
+                            if (!(ok = wait(C::P_FULL + j, np[j] & 1))) break;
+                            ++np[j];
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 4; k < 8; ++k)
+                                umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
+                                             v + (uint64_t)(k * (2048 >> 4)), IDV, 1u);
                             umma_commit(bar0 + 8 * (C::PV_DONE + j));
                             if (j == pc.nj - 1)
                                 umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 1) % C::NS));
@@ -556,11 +663,15 @@ __global__ void __launch_bounds__(384, 1)
             }
             __syncwarp();
         } else {
-            // ============================================== Q rows (warps 2, 3)
+            // ============================================== Q rows (warp 2)
+            // Groups that divide 128: a tile is 128 / G tokens' heads, one box of
+            // the 3-D tensor map (columns, heads, tokens) per half; what it holds
+            // past the sequence belongs to rows that are not written.  Other
+            // groups: row by row.
             constexpr int CPR = D / 8;               // 16-byte chunks per row
-            constexpr int RPI = 64 / CPR;            // rows per pass of the two warps
-            const int t = threadIdx.x - 64;
-            const int c = t % CPR;
+            constexpr int RPI = 32 / CPR;            // rows per pass
+            const int c = lane % CPR;
+            const bool boxes = 128 % p.G == 0;
             int nqj[2] = {0, 0};
             bool ok = true;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
@@ -570,22 +681,49 @@ __global__ void __launch_bounds__(384, 1)
                         ok = __all_sync(kFullMask, wait(C::Q_EMPTY + j, (nqj[j] - 1) & 1));
                     if (!ok) break;
                     ++nqj[j];
-                    const uint32_t dst = sbase + C::OFF_Q + j * C::TILE + (c >> 3) * C::HALF;
+                    const uint32_t fb = bar0 + 8 * (C::Q_FULL + j);
+                    const uint32_t tile = sbase + C::OFF_Q + j * C::TILE;
+                    const int f0 = pc.row0 + 128 * j;
+                    if (boxes && p.qscale >= 0.f) {
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(fb, (uint32_t)C::TILE);
+                            for (int h = 0; h < C::NH; ++h)
+                                tma_load_3d(tile + h * C::HALF, &tmq, fb, 64 * h, pc.kvh * p.G,
+                                            pc.s.start + f0 / p.G);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
+                    const uint32_t dst = tile + (c >> 3) * C::HALF;
+                    int tok = (f0 + lane / CPR) / p.G, g = (f0 + lane / CPR) - tok * p.G;
 #pragma unroll 4
-                    for (int r = t / CPR; r < 128; r += RPI) {
-                        const int f = pc.row0 + 128 * j + r;
-                        const bool live = f < pc.s.rows;
-                        const int tok = live ? f / p.G : 0, g = live ? f - tok * p.G : 0;
+                    for (int r = lane / CPR; r < 128; r += RPI) {
+                        const bool live = f0 + r < pc.s.rows;
                         cp_async16(dst + sw128(r, c),
-                                   q + ((long long)(pc.s.start + tok) * p.H + pc.kvh * p.G + g) * D + 8 * c,
+                                   live ? q + ((long long)(pc.s.start + tok) * p.H + pc.kvh * p.G + g) * D + 8 * c
+                                        : q,
                                    live);
+                        for (g += RPI; g >= p.G; g -= p.G) ++tok;
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
+                    if (p.qscale < 0.f) {  // S = -Q K^T, and the softmax scales by |scale|
+                        for (int r = lane / CPR; r < 128; r += RPI) {
+                            uint4* at = reinterpret_cast<uint4*>(smem + C::OFF_Q + j * C::TILE +
+                                                                 (c >> 3) * C::HALF + sw128(r, c));
+                            uint4 v = *at;
+                            v.x ^= 0x80008000u, v.y ^= 0x80008000u, v.z ^= 0x80008000u, v.w ^= 0x80008000u;
+                            *at = v;
+                        }
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar0 + 8 * (C::Q_FULL + j));
+                    if (lane == 0) mbar_arrive(fb);
                 }
             }
+            if (*abort_all && lane == 0)  // copies in flight land before the CTA can exit
+                for (int j = 0; j < 2; ++j)
+                    if (nqj[j] > 0) (void)mbar_wait_bounded(bar0 + 8 * (C::Q_FULL + j), (nqj[j] - 1) & 1);
+            __syncwarp();
         }
     } else {
         // ============================================================ softmax
@@ -594,8 +732,10 @@ __global__ void __launch_bounds__(384, 1)
         const int r = threadIdx.x - 128 - 128 * j; // row within it (TMEM lane)
         const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t s_col = trow + j * 128, o_col = trow + C::O_COL + j * D;
-        const float qs = p.qscale;
-        const bool neg = qs < 0.f;
+        // (a negative scale's sign is in Q; 0 becomes the smallest positive one, so
+        // that -inf stays -inf)
+        const float qs = fmaxf(fabsf(p.qscale), FLT_MIN);
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         int seq = 0, ns = 0;                       // V stage; tiles of this row tile so far
         int piece = 0;
         bool ok = true;
@@ -623,107 +763,27 @@ __global__ void __launch_bounds__(384, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const unsigned bits = (unsigned)box_bits[vstage] & 0xffu;
-                float x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x[c]);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_loaded32(x[c]);
-                // keys 0 .. lim of the tile are the row's, in pages that are there
-                const int lim = pos - t0;
-                const bool masked = __any_sync(kFullMask, lim < 127) || bits != 0xffu;
-                if (masked) {
-                    const float off = neg ? INFINITY : -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int key = 32 * c + k;
-                            if (key > lim || !((bits >> (key >> 4)) & 1u)) x[c][k] = off;
-                        }
-                }
-                float mt;
-                if (!neg) {
-                    float a[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        a[c] = x[c][0];
-#pragma unroll
-                        for (int k = 1; k < 32; ++k) a[c] = fmaxf(a[c], x[c][k]);
-                    }
-                    mt = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-                } else {
-                    float a[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        a[c] = x[c][0];
-#pragma unroll
-                        for (int k = 1; k < 32; ++k) a[c] = fminf(a[c], x[c][k]);
-                    }
-                    mt = fminf(fminf(a[0], a[1]), fminf(a[2], a[3]));
-                }
-                mt = fmaxf(mt * qs, -FLT_MAX);   // (no key seen, or 0 * inf: the floor)
-                if (i == 0) {
-                    m = mt;
-                } else if (__any_sync(kFullMask, mt > m + 8.f)) {
-                    const bool up = mt > m + 8.f;
-                    const float alpha = up ? ex2_approx(m - mt) : 1.f;
-                    if (up) m = mt;
-                    l2.x *= alpha, l2.y *= alpha;
-                    ok = __all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_col + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            asm volatile("" : "+r"(o[k]));
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        }
-                        tmem_st16(o_col + c, o);
-                    }
-                }
-                const float2 qq = make_float2(qs, qs), mm = make_float2(-m, -m);
-                // P over the row's own S columns, 16 columns (32 keys) at a time
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), qq, mm);
-                        float2 pv = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                        if (masked) {
-                            const int key = 32 * c + 2 * k;
-                            const bool in = (bits >> (key >> 4)) & 1u;
-                            if (key > lim || !in) pv.x = 0.f;
-                            if (key + 1 > lim || !in) pv.y = 0.f;
-                        }
-                        l2 = add2(l2, pv);
-                        pk[k] = pack_bf16x2(pv.x, pv.y);
-                    }
-                    tmem_st16(s_col + 16 * c, pk);
-                }
                 // V's rows that some row of the pair must not see
                 if (j == 0 && (bits != 0xffu || t0 + C::TT - 1 > pair_pos)) {
                     unsigned char* vrow = smem + vstage * C::TILE + r * 128;
                     const bool in = t0 + r < pc.s.n && ((bits >> (r >> 4)) & 1u);
-                    bool found = false;
+                    uint32_t odd = 0;
+                    if (!in || t0 + r > pair_pos) {
 #pragma unroll
-                    for (int h = 0; h < C::NH; ++h)
+                        for (int h = 0; h < C::NH; ++h)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint4* at = reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
-                            if (!in) {
-                                *at = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 v = *at;
-                                found = found || nonfinite2(v.x) || nonfinite2(v.y) ||
-                                        nonfinite2(v.z) || nonfinite2(v.w);
+                            for (int k = 0; k < 8; ++k) {
+                                uint4* at = reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
+                                if (!in) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    const uint4 v = *at;
+                                    odd |= (nonfinite2(v.x) | nonfinite2(v.y)) |
+                                           (nonfinite2(v.z) | nonfinite2(v.w));
+                                }
                             }
-                        }
+                    }
+                    const bool found = (odd & 0x80008000u) != 0;
                     if (wg0_or(found)) {
                         if (*mark_piece != piece) {
                             // group 1 may still be reading the marks of its last piece
@@ -751,10 +811,52 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar0 + 8 * (C::P_FULL + j));
+                // keys 0 .. lim of the tile are the row's, in pages that are there
+                const int lim = pos - t0;
+                const bool masked = __any_sync(kFullMask, lim < 127) || bits != 0xffu;
+                // O's scale-down, should the tile raise the row's reference point
+                auto raise = [&](float mt) {
+                    if (i == 0) {
+                        m = mt;
+                        return true;
+                    }
+                    if (!__any_sync(kFullMask, mt > m + 8.f)) return true;
+                    const bool up = mt > m + 8.f;
+                    const float alpha = up ? ex2_approx(m - mt) : 1.f;
+                    if (up) m = mt;
+                    l2.x *= alpha, l2.y *= alpha;
+                    if (!__all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1))) return false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_col + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            asm volatile("" : "+r"(o[k]));
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        }
+                        tmem_st16(o_col + c, o);
+                    }
+                    return true;
+                };
+                uint32_t vis[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int e = lim - 32 * c;  // the last of the word's keys the row sees
+                    vis[c] = (e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u) &
+                             (((bits >> (2 * c)) & 1u ? 0xffffu : 0u) |
+                              ((bits >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
+                }
+                auto ready = [&](int half) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar0 + 8 * ((half ? C::P_FULL : C::P_HALF) + j));
+                };
+                ok = pf_softmax_tile(s_col, qs, masked, vis, m, l2, raise, ready);
+                if (!ok) break;
             }
             if (!ok) break;
             // ------------------------------------------------ the piece's output
@@ -781,18 +883,30 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (!live) continue;
                 if (pc.whole) {
-                    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + c);
+                    // (whole sectors per thread: the rows of a warp lie apart)
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D + c;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        out[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]),
-                                            pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                            pack_bf16x2(o[8 * k + 4], o[8 * k + 5]),
-                                            pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = pack_bf16x2(o[16 * h + 2 * k], o[16 * h + 2 * k + 1]);
+                        if (out32) {
+                            store32(out + 16 * h, v);
+                        } else {
+                            reinterpret_cast<uint4*>(out)[2 * h] = make_uint4(v[0], v[1], v[2], v[3]);
+                            reinterpret_cast<uint4*>(out)[2 * h + 1] = make_uint4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
                 } else {
-                    float4* out = reinterpret_cast<float4*>(p.part_o + slot * D + c);
+                    float* out = p.part_o + slot * D + c;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        out[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * h + k]);
+                        store32(out + 8 * h, v);
+                    }
                 }
             }
             if (!pc.whole && live) p.part_ml[2 * slot] = m, p.part_ml[2 * slot + 1] = l;
