@@ -1169,6 +1169,11 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
         if (int rc = pool_tmaps(pool)) return rc;
         p.slot_blk = pool->tma_slots[0];
         p.slot_layer = pool->tma_slots[1];
+        // division by G: with s = ceil(log2 G) and m = ceil(2^(31 + s) / G), x m
+        // >> (31 + s) is exact for x < 2^31 (m G - 2^(31 + s) < G <= 2^s)
+        p.div_shift = 31;
+        while ((1LL << (p.div_shift - 31)) < p.G) ++p.div_shift;
+        p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
         e = pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
     } else {
         e = pa::launch_prefill_simt(p, g.D, g.B, s);

@@ -147,6 +147,8 @@ struct PrefillParams {
     int grid;                // bf16: persistent CTAs, and per CTA two int4: the
     int4* cut;               // pair whose first part it holds while others go on
     int slot_blk, slot_layer;  // tensor-map dimensions of the pool's axes
+    unsigned div_mul;        // x / G = x * div_mul >> div_shift for x < 2^31
+    int div_shift;
 };
 
 // The pages of a pool (see pa_pages.cu).

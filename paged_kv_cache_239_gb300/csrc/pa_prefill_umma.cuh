@@ -23,7 +23,8 @@
 //  * warp 1: tensor memory, and one thread issuing for each key tile i and row
 //    tile j  O_j += P_j(i) V(i), then S_j(i + 1) = Q_j K(i + 1)^T: the softmax of
 //    one row tile runs under the products of the other;
-//  * warp 2: Q of the next pair, by tensor map or row by row (cp.async);
+//  * warp 2: Q of the next pair, by tensor map or row by row (cp.async), and the
+//    look over V (below);
 //  * warps 4-7 and 8-11: softmax of row tile 0 and 1, one row per thread, so no
 //    exchange between threads: S from tensor memory, running maximum (raised,
 //    and O rescaled, only when a score exceeds it by more than 2^8: any
@@ -61,24 +62,27 @@ struct PrefillCfg {
     static constexpr int NH = D / 64;              // 64-column halves
     static constexpr int HALF = 128 * 128;         // one half of a 128-row tile (bytes)
     static constexpr int TILE = NH * HALF;
-    static constexpr int NS = D == 128 ? 5 : 9;   // K/V stages
+    static constexpr int NS = D == 128 ? 5 : 8;   // K/V stages
     static constexpr int OFF_Q = NS * TILE;
     static constexpr int OFF_CTRL = OFF_Q + 2 * TILE;
-    // ctrl (bytes): barriers | TMEM address, abort, mark_piece, wg1_done |
-    // box bits per stage | schedule | scan scratch, then the producers' page ids |
-    // marks [3][D]
-    static constexpr int TMEM_SLOT = 256, ABORT = 260, MARK_PIECE = 264, WG1_DONE = 268,
-                         BITS = 272, SCHED = 320, SCAN = 384, BLOCKS = SCAN, MARKS = 512;
-    static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 3 * 128 * 4 + 1024;
+    // ctrl (bytes): barriers | TMEM address, abort, mark_piece, done[2] | box bits
+    // per stage | schedule | the producers' page ids | pieces [NP] | marks [3][D]
+    // (the schedule's scratch before)
+    static constexpr int NP = 4;
+    static constexpr int TMEM_SLOT = 384, ABORT = 388, MARK_PIECE = 392, DONE = 396, BITS = 404,
+                         SCHED = 448, BLOCKS = 496, PIECES = 576, MARKS = 832, SCAN = MARKS;
+    static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 3 * 128 * 4;
     static constexpr int THREADS = 384;
     // TMEM: S_0, S_1 (P in their first 64 columns), O_0, O_1
     static constexpr int O_COL = 256;
     static constexpr int TMEM_COLS = 512;
     // barriers
     static constexpr int KV_FULL = 0, KV_EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
-                         S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6, P_HALF = Q_FULL + 8,
-                         PV_DONE = Q_FULL + 10, FINAL = Q_FULL + 12, NBAR = Q_FULL + 13;
-    static_assert(NBAR * 8 <= TMEM_SLOT && NS <= 12, "ctrl layout");
+                         S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6,  // three parts, [part][row tile]
+                         PV_DONE = Q_FULL + 12, FINAL = Q_FULL + 14,
+                         V_LOOK = Q_FULL + 15, V_CLEAN = Q_FULL + 16,
+                         PC_FULL = Q_FULL + 17, PC_EMPTY = PC_FULL + NP, NBAR = PC_EMPTY + NP;
+    static_assert(NBAR * 8 <= TMEM_SLOT && NS <= 11, "ctrl layout");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
@@ -111,20 +115,34 @@ __device__ __forceinline__ PfSeq pf_sequence(const PrefillParams& p, int b, bool
     return s;
 }
 
+// x / G for 0 <= x < 2^31 (the host's multiplier: a 32-bit division costs ~30
+// instructions, and the set-up runs many).
+__device__ __forceinline__ int pf_div(const PrefillParams& p, int x) {
+    return (int)(((unsigned long long)(unsigned)x * p.div_mul) >> p.div_shift);
+}
+
 // Key tiles of pair i of a sequence (at least one: the pair owes its output).
-__device__ __forceinline__ int pf_key_tiles(const PfSeq& s, int i, int G) {
+__device__ __forceinline__ int pf_key_tiles(const PrefillParams& p, const PfSeq& s, int i) {
     const int last = min(s.rows, 256 * (i + 1)) - 1;
-    const int see = s.first_pos + last / G + 1;
+    const int see = s.first_pos + pf_div(p, last) + 1;
     return see > 128 ? (see + 127) >> 7 : 1;
 }
 
-// A piece: key tiles [kt0, kt1) of one pair.
-struct PfPiece {
-    int b, kvh, i, kt0, kt1, kvt;
-    PfSeq s;
-    long long gpos;   // global unit of the pair's first key tile
-    bool whole, first;
-    int nj, row0;     // row tiles (1 or 2), first row of the pair
+// a / b, in 32 bits where both fit; out of line (see pf_wait_call).
+__device__ __noinline__ long long pf_div64(long long a, long long b) {
+    if ((unsigned long long)(a | b) >> 32) return a / b;
+    return (unsigned)a / (unsigned)b;
+}
+
+// A piece: key tiles [kt0, kt1) of one pair, as its roles see it.  The K
+// producer walks the CTA's share and hands the pieces to the others in a small
+// ring in shared memory.
+struct alignas(16) PfPiece {
+    int kvh, kt0, kt1, nj;   // KV head, key tiles, row tiles (1 or 2; 0: no more pieces)
+    int row0, rows, start, first_pos;  // first row of the pair; the sequence's rows, token, position
+    int n, pair_pos, b, flags;  // context; position of the pair's first row; sequence
+    __device__ __forceinline__ bool whole() const { return flags & 1; }
+    __device__ __forceinline__ bool first() const { return flags & 2; }
 };
 
 struct PfWalk {
@@ -142,7 +160,8 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
     if (bad && report) atomicOr(p.status, kStatusBadLength);
     long long u = 0;
     if (s.tiles <= 8)
-        for (int i = 0; i < s.tiles; ++i) u += kPairUnits + pf_key_tiles(s, i, p.G);
+#pragma unroll 1
+        for (int i = 0; i < s.tiles; ++i) u += kPairUnits + pf_key_tiles(p, s, i);
     unsigned big = __ballot_sync(kFullMask, s.tiles > 8);
     while (big) {
         const int f = __ffs(big) - 1;
@@ -152,7 +171,8 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
         o.rows = __shfl_sync(kFullMask, s.rows, f);
         o.tiles = __shfl_sync(kFullMask, s.tiles, f);
         long long v = 0;
-        for (int i = lane; i < o.tiles; i += 32) v += kPairUnits + pf_key_tiles(o, i, p.G);
+#pragma unroll 1
+        for (int i = lane; i < o.tiles; i += 32) v += kPairUnits + pf_key_tiles(p, o, i);
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(kFullMask, v, x);
         if (lane == f) u = v;
@@ -170,6 +190,7 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
     long long* out = reinterpret_cast<long long*>(ctrl + C::SCHED);
     int* outi = reinterpret_cast<int*>(ctrl + C::SCHED + 32);
     long long u = 0, mine = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += C::THREADS) {
         u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, blockIdx.x == 0);
         mine += u;
@@ -187,10 +208,11 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
     const long long j = blockIdx.x;
     long long lo = 0, hi = 0;
     if (j < grid) {
-        lo = (j * T + grid - 1) / grid;
-        hi = ((j + 1) * T + grid - 1) / grid;
+        lo = pf_div64(j * T + grid - 1, grid);
+        hi = pf_div64((j + 1) * T + grid - 1, grid);
     }
     long long before = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += C::THREADS) {
         if (p.batch > C::THREADS) u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, false);
         long long incl = u * p.Hkv;
@@ -210,8 +232,9 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
         const long long at = base + incl - u * p.Hkv;
         if (lo >= at && lo < at + u * p.Hkv && hi > lo) {
             outi[0] = b0 + threadIdx.x;
-            outi[1] = (int)((lo - at) / u);
-            out[3] = (lo - at) % u;
+            const long long h = pf_div64(lo - at, u);
+            outi[1] = (int)h;
+            out[3] = lo - at - h * u;
         }
     }
     __syncthreads();
@@ -221,8 +244,9 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
         const PfSeq s = pf_sequence<C::B>(p, outi[0], &bad);
         long long off = out[3];
         int i = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < s.tiles; i0 += 32) {
-            const int c = i0 + lane < s.tiles ? kPairUnits + pf_key_tiles(s, i0 + lane, p.G) : 0;
+            const int c = i0 + lane < s.tiles ? kPairUnits + pf_key_tiles(p, s, i0 + lane) : 0;
             long long incl = c;
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) {
@@ -257,18 +281,23 @@ __device__ __forceinline__ void pf_walk_begin(const PrefillParams& p, const unsi
     w.s = pf_sequence<C::B>(p, w.b, &bad);
 }
 
+// The next piece with work; kvt: the pair's key tiles, gpos: the global unit of
+// its first one.
 template <typename C>
-__device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, PfPiece& pc) {
+__device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, PfPiece& pc,
+                                             int& kvt, long long& gpos) {
     while (w.left > 0) {
-        const int kvt = pf_key_tiles(w.s, w.i, p.G);
+        kvt = pf_key_tiles(p, w.s, w.i);
         const long long c = kPairUnits + kvt;
         const long long take = min(c - w.off, w.left);
         const int u0 = (int)max(w.off - kPairUnits, 0LL), u1 = (int)(w.off + take - kPairUnits);
-        pc.b = w.b, pc.kvh = w.kvh, pc.i = w.i, pc.kt0 = u0, pc.kt1 = u1, pc.kvt = kvt;
-        pc.s = w.s, pc.gpos = w.gpos + kPairUnits, pc.whole = u0 == 0 && u1 == kvt;
-        pc.first = w.count == 0;
-        pc.row0 = 256 * w.i;
-        pc.nj = w.s.rows - pc.row0 > 128 ? 2 : 1;
+        gpos = w.gpos + kPairUnits;
+        pc.kvh = w.kvh, pc.kt0 = u0, pc.kt1 = u1;
+        pc.row0 = 256 * w.i, pc.rows = w.s.rows, pc.start = w.s.start;
+        pc.nj = pc.rows - pc.row0 > 128 ? 2 : 1;
+        pc.first_pos = w.s.first_pos, pc.n = w.s.n, pc.b = w.b;
+        pc.pair_pos = pc.first_pos + pf_div(p, pc.row0);
+        pc.flags = (u0 == 0 && u1 == kvt ? 1 : 0) | (w.count == 0 ? 2 : 0);
         w.left -= take;
         if (w.off + take == c) {  // on to the next pair
             w.off = 0, w.gpos += c;
@@ -292,6 +321,7 @@ __device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, 
             return true;
         }
     }
+    pc.nj = 0;
     return false;
 }
 
@@ -363,13 +393,16 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// umma_wait for waits that are on the critical path: the timer and the abort
-// flag are looked at once in 64 tries.
+// umma_wait for waits on the critical path: the timer and the abort flag are
+// looked at once in 64 tries.  pf_wait_call is the same out of line, for the
+// roles that wait in many places (code competes for the instruction cache).
 __device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, volatile int* abort_all,
                                         unsigned* status) {
+#pragma unroll 1
     for (int it = 0; it < 64; ++it)
         if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
+#pragma unroll 1
     for (uint32_t it = 0; it < (1u << 30); ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63) != 63) continue;
@@ -380,6 +413,10 @@ __device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, volatile 
     atomicOr(status, kStatusTimeout);
     return false;
 }
+__device__ __noinline__ bool pf_wait_call(uint32_t bar, uint32_t parity, volatile int* abort_all,
+                                          unsigned* status) {
+    return pf_wait(bar, parity, abort_all, status);
+}
 
 // 32 bytes to a 32-byte aligned address.
 __device__ __forceinline__ void store32(void* at, const uint32_t (&v)[8]) {
@@ -388,36 +425,23 @@ __device__ __forceinline__ void store32(void* at, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// Barrier over the 128 threads of softmax group 0 with an OR of `v`.
-__device__ __forceinline__ bool wg0_or(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
-
-// Bit 15 or 31 set where a bf16 of the word is infinite or NaN (its exponent,
-// all ones, carries into the sign's place).
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
-    return (w & 0x7f807f80u) + 0x00800080u;
-}
-
-// One row's part of a key tile: reads S (128 columns at s_col), lets `raise`
-// settle the row's reference point m (false: stop), and writes P over S's first
-// 64 columns, its sum added to l2.  With `masked`, only the keys whose bits are
-// set in vis (32 to a word) have weight: the others' scores become -inf and
-// their weights 0 (qs > 0, and m is never -inf).
+// One row's part of a key tile: reads S (128 columns at s_col), writes P over
+// S's first 64 columns and adds its sum to l2; ready(k) follows the first two
+// quarters of P (k = 0), the third (1) and the last (2).  The first quarters'
+// exponentials are taken at the reference point m as it stands, under the
+// search for the tile's maximum; raise(max) settles m, and where it had to move
+// (true) they are taken again.  With `masked`, only the keys whose bits are set
+// in vis (32 to a word) have weight: the others' scores become -inf and their
+// weights 0 (qs > 0, and m is never -inf).  False: stop.
 template <typename Raise, typename Ready>
 __device__ __forceinline__ bool pf_softmax_tile(uint32_t s_col, float qs, bool masked,
-                                                const uint32_t (&vis)[4], float& m, float2& l2,
+                                                const uint32_t (&vis)[4], const float& m, float2& l2,
                                                 Raise raise, Ready ready) {
     float x[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x[c]);
+    tmem_ld32(s_col, x[0]);
+    tmem_ld32(s_col + 32, x[1]);
+    tmem_ld32(s_col + 64, x[2]);
+    tmem_ld32(s_col + 96, x[3]);
     tmem_wait_ld();
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_loaded32(x[c]);
@@ -428,6 +452,19 @@ __device__ __forceinline__ bool pf_softmax_tile(uint32_t s_col, float qs, bool m
             for (int k = 0; k < 32; ++k)
                 if (!((vis[c] >> k) & 1u)) x[c][k] = -INFINITY;
     }
+    const float2 qq = make_float2(qs, qs);
+    float2 sum = make_float2(0.f, 0.f), mm = make_float2(-m, -m);
+    auto quarter = [&](int c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), qq, mm);
+            const float2 pv = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+            sum = add2(sum, pv);
+            pk[k] = pack_bf16x2(pv.x, pv.y);
+        }
+        tmem_st16(s_col + 16 * c, pk);
+    };
     float a[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -437,23 +474,29 @@ __device__ __forceinline__ bool pf_softmax_tile(uint32_t s_col, float qs, bool m
     }
     const float mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])),
                            fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
-    // (no key seen: the finite floor)
-    if (!raise(fmaxf(mx * qs, -FLT_MAX))) return false;
-    const float2 qq = make_float2(qs, qs), mm = make_float2(-m, -m);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float2 e = fma2(make_float2(x[c][2 * k], x[c][2 * k + 1]), qq, mm);
-            const float2 pv = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-            l2 = add2(l2, pv);
-            pk[k] = pack_bf16x2(pv.x, pv.y);
-        }
-        tmem_st16(s_col + 16 * c, pk);
-        if (c & 1) ready(c >> 1);
+#pragma unroll 1
+    for (bool again = true; again;) {
+        quarter(0);
+        quarter(1);
+        // (no key seen: the finite floor)
+        const int moved = raise(fmaxf(mx * qs, -FLT_MAX));
+        if (moved < 0) return false;
+        again = moved > 0;
+        if (again) sum = make_float2(0.f, 0.f), mm = make_float2(-m, -m);
     }
+    ready(0);
+    quarter(2);
+    ready(1);
+    quarter(3);
+    ready(2);
+    l2 = add2(l2, sum);
     return true;
+}
+
+// Whether tile kt of a piece reaches past the pair's first row: its V holds
+// values that some row must not see, and is looked over before use.
+__device__ __forceinline__ bool pf_unclean(const PfPiece& pc, int kt) {
+    return 128 * (kt + 1) - 1 > pc.pair_pos;
 }
 
 // What a column's remembered values (first positions of a NaN, +inf, -inf) add
@@ -470,27 +513,32 @@ __global__ void __launch_bounds__(384, 1)
                            const __grid_constant__ CUtensorMap tmq) {
     pdl_trigger();
     using C = PrefillCfg<D, B>;
-    extern __shared__ unsigned char smem_raw[];
-    const uint32_t raw_addr = smem_addr(smem_raw);
-    const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
-    unsigned char* smem = smem_raw + (sbase - raw_addr);
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sbase = smem_addr(smem);
+    if (sbase & 1023u) {  // (the swizzled tiles need it; there is no other shared memory)
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
     unsigned char* ctrl = smem + C::OFF_CTRL;
     const uint32_t bar0 = sbase + C::OFF_CTRL;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + C::TMEM_SLOT);
     volatile int* abort_all = reinterpret_cast<volatile int*>(ctrl + C::ABORT);
+    PfPiece* pieces = reinterpret_cast<PfPiece*>(ctrl + C::PIECES);
     volatile int* mark_piece = reinterpret_cast<volatile int*>(ctrl + C::MARK_PIECE);
-    volatile int* wg1_done = reinterpret_cast<volatile int*>(ctrl + C::WG1_DONE);
+    volatile int* done = reinterpret_cast<volatile int*>(ctrl + C::DONE);  // pieces, per softmax group
     volatile int* box_bits = reinterpret_cast<volatile int*>(ctrl + C::BITS);
     int* marks = reinterpret_cast<int*>(ctrl + C::MARKS);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < C::NBAR; ++i) {
-            const bool p_full = i >= C::P_FULL && i < C::P_FULL + 4;  // (and P_HALF)
-            mbar_init(bar0 + 8 * i, p_full ? 4 : 1);
+            const bool p_full = i >= C::P_FULL && i < C::P_FULL + 6;
+            const bool pc_empty = i >= C::PC_EMPTY && i < C::PC_EMPTY + C::NP;
+            mbar_init(bar0 + 8 * i, p_full ? 4 : pc_empty ? 11 : 1);
         }
-        *abort_all = 0, *mark_piece = -1, *wg1_done = 0;
+        *abort_all = 0, *mark_piece = -1, done[0] = 0, done[1] = 0;
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
@@ -508,12 +556,25 @@ __global__ void __launch_bounds__(384, 1)
     auto wait = [&](int bar, uint32_t parity) {
         return pf_wait(bar0 + 8 * bar, parity, abort_all, p.status);
     };
-    PfWalk w;
-    pf_walk_begin<C>(p, ctrl, w);
     PfPiece pc;
+    int np = 0;  // pieces so far (every warp's own count)
 
     if (warp < 4) {
         regs_dec<104>();
+        auto wait = [&](int bar, uint32_t parity) {
+            const uint32_t at = bar0 + 8 * bar;
+            return mbar_try_wait(at, parity) || pf_wait_call(at, parity, abort_all, p.status);
+        };
+        // the next piece, by the whole warp
+        auto next_piece = [&] {
+            const int slot = np % C::NP;
+            if (!__all_sync(kFullMask, wait(C::PC_FULL + slot, (np / C::NP) & 1))) return false;
+            pc = pieces[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar0 + 8 * (C::PC_EMPTY + slot));
+            ++np;
+            return pc.nj > 0;
+        };
         if (warp == 0 || warp == 3) {
             // ====================================== K tiles (warp 0), V tiles (warp 3)
             const int kv = warp == 0 ? 0 : 1;
@@ -524,27 +585,49 @@ __global__ void __launch_bounds__(384, 1)
             const uint64_t pol = l2_policy_evict_normal();
             if (kv == 0 && lane == 0 && p.cut != nullptr)
                 p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);  // (no cut pair yet)
-            while (!aborted && pf_walk_next<C>(p, w, pc)) {
-                if (kv == 0 && lane == 0 && p.cut != nullptr && !pc.whole && pc.kt0 == 0) {
-                    // this CTA holds the first part of a pair that others go on with
-                    const long long T = *reinterpret_cast<const long long*>(ctrl + C::SCHED);
-                    const long long last = (pc.gpos + pc.kvt - 1) * min((long long)gridDim.x, T) / T;
-                    p.cut[2 * blockIdx.x] = make_int4(pc.b, pc.kvh, pc.i, pc.s.start);
-                    p.cut[2 * blockIdx.x + 1] =
-                        make_int4((int)(last - blockIdx.x) + 1, pc.first ? 0 : 1, pc.s.rows, 0);
+            PfWalk w;
+            if (kv == 0) pf_walk_begin<C>(p, ctrl, w);
+            while (!aborted) {
+                if (kv == 0) {
+                    int kvt;
+                    long long gpos;
+                    const bool more = pf_walk_next<C>(p, w, pc, kvt, gpos);
+                    const int slot = np % C::NP;
+                    if (np >= C::NP &&
+                        !__all_sync(kFullMask, wait(C::PC_EMPTY + slot, (np / C::NP - 1) & 1)))
+                        break;
+                    ++np;
+                    if (lane == 0) {
+                        pieces[slot] = pc;
+                        mbar_arrive(bar0 + 8 * (C::PC_FULL + slot));
+                        if (more && p.cut != nullptr && !pc.whole() && pc.kt0 == 0) {
+                            // this CTA holds the first part of a pair that others go on with
+                            const long long T = *reinterpret_cast<const long long*>(ctrl + C::SCHED);
+                            const long long last =
+                                pf_div64((gpos + kvt - 1) * min((long long)gridDim.x, T), T);
+                            p.cut[2 * blockIdx.x] = make_int4(pc.b, pc.kvh, pc.row0, pc.start);
+                            p.cut[2 * blockIdx.x + 1] =
+                                make_int4((int)(last - blockIdx.x) + 1, pc.first() ? 0 : 1, pc.rows, 0);
+                        }
+                    }
+                    __syncwarp();
+                    if (!more) break;
+                } else if (!next_piece()) {
+                    break;
                 }
                 auto box_block = [&](int kt) {
                     const int tok = kt * C::TT + 16 * lane;
-                    return (kt < pc.kt1 && lane < 8 && tok < pc.s.n)
+                    return (kt < pc.kt1 && lane < 8 && tok < pc.n)
                                ? ld_dep(p.bt + (long long)pc.b * p.maxb + tok / B)
                                : -1;
                 };
                 int blk_next = box_block(pc.kt0);
+#pragma unroll 1
                 for (int kt = pc.kt0; kt < pc.kt1; ++kt, seq += 2) {
                     const int tok = kt * C::TT + 16 * lane;
                     const int blk = blk_next;
                     blk_next = box_block(kt + 1);
-                    const bool inside = lane < 8 && tok < pc.s.n;
+                    const bool inside = lane < 8 && tok < pc.n;
                     const bool valid = inside && blk >= 0 && blk < p.num_blocks;
                     const unsigned vmask = __ballot_sync(kFullMask, valid);
                     if (kv && inside && !valid) atomicOr(p.status, kStatusBadBlock);
@@ -556,6 +639,17 @@ __global__ void __launch_bounds__(384, 1)
                         break;
                     }
                     __syncwarp();
+                    if (kv && vmask != 0xffu) {  // missing boxes of V are zero: 0 * stale is not
+#pragma unroll 1
+                        for (int x = lane; x < 8 * 128 * C::NH; x += 32) {
+                            const int box = (x >> 7) & 7;
+                            if (!((vmask >> box) & 1u))
+                                *reinterpret_cast<uint4*>(smem + stage * C::TILE + (x >> 10) * C::HALF +
+                                                          (x & 1023) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                     // (one thread issues all boxes: eight lanes taking turns at it
                     // cost the warp several times the instructions)
                     if (elect_one()) {
@@ -597,7 +691,7 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t dK = umma_desc_sw128(sbase, 0, 1024);
                 const uint64_t dV = umma_desc_sw128(sbase, C::HALF, 1024);
                 const uint64_t dQ = umma_desc_sw128(sbase + C::OFF_Q, 0, 1024);
-                int seq = 0, np[2] = {0, 0}, nqj[2] = {0, 0};
+                int seq = 0, npj[2] = {0, 0}, nqj[2] = {0, 0}, nclean = 0;
                 bool ok = true;
                 auto stage_full = [&](int s) { return wait(C::KV_FULL + s % C::NS, (s / C::NS) & 1); };
                 auto score = [&](int j, int s) {  // S_j = Q_j K^T, K in stage s
@@ -610,44 +704,60 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     umma_commit(bar0 + 8 * (C::S_FULL + j));
                 };
-                while (ok && pf_walk_next<C>(p, w, pc)) {
+                while (ok) {
+                    const int slot = np % C::NP;
+                    if (!(ok = wait(C::PC_FULL + slot, (np / C::NP) & 1))) break;
+                    pc = pieces[slot];
+                    mbar_arrive(bar0 + 8 * (C::PC_EMPTY + slot));
+                    ++np;
+                    if (pc.nj == 0) break;
                     const int nk = pc.kt1 - pc.kt0;
+#pragma unroll 1
                     for (int j = 0; j < pc.nj && ok; ++j) {
                         ok = wait(C::Q_FULL + j, nqj[j] & 1);
                         ++nqj[j];
                     }
                     if (!ok || !(ok = stage_full(seq))) break;
                     tc_fence_after();
+                    if (pf_unclean(pc, pc.kt0)) mbar_arrive(bar0 + 8 * C::V_LOOK);
+#pragma unroll 1
                     for (int j = 0; j < pc.nj; ++j) {
                         score(j, seq);
                         if (nk == 1) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
                     }
                     umma_commit(bar0 + 8 * (C::KV_EMPTY + seq % C::NS));
+#pragma unroll 1
                     for (int i = 0; i < nk && ok; ++i, seq += 2) {
                         const uint64_t v = dV + (uint64_t)((((seq + 1) % C::NS) * C::TILE) >> 4);
+#pragma unroll 1
                         for (int j = 0; j < pc.nj && ok; ++j) {
-                            // the first half of the keys while the exponentials of
-                            // the second are still under way
-                            ok = wait(C::P_HALF + j, np[j] & 1) && (j > 0 || stage_full(seq + 1));
+                            // by the parts of P as they come: the exponentials of
+                            // the rest are still under way
+                            if (j == 0) {
+                                ok = stage_full(seq + 1);
+                                if (ok && pf_unclean(pc, pc.kt0 + i))
+                                    ok = wait(C::V_CLEAN, nclean++ & 1);
+                            }
+#pragma unroll
+                            for (int part = 0; part < 3; ++part) {
+                                if (!ok || !(ok = wait(C::P_FULL + 2 * part + j, npj[j] & 1))) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int k = part ? 2 + 2 * part : 0; k < 4 + 2 * part; ++k)
+                                    umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
+                                                 v + (uint64_t)(k * (2048 >> 4)), IDV,
+                                                 (i > 0 || k > 0) ? 1u : 0u);
+                            }
                             if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
-                                             v + (uint64_t)(k * (2048 >> 4)), IDV,
-                                             (i > 0 || k > 0) ? 1u : 0u);
-                            if (!(ok = wait(C::P_FULL + j, np[j] & 1))) break;
-                            ++np[j];
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 4; k < 8; ++k)
-                                umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
-                                             v + (uint64_t)(k * (2048 >> 4)), IDV, 1u);
+                            ++npj[j];
                             umma_commit(bar0 + 8 * (C::PV_DONE + j));
                             if (j == pc.nj - 1)
                                 umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 1) % C::NS));
                             if (i + 1 < nk) {
-                                if (j == 0 && !(ok = stage_full(seq + 2))) break;
+                                if (j == 0) {
+                                    if (!(ok = stage_full(seq + 2))) break;
+                                    if (pf_unclean(pc, pc.kt0 + i + 1)) mbar_arrive(bar0 + 8 * C::V_LOOK);
+                                }
                                 tc_fence_after();
                                 score(j, seq + 2);
                                 if (i + 2 == nk) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
@@ -672,10 +782,11 @@ __global__ void __launch_bounds__(384, 1)
             constexpr int RPI = 32 / CPR;            // rows per pass
             const int c = lane % CPR;
             const bool boxes = 128 % p.G == 0;
-            int nqj[2] = {0, 0};
+            int nqj[2] = {0, 0}, vseq = 1, nlook = 0, piece = 0, mark_at = -1;
             bool ok = true;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-            while (ok && pf_walk_next<C>(p, w, pc)) {
+            while (ok && next_piece()) {
+#pragma unroll 1
                 for (int j = 0; j < pc.nj && ok; ++j) {
                     if (nqj[j] > 0)
                         ok = __all_sync(kFullMask, wait(C::Q_EMPTY + j, (nqj[j] - 1) & 1));
@@ -689,24 +800,25 @@ __global__ void __launch_bounds__(384, 1)
                             mbar_arrive_expect_tx(fb, (uint32_t)C::TILE);
                             for (int h = 0; h < C::NH; ++h)
                                 tma_load_3d(tile + h * C::HALF, &tmq, fb, 64 * h, pc.kvh * p.G,
-                                            pc.s.start + f0 / p.G);
+                                            pc.start + pf_div(p, f0));
                         }
                         __syncwarp();
                         continue;
                     }
                     const uint32_t dst = tile + (c >> 3) * C::HALF;
-                    int tok = (f0 + lane / CPR) / p.G, g = (f0 + lane / CPR) - tok * p.G;
+                    int tok = pf_div(p, f0 + lane / CPR), g = (f0 + lane / CPR) - tok * p.G;
 #pragma unroll 4
                     for (int r = lane / CPR; r < 128; r += RPI) {
-                        const bool live = f0 + r < pc.s.rows;
+                        const bool live = f0 + r < pc.rows;
                         cp_async16(dst + sw128(r, c),
-                                   live ? q + ((long long)(pc.s.start + tok) * p.H + pc.kvh * p.G + g) * D + 8 * c
+                                   live ? q + ((long long)(pc.start + tok) * p.H + pc.kvh * p.G + g) * D + 8 * c
                                         : q,
                                    live);
                         for (g += RPI; g >= p.G; g -= p.G) ++tok;
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     if (p.qscale < 0.f) {  // S = -Q K^T, and the softmax scales by |scale|
+#pragma unroll 1
                         for (int r = lane / CPR; r < 128; r += RPI) {
                             uint4* at = reinterpret_cast<uint4*>(smem + C::OFF_Q + j * C::TILE +
                                                                  (c >> 3) * C::HALF + sw128(r, c));
@@ -718,6 +830,79 @@ __global__ void __launch_bounds__(384, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(fb);
+                }
+                // V of the piece's last tiles: rows past the context are zeroed,
+                // values that are not finite zeroed and remembered
+                ++piece;
+#pragma unroll 1
+                for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt, vseq += 2) {
+                    if (!pf_unclean(pc, kt)) continue;
+                    const int t0 = kt * C::TT, stage = vseq % C::NS;
+                    // (not before the tile's S is issued: a wait may be no more than
+                    // one phase ahead of its barrier)
+                    ok = __all_sync(kFullMask, wait(C::V_LOOK, nlook++ & 1) &&
+                                                   wait(C::KV_FULL + stage, (vseq / C::NS) & 1));
+                    if (!ok) break;
+                    uint32_t odd = 0;
+#pragma unroll 1
+                    for (int r = lane; r < 128; r += 32) {
+                        unsigned char* vrow = smem + stage * C::TILE + r * 128;
+                        if (t0 + r <= pc.pair_pos) continue;
+                        // 0 * x summed up is NaN as soon as one x is not finite
+                        __nv_bfloat162 z[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) z[k] = __floats2bfloat162_rn(0.f, 0.f);
+                        const __nv_bfloat162 zero = z[0];
+#pragma unroll
+                        for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                uint4* at = reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
+                                if (t0 + r >= pc.n) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    const uint4 v = *at;
+                                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        z[e] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]), zero, z[e]);
+                                }
+                            }
+                        const float2 f = __bfloat1622float2(__hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3])));
+                        if (f.x + f.y != 0.f) odd |= 1u << (r >> 5);
+                    }
+                    if (__any_sync(kFullMask, odd != 0)) {
+                        if (mark_at != piece) {
+                            // (the softmax warps may still be reading the last marks)
+#pragma unroll 1
+                            for (int n = 0; (done[0] < piece - 1 || done[1] < piece - 1) && !*abort_all &&
+                                            n < (1 << 24); ++n)
+                                __nanosleep(100);
+#pragma unroll 1
+                            for (int k = lane; k < 3 * D; k += 32) marks[k] = INT_MAX;
+                            mark_at = piece;
+                            if (lane == 0) *mark_piece = piece;
+                            __syncwarp();
+                        }
+#pragma unroll 1
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            if (!((odd >> q4) & 1u)) continue;
+                            const int r = 32 * q4 + lane;
+#pragma unroll 1
+                            for (int x = 0; x < 64 * C::NH; ++x) {
+                                __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(
+                                    smem + stage * C::TILE + r * 128 + (x >> 6) * C::HALF) + (x & 63);
+                                const float v = __bfloat162float(*at);
+                                if (isfinite(v)) continue;
+                                const int d = (x & ~63) + ((((x >> 3) & 7) ^ (r & 7)) << 3) + (x & 7);
+                                atomicMin(marks + (v != v ? 0 : v > 0.f ? D : 2 * D) + d, t0 + r);
+                                *at = __float2bfloat16(0.f);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar0 + 8 * C::V_CLEAN);
                 }
             }
             if (*abort_all && lane == 0)  // copies in flight land before the CTA can exit
@@ -739,21 +924,28 @@ __global__ void __launch_bounds__(384, 1)
         int seq = 0, ns = 0;                       // V stage; tiles of this row tile so far
         int piece = 0;
         bool ok = true;
-        while (ok && pf_walk_next<C>(p, w, pc)) {
+        while (ok) {
+            const int slot = np % C::NP;
+            if (!(ok = __all_sync(kFullMask, wait(C::PC_FULL + slot, (np / C::NP) & 1)))) break;
+            pc = pieces[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar0 + 8 * (C::PC_EMPTY + slot));
+            ++np;
+            if (pc.nj == 0) break;
             ++piece;
             const int nk = pc.kt1 - pc.kt0;
             if (j >= pc.nj) {
                 seq += 2 * nk;
-                if (r == 0) *wg1_done = piece;
+                if (r == 0) done[j] = piece;
                 continue;
             }
             const int f = pc.row0 + 128 * j + r;
-            const bool live = f < pc.s.rows;
-            const int tok = f / p.G;
-            const int pos = live ? pc.s.first_pos + tok : -1;
-            const int pair_pos = pc.s.first_pos + pc.row0 / p.G;   // the pair's first row's
+            const bool live = f < pc.rows;
+            const int tok = pf_div(p, f);
+            const int pos = live ? pc.first_pos + tok : -1;
             float m = -FLT_MAX;   // reference point of the exponentials (scaled, base 2)
             float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll 1
             for (int i = 0; i < nk; ++i, seq += 2, ++ns) {
                 const int t0 = (pc.kt0 + i) * C::TT;
                 const int vstage = (seq + 1) % C::NS;
@@ -763,69 +955,25 @@ __global__ void __launch_bounds__(384, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const unsigned bits = (unsigned)box_bits[vstage] & 0xffu;
-                // V's rows that some row of the pair must not see
-                if (j == 0 && (bits != 0xffu || t0 + C::TT - 1 > pair_pos)) {
-                    unsigned char* vrow = smem + vstage * C::TILE + r * 128;
-                    const bool in = t0 + r < pc.s.n && ((bits >> (r >> 4)) & 1u);
-                    uint32_t odd = 0;
-                    if (!in || t0 + r > pair_pos) {
-#pragma unroll
-                        for (int h = 0; h < C::NH; ++h)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                uint4* at = reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
-                                if (!in) {
-                                    *at = make_uint4(0, 0, 0, 0);
-                                } else {
-                                    const uint4 v = *at;
-                                    odd |= (nonfinite2(v.x) | nonfinite2(v.y)) |
-                                           (nonfinite2(v.z) | nonfinite2(v.w));
-                                }
-                            }
-                    }
-                    const bool found = (odd & 0x80008000u) != 0;
-                    if (wg0_or(found)) {
-                        if (*mark_piece != piece) {
-                            // group 1 may still be reading the marks of its last piece
-                            for (int n = 0; *wg1_done < piece - 1 && !*abort_all && n < (1 << 24); ++n)
-                                __nanosleep(100);
-                            wg0_or(false);   // (all have read mark_piece)
-                            for (int k = r; k < 3 * D; k += 128) marks[k] = INT_MAX;
-                            *mark_piece = piece;
-                            wg0_or(false);
-                        }
-                        if (found) {
-                            for (int h = 0; h < C::NH; ++h)
-                                for (int k = 0; k < 8; ++k) {
-                                    __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(
-                                        vrow + h * C::HALF + k * 16);
-                                    for (int e = 0; e < 8; ++e) {
-                                        const float v = __bfloat162float(at[e]);
-                                        if (isfinite(v)) continue;
-                                        const int d = h * 64 + (k ^ (r & 7)) * 8 + e;
-                                        atomicMin(marks + (v != v ? 0 : v > 0.f ? D : 2 * D) + d, t0 + r);
-                                        at[e] = __float2bfloat16(0.f);
-                                    }
-                                }
-                        }
-                    }
-                    fence_proxy_async_smem();
-                }
                 // keys 0 .. lim of the tile are the row's, in pages that are there
                 const int lim = pos - t0;
                 const bool masked = __any_sync(kFullMask, lim < 127) || bits != 0xffu;
-                // O's scale-down, should the tile raise the row's reference point
+                // settles the row's reference point: 0, it stays; 1, raised, the
+                // sum and O scaled down; -1, stop
+                bool settled = false;
                 auto raise = [&](float mt) {
+                    if (settled) return 0;
+                    settled = true;
                     if (i == 0) {
                         m = mt;
-                        return true;
+                        return 1;
                     }
-                    if (!__any_sync(kFullMask, mt > m + 8.f)) return true;
+                    if (!__any_sync(kFullMask, mt > m + 8.f)) return 0;
                     const bool up = mt > m + 8.f;
                     const float alpha = up ? ex2_approx(m - mt) : 1.f;
                     if (up) m = mt;
                     l2.x *= alpha, l2.y *= alpha;
-                    if (!__all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1))) return false;
+                    if (!__all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1))) return -1;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -839,7 +987,7 @@ __global__ void __launch_bounds__(384, 1)
                         }
                         tmem_st16(o_col + c, o);
                     }
-                    return true;
+                    return 1;
                 };
                 uint32_t vis[4];
 #pragma unroll
@@ -849,11 +997,11 @@ __global__ void __launch_bounds__(384, 1)
                              (((bits >> (2 * c)) & 1u ? 0xffffu : 0u) |
                               ((bits >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
                 }
-                auto ready = [&](int half) {
+                auto ready = [&](int k) {
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar0 + 8 * ((half ? C::P_FULL : C::P_HALF) + j));
+                    if (lane == 0) mbar_arrive(bar0 + 8 * (C::P_FULL + 2 * k + j));
                 };
                 ok = pf_softmax_tile(s_col, qs, masked, vis, m, l2, raise, ready);
                 if (!ok) break;
@@ -864,12 +1012,11 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             tc_fence_after();
             const float l = l2.x + l2.y;
-            const bool marked = *mark_piece == piece;
-            const float inv = pc.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const float inv = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
             const long long orow =
-                live ? (long long)(pc.s.start + tok) * p.H + pc.kvh * p.G + (f - tok * p.G) : 0;
-            const long long slot = ((long long)blockIdx.x * 2 + (pc.first ? 0 : 1)) * C::ROWS + 128 * j + r;
-#pragma unroll
+                live ? (long long)(pc.start + tok) * p.H + pc.kvh * p.G + (f - tok * p.G) : 0;
+            const long long part = ((long long)blockIdx.x * 2 + (pc.first() ? 0 : 1)) * C::ROWS + 128 * j + r;
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(o_col + c, o);
@@ -877,12 +1024,7 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_loaded32(o);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] *= inv;
-                if (marked) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] += poison(marks, D, c + k, pos);
-                }
-                if (!live) continue;
-                if (pc.whole) {
+                if (live && pc.whole()) {
                     // (whole sectors per thread: the rows of a warp lie apart)
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D + c;
 #pragma unroll
@@ -898,8 +1040,8 @@ __global__ void __launch_bounds__(384, 1)
                             reinterpret_cast<uint4*>(out)[2 * h + 1] = make_uint4(v[4], v[5], v[6], v[7]);
                         }
                     }
-                } else {
-                    float* out = p.part_o + slot * D + c;
+                } else if (live) {
+                    float* out = p.part_o + part * D + c;
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t v[8];
@@ -908,12 +1050,26 @@ __global__ void __launch_bounds__(384, 1)
                         store32(out + 8 * h, v);
                     }
                 }
+                __syncwarp();  // (tcgen05.ld wants the warp together)
             }
-            if (!pc.whole && live) p.part_ml[2 * slot] = m, p.part_ml[2 * slot + 1] = l;
-            if (j == 1) {
+            if (live && *mark_piece == piece) {
+                // values that are not finite, into the rows that see them
+#pragma unroll 1
+                for (int d = 0; d < D; ++d) {
+                    const float v = poison(marks, D, d, pos);
+                    if (v == 0.f) continue;
+                    if (pc.whole())
+                        static_cast<__nv_bfloat16*>(p.out)[orow * D + d] = __float2bfloat16(v);
+                    else
+                        p.part_o[part * D + d] = v;
+                }
+            }
+            if (!pc.whole() && live) p.part_ml[2 * part] = m, p.part_ml[2 * part + 1] = l;
+            if (j == 0)  // (all have read the marks)
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            else
                 asm volatile("bar.sync 2, 128;" ::: "memory");
-                if (r == 0) *wg1_done = piece;
-            }
+            if (r == 0) done[j] = piece;
         }
         if (!ok) *abort_all = 1;
     }
@@ -933,7 +1089,7 @@ __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const Prefill
     const int4 e = ld_dep(p.cut + 2 * blockIdx.x + 1);
     const int pieces = e.x;
     if (pieces <= 1) return;
-    const int row0 = 256 * a.z;
+    const int row0 = a.z;
     constexpr int V = D / 32;
     for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 256; r += gridDim.y * 8) {
         const int f = row0 + r;
@@ -959,7 +1115,7 @@ __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const Prefill
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int tok = f / p.G;
+        const int tok = pf_div(p, f);
         const long long orow = (long long)(a.w + tok) * p.H + a.y * p.G + (f - tok * p.G);
         uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + lane * V);
 #pragma unroll
