@@ -169,23 +169,40 @@ def _check(rc: int, func: str) -> None:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    dp = getattr(x, "data_ptr", None)
-    if dp is not None:
-        return dp()
-    raise TypeError(f"cannot pass {type(x).__name__} as a pointer")
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+        raise TypeError(f"cannot pass {type(x).__name__} as a pointer") from None
+
+
+_raw_stream = None  # the raw handle of torch's current stream on the current device
+
+
+def _find_raw_stream():
+    """torch.cuda.current_stream() builds a Stream object (about 3 us, as long as a
+    small launch takes); the raw getter behind it does not."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if not torch.cuda.is_available():
+        return lambda: None
+    torch.cuda.init()
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
-        import torch
-
-        if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream
-        return None
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

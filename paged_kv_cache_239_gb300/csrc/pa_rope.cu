@@ -32,7 +32,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 64;
 
 template <typename T>
 struct Chunk;  // 16 bytes of a row as floats
@@ -91,13 +91,32 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
     constexpr int E = C::E;
     constexpr int LPR = D / E;       // lanes per row
     constexpr int RPW = 32 / LPR;    // rows per warp and pass
+    constexpr int U = 4;             // passes in flight
     const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    const int t = (int)(w / p.splits);
-    const int split = (int)(w % p.splits);
+    const unsigned w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(w / (unsigned)p.splits);
+    const int split = (int)(w % (unsigned)p.splits);
     if (t >= p.num_tokens) return;
     const int c = lane % LPR;        // this lane's chunk of its row
     const int sub = lane / LPR;
+    const int rows = p.H + 2 * p.Hkv;
+    const int step = p.splits * RPW;
+
+    // This lane's chunk of row r (queries, keys, values in that order).
+    auto load = [&](int r) {
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.Hkv;
+        const T* src = is_q ? static_cast<const T*>(p.q) + (long long)t * p.q_stride + (long long)r * D
+                       : is_k ? static_cast<const T*>(p.k) + (long long)t * p.k_stride +
+                                    (long long)(r - p.H) * D
+                              : static_cast<const T*>(p.v) + (long long)t * p.v_stride +
+                                    (long long)(r - p.H - p.Hkv) * D;
+        return ld_dep(reinterpret_cast<const uint4*>(src) + c);
+    };
+    // the first rows are on their way while the token's place is looked up
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = load(split * RPW + sub + u * step);
 
     // ---- where the token stands ----
     int b = t, s0 = t, n_new = 1;
@@ -117,6 +136,13 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
         if (split == 0 && lane == 0) atomicOr(p.status, kStatusBadBlock);
         blk = -1;
     }
+    const long long slot = (long long)blk * p.s_blk + p.tile_off + (long long)(pos % p.B) * D;
+    const bool norm = p.q_weight != nullptr;
+    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+    if (norm) {
+        wq = ld_dep(static_cast<const uint4*>(p.q_weight) + c);
+        wk = ld_dep(static_cast<const uint4*>(p.k_weight) + c);
+    }
 
     // ---- this lane's sines ----
     constexpr int NF = INTERLEAVED ? E / 2 : E;
@@ -135,61 +161,70 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
     }
     // halves: the partner chunk, and the sign of its sine's term
     const int partner = turns ? (c < rc / 2 ? lane + rc / 2 : lane - rc / 2) : lane;
-    const bool low = c < rc / 2;
+    if (!INTERLEAVED && c < rc / 2) {
+#pragma unroll
+        for (int k = 0; k < NF; ++k) sn[k] = -sn[k];
+    }
 
-    const int rows = p.H + 2 * p.Hkv;
-    for (int r0 = split * RPW; r0 < rows; r0 += p.splits * RPW) {
-        const int r = r0 + sub;
-        const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.Hkv;
-        const bool live = r < rows;
-        const int h = is_q ? r : is_k ? r - p.H : r - p.H - p.Hkv;
-        const T* src = static_cast<const T*>(is_q ? p.q : is_k ? p.k : p.v) +
-                       (long long)t * (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) +
-                       (long long)h * D;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = ld_dep(reinterpret_cast<const uint4*>(src) + c);
-        const T* weight = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
-        float x[E];
-        C::unpack(raw, x);
-        if (p.q_weight != nullptr) {
-            float ss = 0.f;
+    for (int r0 = split * RPW; r0 < rows; r0 += U * step) {
+        uint4 next[U];
 #pragma unroll
-            for (int k = 0; k < E; ++k) ss += x[k] * x[k];
+        for (int u = 0; u < U; ++u) next[u] = load(r0 + sub + (U + u) * step);
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-            const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-            float wv[E];
-            C::unpack(ld_dep(reinterpret_cast<const uint4*>(weight) + c), wv);
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + sub + u * step;
+            if (r0 + u * step >= rows) break;  // (the whole warp)
+            const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.Hkv;
+            float x[E];
+            C::unpack(raw[u], x);
+            if (norm) {
+                float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < E; ++k) x[k] = x[k] * rs * wv[k];
-        }
-        if constexpr (INTERLEAVED) {
-            if (turns) {
+                for (int k = 0; k < E; k += 2) {
+                    const float2 v = make_float2(x[k], x[k + 1]);
+                    s2 = fma2(v, v, s2);
+                }
+                float ss = s2.x + s2.y;
 #pragma unroll
-                for (int k = 0; k < NF; ++k) {
-                    const float a = x[2 * k], d = x[2 * k + 1];
-                    x[2 * k] = a * cs[k] - d * sn[k];
-                    x[2 * k + 1] = a * sn[k] + d * cs[k];
+                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+                const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+                float wv[E];
+                C::unpack(is_q ? wq : wk, wv);
+#pragma unroll
+                for (int k = 0; k < E; k += 2) {
+                    const float2 v = mul2(mul2(make_float2(x[k], x[k + 1]), make_float2(rs, rs)),
+                                          make_float2(wv[k], wv[k + 1]));
+                    x[k] = v.x, x[k + 1] = v.y;
                 }
             }
-        } else {
+            if constexpr (INTERLEAVED) {
+                if (turns) {  // (the rest passes as it is, be it infinite)
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float o = __shfl_sync(kFullMask, x[k], partner);
-                if (turns) x[k] = low ? x[k] * cs[k] - o * sn[k] : o * sn[k] + x[k] * cs[k];
+                    for (int k = 0; k < NF; ++k) {
+                        const float a = x[2 * k], d = x[2 * k + 1];
+                        x[2 * k] = a * cs[k] - d * sn[k];
+                        x[2 * k + 1] = a * sn[k] + d * cs[k];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    const float o = __shfl_sync(kFullMask, x[k], partner);
+                    if (turns) x[k] = x[k] * cs[k] + o * sn[k];
+                }
+            }
+            if (r >= rows) continue;
+            if (is_q) {
+                reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + ((long long)t * p.H + r) * D)[c] =
+                    good ? C::pack(x) : make_uint4(0, 0, 0, 0);
+            } else if (blk >= 0) {
+                const int h = is_k ? r - p.H : r - p.H - p.Hkv;
+                T* dst = static_cast<T*>(is_k ? p.k_base : p.v_base) + slot + (long long)h * p.s_head;
+                reinterpret_cast<uint4*>(dst)[c] = is_k ? C::pack(x) : raw[u];
             }
         }
-        if (!live) continue;
-        if (is_q) {
-            uint4 y = good ? C::pack(x) : make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) +
-                                     ((long long)t * p.H + h) * D)[c] = y;
-        } else if (blk >= 0) {
-            const uint4 y = is_k ? C::pack(x) : raw;
-            T* dst = static_cast<T*>(is_k ? p.k_base : p.v_base) + (long long)blk * p.s_blk +
-                     p.tile_off + (long long)h * p.s_head + (long long)(pos % p.B) * D;
-            reinterpret_cast<uint4*>(dst)[c] = y;
-        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = next[u];
     }
 }
 
@@ -214,7 +249,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p_in, int dtype, int D, int n
     p.splits = (int)splits;
     const long long warps = splits * p.num_tokens;
     const long long grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     if (dtype == 1 && D == 64) return launch_d<__nv_bfloat16, 64>(p, (int)grid, s);
     if (dtype == 1 && D == 128) return launch_d<__nv_bfloat16, 128>(p, (int)grid, s);
     if (dtype == 0 && D == 64) return launch_d<float, 64>(p, (int)grid, s);

@@ -32,6 +32,7 @@ class BlockPool:
         self.num_blocks, self.block_size, self.num_layers = num_blocks, block_size, num_layers
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
         self.dtype = tensor.dtype
+        self._device_index = tensor.get_device()
         self.handle = B.pa_pool_create(tensor, num_blocks, num_layers, num_kv_heads, block_size,
                                        head_dim, tensor.dtype)
 
@@ -164,21 +165,19 @@ class BlockPool:
         tokens; query_starts [batch + 1] says which rows are whose (None: one
         token per sequence).  ``out`` may be q itself when q is contiguous."""
         tokens, num_heads = q.shape[0], q.shape[1]
-        self._check_rows(q, tokens, num_heads, "q")
-        self._check_rows(k, tokens, self.num_kv_heads, "k")
-        self._check_rows(v, tokens, self.num_kv_heads, "v")
-        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                self._check_dense(w, (self.head_dim,), self.dtype, name)
+        q_stride = self._check_rows(q, tokens, num_heads, "q")
+        k_stride = self._check_rows(k, tokens, self.num_kv_heads, "k")
+        v_stride = self._check_rows(v, tokens, self.num_kv_heads, "v")
+        if q_weight is not None:
+            self._check_dense(q_weight, (self.head_dim,), self.dtype, "q_weight")
+        if k_weight is not None:
+            self._check_dense(k_weight, (self.head_dim,), self.dtype, "k_weight")
         batch, maxb = self._check_batch(block_tables, context_lens, query_starts)
         if out is None:
             out = self._empty(q.shape, self.dtype, stream)
         else:
             self._check_dense(out, (tokens, num_heads, self.head_dim), self.dtype, "out")
-        B.pa_norm_rope_write_kv(self.handle, layer, out, q, q.stride(0) if tokens > 1 else
-                                num_heads * self.head_dim, k, k.stride(0) if tokens > 1 else
-                                self.num_kv_heads * self.head_dim, v, v.stride(0) if tokens > 1
-                                else self.num_kv_heads * self.head_dim,
+        B.pa_norm_rope_write_kv(self.handle, layer, out, q, q_stride, k, k_stride, v, v_stride,
                                 None if rope is None else rope.handle, q_weight, k_weight, eps,
                                 block_tables, maxb, context_lens, query_starts, batch, tokens,
                                 num_heads, stream)
@@ -205,9 +204,10 @@ class BlockPool:
             out = self._empty(shape, self.dtype, stream)
         else:
             self._check_dense(out, shape, self.dtype, "out")
-        need = self.prefill_workspace_size(batch, tokens, num_heads, maxb)
-        if need and workspace is None:
-            workspace = self._empty((need,), torch.uint8, stream)
+        if workspace is None:  # (the call checks one that is given)
+            need = self.prefill_workspace_size(batch, tokens, num_heads, maxb)
+            if need:
+                workspace = self._empty((need,), torch.uint8, stream)
         wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         B.pa_prefill_attention(out, q, self.handle, layer, block_tables, maxb, context_lens,
                                query_starts, batch, tokens, num_heads, scale, workspace, wbytes,
@@ -245,7 +245,8 @@ class BlockPool:
         """device_free_blocks for rows that may share pages."""
         batch, maxb = self._check_batch(block_tables, context_lens)
         self._check_pages(stack, shares)
-        self._check_dense(finished, (batch,), (torch.uint8, torch.bool), "finished")
+        self._check_dense(finished, (batch,),
+                          torch.bool if finished.dtype is torch.bool else torch.uint8, "finished")
         B.pa_device_free_shared(self.handle, stack, shares, block_tables, maxb, context_lens,
                                 finished, batch, stream)
 
@@ -291,34 +292,36 @@ class BlockPool:
             return torch.empty(shape, dtype=dtype, device=self.pool.device)
 
     def _check_dense(self, t: torch.Tensor, shape, dtype, name: str) -> None:
-        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, "
-                             f"not {tuple(t.shape)}")
-        if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        if (t.shape == shape and t.dtype is dtype and t.get_device() == self._device_index
+                and t.is_contiguous()):
+            return
+        if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-        if t.device != self.pool.device:
+        if t.get_device() != self._device_index:
             raise ValueError(f"{name} is on {t.device}, the pool on {self.pool.device}")
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, "
+                         f"not {tuple(t.shape)}")
 
-    def _check_rows(self, t: torch.Tensor, tokens: int, heads: int, name: str) -> None:
+    def _check_rows(self, t: torch.Tensor, tokens: int, heads: int, name: str) -> int:
+        """The stride between the tokens of [tokens, heads, head_dim] rows."""
         d = self.head_dim
-        if tuple(t.shape) != (tokens, heads, d) or t.dtype != self.dtype:
+        if t.shape != (tokens, heads, d) or t.dtype is not self.dtype:
             raise ValueError(f"{name} must be {self.dtype} [{tokens}, {heads}, {d}], "
                              f"not {t.dtype} {tuple(t.shape)}")
-        if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        if t.device != self.pool.device:
+        if t.get_device() != self._device_index:
             raise ValueError(f"{name} is on {t.device}, the pool on {self.pool.device}")
+        stride = t.stride()
+        if tokens and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        return stride[0] if tokens > 1 else heads * d
 
     def _check_batch(self, block_tables, context_lens, query_starts=None):
-        batch = context_lens.shape[0]
-        if block_tables.dim() != 2:
-            raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
-        self._check_dense(block_tables, (batch, block_tables.shape[1]), torch.int32,
-                          "block_tables")
+        batch, maxb = block_tables.shape  # (two dimensions, or a ValueError)
+        self._check_dense(block_tables, (batch, maxb), torch.int32, "block_tables")
         self._check_dense(context_lens, (batch,), torch.int32, "context_lens")
         if query_starts is not None:
             self._check_dense(query_starts, (batch + 1,), torch.int32, "query_starts")
-        return batch, block_tables.shape[1]
+        return batch, maxb
 
     def _check_pages(self, stack, shares) -> None:
         self._check_dense(stack, (self.num_blocks + 1,), torch.int32, "stack")

@@ -145,6 +145,25 @@ def test_norm_rope_far_positions(cuda_device):
     check(got, want, R.norm_rope_bound(want, size, torch.float32) + 2.0 ** -22 * size)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_infinities_stay_in_their_pairs(cuda_device, dtype, interleaved):
+    """An infinite element reaches its own pair of its own head, the part that does
+    not turn keeps it to itself, and values are copied whatever they are."""
+    dev, d, block, dt = cuda_device, 64, 16, DT[dtype]
+    cache = BlockPool(2, block, 1, 2, d, tensor=torch.zeros((2, 2, 1, 2, block, d), dtype=dt, device=dev))
+    q, k, v = (randn((1, 2, d), dt, dev, i) for i in range(3))
+    q[0, 0, 3], q[0, 0, 50], v[0, 1, 7] = float("inf"), -float("inf"), float("nan")
+    out = cache.norm_rope_write_kv(0, q, k, v, ints([[1]], dev), ints([3], dev),
+                                   rope=Rope(32, interleaved=interleaved))
+    pair = [2, 3] if interleaved else [3, 19]
+    bad = (~torch.isfinite(out[0])).nonzero().tolist()
+    assert bad == [[0, pair[0]], [0, pair[1]], [0, 50]] and float(out[0, 0, 50]) == -float("inf")
+    assert torch.equal(out[0, :, 32:50], q[0, :, 32:50])
+    assert torch.equal(cache.pool[1, 1, 0, :, 2].nan_to_num(5.0), v[0].nan_to_num(5.0))
+    assert torch.equal(cache.norm_rope_write_kv(0, q, k, v, ints([[1]], dev), ints([3], dev)), q)
+
+
 def test_norm_rope_bad_inputs(cuda_device):
     dev, d, block, dt = cuda_device, 64, 16, torch.bfloat16
     pool_t = torch.zeros((4, 2, 1, 1, block, d), dtype=dt, device=dev)
