@@ -10,6 +10,7 @@
 // Sharing: shares[id] counts the owners of page id beyond the first, so an
 // array of zeros describes a pool in which nothing is shared, and the calls
 // that do not know of sharing keep their meaning.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -112,99 +113,105 @@ pa_copy_blocks_kernel(const PageGeom g, const int* src, const int* dst, const in
 
 // --------------------------------------------------------------------- fork
 
-// Child i takes its parent's table: full pages by reference, the partial last
-// page (if any) as a page of its own from the stack's top, in increasing i.
-__global__ void __launch_bounds__(kPlanThreads) pa_fork_plan_kernel(const ForkParams p) {
-    pdl_trigger();
-    pdl_wait();
-    __shared__ int s_warp[32];
-    __shared__ int s_par[kPlanThreads], s_chi[kPlanThreads], s_len[kPlanThreads], s_new[kPlanThreads];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int height = stack_height(p.stack, p.g.num_blocks, p.g.status);
-    int taken = 0;
-    for (int at = 0; at < p.n; at += kPlanThreads) {
-        const int i = at + threadIdx.x;
-        int need = 0, par = -1, chi = -1, len = 0;
-        if (i < p.n) {
-            par = ld_dep(p.parents + i), chi = ld_dep(p.children + i);
-            if (par < 0 || par >= p.batch || chi < 0 || chi >= p.batch || par == chi) {
-                par = -1;
-                atomicOr(p.g.status, kStatusBadLength);
-            } else {
-                len = ld_dep(p.lens + par);
-                if (len < 0 || len > p.maxb * p.g.B) {
-                    par = -1;
-                    atomicOr(p.g.status, kStatusBadLength);
-                }
-            }
-            need = par >= 0 && len % p.g.B != 0;
-        }
-        int total = 0;
-        const int r = taken + cta_exclusive_scan(need, s_warp, total);
-        int id = -1;
-        if (need) {
-            if (r < height)
-                id = ld_dep(p.stack + height - r);
-            else
-                atomicOr(p.g.status, kStatusNoFreeBlocks);
-        }
-        taken += total;
-        s_par[threadIdx.x] = par, s_chi[threadIdx.x] = chi;
-        s_len[threadIdx.x] = len, s_new[threadIdx.x] = id;
-        __syncthreads();
-        const int here = min(kPlanThreads, p.n - at);
-        for (int k = warp; k < here; k += kPlanThreads / 32) {
-            if (s_par[k] < 0) continue;
-            const int* from = p.bt + (long long)s_par[k] * p.maxb;
-            int* to = p.bt + (long long)s_chi[k] * p.maxb;
-            const int full = s_len[k] / p.g.B;
-            for (int j = lane; j < p.maxb; j += 32) {
-                int e = -1;
-                if (j < full) {
-                    e = ld_dep(from + j);
-                    if (e < 0 || e >= p.g.num_blocks) {
-                        e = -1;
-                        atomicOr(p.g.status, kStatusBadBlock);
-                    } else {
-                        atomicAdd(p.shares + e, 1);
-                    }
-                } else if (j == full) {
-                    e = s_new[k];
-                }
-                to[j] = e;
-            }
-            if (lane == 0) p.lens[s_chi[k]] = s_len[k];
-        }
-        __syncthreads();
+// A pair of a fork: the parent's row and length, or par = -1 where it is to be
+// skipped (flagged by `report`).
+struct ForkPair {
+    int par, chi, len;
+};
+__device__ __forceinline__ ForkPair fork_pair(const ForkParams& p, int i, bool report) {
+    ForkPair f{ld_dep(p.parents + i), ld_dep(p.children + i), 0};
+    bool good = f.par >= 0 && f.par < p.batch && f.chi >= 0 && f.chi < p.batch && f.par != f.chi;
+    if (good) {
+        f.len = ld_dep(p.lens + f.par);
+        good = f.len >= 0 && f.len <= p.maxb * p.g.B;
     }
-    if (threadIdx.x == 0) p.stack[0] = taken < height ? height - taken : 0;
+    if (!good) {
+        f.par = -1;
+        if (report) atomicOr(p.g.status, kStatusBadLength);
+    }
+    return f;
 }
 
-// The live rows of every child's partial last page, from its parent's.
-__global__ void __launch_bounds__(kCopyThreads) pa_fork_copy_kernel(const ForkParams p) {
+// How many of the pairs before `n` take a page (the CTA counts together).
+__device__ __forceinline__ int fork_pages_before(const ForkParams& p, int n) {
+    int mine = 0;
+    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        const int i = i0 + threadIdx.x;
+        bool need = false;
+        if (i < n) {
+            const ForkPair f = fork_pair(p, i, false);
+            need = f.par >= 0 && f.len % p.g.B != 0;
+        }
+        mine += __syncthreads_count(need);
+    }
+    return mine;
+}
+
+// Child blockIdx.x takes its parent's table: full pages by reference, the
+// partial last page (if any) as a page of its own from the stack's top, in
+// increasing order of the children.  Each CTA counts the pages that the
+// children before its own take (an n-th of a launch's reads, against a second
+// launch's latency), so that the rows and the copies run side by side; CTAs (x,
+// 0) write the rows, all of them copy the tiles of the last page.  The stack's
+// height is set by the kernel after this one, since every CTA reads it here.
+__global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams p) {
     pdl_trigger();
     pdl_wait();
+    const int i = blockIdx.x;
+    const bool first = blockIdx.y == 0;
     const int lane = threadIdx.x & 31;
-    const int tiles = 2 * p.g.L * p.g.Hkv;
-    const long long total = (long long)p.n * tiles;
-    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
-    for (long long w = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); w < total;
-         w += warps) {
-        const int i = (int)(w / tiles), tile = (int)(w % tiles);
-        const int par = ld_dep(p.parents + i), chi = ld_dep(p.children + i);
-        if (par < 0 || par >= p.batch || chi < 0 || chi >= p.batch || par == chi) continue;
-        const int len = ld_dep(p.lens + par);
-        if (len < 0 || len > p.maxb * p.g.B) continue;
-        const int rows = len % p.g.B, full = len / p.g.B;
-        if (rows == 0) continue;
-        const int a = ld_dep(p.bt + (long long)par * p.maxb + full);
-        const int b = ld_dep(p.bt + (long long)chi * p.maxb + full);
-        if (a < 0 || a >= p.g.num_blocks || b < 0 || b >= p.g.num_blocks) {
-            if (tile == 0 && lane == 0) atomicOr(p.g.status, kStatusBadBlock);
-            continue;
-        }
-        if (a != b) warp_copy_tile(p.g, tile, a, b, rows * (p.g.tile_bytes / p.g.B / 16), lane);
+    const int height = stack_height(p.stack, p.g.num_blocks, p.g.status);
+    const ForkPair f = fork_pair(p, i, first && threadIdx.x == 0);
+    const int rank = fork_pages_before(p, i);
+    if (f.par < 0) return;
+    const int full = f.len / p.g.B, rows = f.len % p.g.B;
+    int id = -1;
+    if (rows) {
+        if (rank < height)
+            id = ld_dep(p.stack + height - rank);
+        else if (first && threadIdx.x == 0)
+            atomicOr(p.g.status, kStatusNoFreeBlocks);
     }
+    const int* from = p.bt + (long long)f.par * p.maxb;
+    if (first) {
+        int* to = p.bt + (long long)f.chi * p.maxb;
+        for (int j = threadIdx.x; j < p.maxb; j += kCopyThreads) {
+            int e = -1;
+            if (j < full) {
+                e = ld_dep(from + j);
+                if (e < 0 || e >= p.g.num_blocks) {
+                    e = -1;
+                    atomicOr(p.g.status, kStatusBadBlock);
+                } else {
+                    atomicAdd(p.shares + e, 1);
+                }
+            } else if (j == full) {
+                e = id;
+            }
+            to[j] = e;
+        }
+        if (threadIdx.x == 0) p.lens[f.chi] = f.len;
+    }
+    if (rows == 0 || id == -1) return;
+    // the live rows of the partial last page
+    const int old = ld_dep(from + full);
+    if (old < 0 || old >= p.g.num_blocks || id < 0 || id >= p.g.num_blocks) {
+        if (first && threadIdx.x == 0) atomicOr(p.g.status, kStatusBadBlock);
+        return;
+    }
+    const int tiles = 2 * p.g.L * p.g.Hkv;
+    const int chunks = rows * (p.g.tile_bytes / p.g.B / 16);
+    for (int t = blockIdx.y * (kCopyThreads / 32) + (threadIdx.x >> 5); t < tiles;
+         t += gridDim.y * (kCopyThreads / 32))
+        if (old != id) warp_copy_tile(p.g, t, old, id, chunks, lane);
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pa_fork_height_kernel(const ForkParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int height = stack_height(p.stack, p.g.num_blocks, p.g.status);
+    const int taken = fork_pages_before(p, p.n);
+    if (threadIdx.x == 0) p.stack[0] = taken < height ? height - taken : 0;
 }
 
 // --------------------------------------------------------------- shared free
@@ -215,43 +222,144 @@ __global__ void __launch_bounds__(kCopyThreads) pa_fork_copy_kernel(const ForkPa
 //  1  shares[id] -= 1 for every such entry: < 0 where no owner is left;
 //  2  the owners of those pages bid with their place in the order; the lowest
 //     code (the last place) stays in shares[id];
-//  3  each row counts its winning entries, a scan gives the rows their slots,
-//     and the winners push and put shares[id] back to 0.
+//  3  the winning entries are counted, a scan gives them their slots, and they
+//     push and put shares[id] back to 0.
+// The steps wait for one another.  A cluster of CTAs takes an equal share of the
+// entries each and keeps their ids in shared memory between the steps: what
+// bounds it is the scattered accesses to `shares`, about one per cycle and SM
+// (64 finished groups of 3, 6,900 entries: one CTA 17 us).  Tables too large for
+// that are read again in every step, by one CTA.
+constexpr int kFreeCluster = 8;
+constexpr int kFreeRows = 8192;                    // rows whose places fit
+constexpr int kFreeEntries = kFreeCluster * 24576;  // entries whose ids fit
+
+// Pages of row b that are given up (0 for a row that is not finished).
+__device__ __forceinline__ int free_row_blocks(const FreeSharedParams& p, int b, bool report) {
+    if (b >= p.batch || !p.finished[b]) return 0;
+    const int n = ld_dep(p.lens + b);
+    if (n < 0 || n > p.maxb * p.B) {
+        if (report) atomicOr(p.status, kStatusBadLength);
+        return 0;
+    }
+    return (n + p.B - 1) / p.B;
+}
+// The code of a place < 2^30: below every count that `shares` can hold.
+__device__ __forceinline__ int free_bid(long long place) {
+    return (int)(0x80000000u + (0x40000000u - (unsigned)place));
+}
+__device__ __forceinline__ void free_push(const FreeSharedParams& p, int slot, int id) {
+    if (slot < p.num_blocks)
+        p.stack[1 + slot] = id;
+    else
+        atomicOr(p.status, kStatusBadBlock);  // more ids than the pool holds
+    p.shares[id] = 0;
+}
+__device__ __forceinline__ void free_height(const FreeSharedParams& p, int height, int pushed) {
+    const long long h = (long long)height + pushed;
+    p.stack[0] = (int)(h < p.num_blocks ? h : p.num_blocks);
+}
+
 __global__ void __launch_bounds__(kPlanThreads) pa_free_shared_kernel(const FreeSharedParams p) {
+    pdl_trigger();
+    pdl_wait();
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ int s_start[];       // [batch + 1] places of the rows, then ids
+    int* s_ids = s_start + p.batch + 1;
+    __shared__ int s_warp[32], s_wins[kFreeCluster];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int height = stack_height(p.stack, p.num_blocks, p.status);
+    int count = 0;
+    for (int at = 0; at < p.batch; at += kPlanThreads) {
+        const int nblk = free_row_blocks(p, at + threadIdx.x, rank == 0);
+        int total = 0;
+        const int start = count + cta_exclusive_scan(nblk, s_warp, total);
+        if (at + threadIdx.x < p.batch) s_start[at + threadIdx.x] = start;
+        count += total;
+    }
+    if (threadIdx.x == 0) s_start[p.batch] = count;
+    __syncthreads();
+    // this CTA's entries: places [lo, hi)
+    const int each = (count + ctas - 1) / ctas;
+    const int lo = min(rank * each, count), hi = min(lo + each, count);
+    for (int k = warp; k < p.batch; k += kPlanThreads / 32) {
+        const int start = s_start[k];
+        const int j1 = min(s_start[k + 1], hi) - start;
+        int* row = p.bt + (long long)k * p.maxb;
+#pragma unroll 4
+        for (int j = max(lo - start, 0) + lane; j < j1; j += 32) {
+            int id = ld_dep(row + j);
+            row[j] = -1;
+            if (id < 0 || id >= p.num_blocks) {
+                id = -1;
+                atomicOr(p.status, kStatusBadBlock);
+            } else {
+                atomicSub(p.shares + id, 1);
+            }
+            s_ids[start + j - lo] = id;
+        }
+    }
+    __threadfence();
+    cluster.sync();
+    for (int e = lo + threadIdx.x; e < hi; e += kPlanThreads) {
+        const int id = s_ids[e - lo];
+        if (id >= 0 && __ldcg(p.shares + id) < 0) atomicMin(p.shares + id, free_bid(e));
+    }
+    __threadfence();
+    cluster.sync();
+    // a thread's entries are neighbours (an odd number of them: no two lanes on one
+    // bank), so that one scan orders all
+    const int mine_n = (hi - lo + kPlanThreads - 1) / kPlanThreads | 1;
+    const int e0 = min(lo + (int)threadIdx.x * mine_n, hi), e1 = min(e0 + mine_n, hi);
+    int mine = 0;
+#pragma unroll 4
+    for (int e = e0; e < e1; ++e) {
+        const int id = s_ids[e - lo];
+        const bool win = id >= 0 && __ldcg(p.shares + id) == free_bid(e);
+        if (!win) s_ids[e - lo] = -1;
+        mine += win;
+    }
+    int wins = 0;
+    int slot = height + cta_exclusive_scan(mine, s_warp, wins);
+    if (threadIdx.x < ctas) cluster.map_shared_rank(s_wins, threadIdx.x)[rank] = wins;
+    cluster.sync();  // (and no CTA resets `shares` before all have compared)
+    int pushed = 0;
+    for (int r = 0; r < ctas; ++r) {
+        if (r < rank) slot += s_wins[r];
+        pushed += s_wins[r];
+    }
+    for (int e = e0; e < e1; ++e) {
+        const int id = s_ids[e - lo];
+        if (id >= 0) free_push(p, slot++, id);
+    }
+    if (rank == 0 && threadIdx.x == 0) free_height(p, height, pushed);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pa_free_shared_large_kernel(const FreeSharedParams p) {
     pdl_trigger();
     pdl_wait();
     __shared__ int s_warp[32];
     __shared__ int s_nblk[kPlanThreads], s_slot[kPlanThreads];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int height = stack_height(p.stack, p.num_blocks, p.status);
-    // pages of row b that are given up (0 for a row that is not finished)
-    auto row_blocks = [&](int b, bool report) {
-        if (b >= p.batch || !p.finished[b]) return 0;
-        const int n = ld_dep(p.lens + b);
-        if (n < 0 || n > p.maxb * p.B) {
-            if (report) atomicOr(p.status, kStatusBadLength);
-            return 0;
-        }
-        return (n + p.B - 1) / p.B;
-    };
-    auto bid = [&](int b, int j) {
-        return (int)(0x80000000u + (0x40000000u - (unsigned)((long long)b * p.maxb + j)));
-    };
+    auto good = [&](int id) { return id >= 0 && id < p.num_blocks; };
+    int pushed = 0;
     for (int pass = 0; pass < 2; ++pass) {
         for (int at = 0; at < p.batch; at += kPlanThreads) {
-            s_nblk[threadIdx.x] = row_blocks(at + threadIdx.x, pass == 0);
+            s_nblk[threadIdx.x] = free_row_blocks(p, at + threadIdx.x, pass == 0);
             __syncthreads();
             const int here = min(kPlanThreads, p.batch - at);
             for (int k = warp; k < here; k += kPlanThreads / 32) {
                 const int* row = p.bt + (long long)(at + k) * p.maxb;
                 for (int j = lane; j < s_nblk[k]; j += 32) {
                     const int id = row[j];
-                    if (id < 0 || id >= p.num_blocks) {
+                    if (!good(id)) {
                         if (pass == 0) atomicOr(p.status, kStatusBadBlock);
                     } else if (pass == 0) {
                         atomicSub(p.shares + id, 1);
                     } else if (__ldcg(p.shares + id) < 0) {
-                        atomicMin(p.shares + id, bid(at + k, j));
+                        atomicMin(p.shares + id, free_bid((long long)(at + k) * p.maxb + j));
                     }
                 }
             }
@@ -260,9 +368,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_free_shared_kernel(const Free
         __threadfence();
         __syncthreads();
     }
-    int pushed = 0;
     for (int at = 0; at < p.batch; at += kPlanThreads) {
-        s_nblk[threadIdx.x] = row_blocks(at + threadIdx.x, false);
+        s_nblk[threadIdx.x] = free_row_blocks(p, at + threadIdx.x, false);
         s_slot[threadIdx.x] = 0;
         __syncthreads();
         const int here = min(kPlanThreads, p.batch - at);
@@ -271,7 +378,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_free_shared_kernel(const Free
             int mine = 0;
             for (int j = lane; j < s_nblk[k]; j += 32) {
                 const int id = row[j];
-                mine += id >= 0 && id < p.num_blocks && __ldcg(p.shares + id) == bid(at + k, j);
+                mine += good(id) && __ldcg(p.shares + id) == free_bid((long long)(at + k) * p.maxb + j);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kFullMask, mine, o);
@@ -293,26 +400,16 @@ __global__ void __launch_bounds__(kPlanThreads) pa_free_shared_kernel(const Free
                     id = row[j];
                     row[j] = -1;
                 }
-                const bool win = id >= 0 && id < p.num_blocks &&
-                                 __ldcg(p.shares + id) == bid(at + k, j);
+                const bool win =
+                    good(id) && __ldcg(p.shares + id) == free_bid((long long)(at + k) * p.maxb + j);
                 const unsigned wins = __ballot_sync(kFullMask, win);
-                if (win) {
-                    const int to = slot + __popc(wins & ((1u << lane) - 1u));
-                    if (to < p.num_blocks)
-                        p.stack[1 + to] = id;
-                    else
-                        atomicOr(p.status, kStatusBadBlock);  // more ids than the pool holds
-                    p.shares[id] = 0;
-                }
+                if (win) free_push(p, slot + __popc(wins & ((1u << lane) - 1u)), id);
                 slot += __popc(wins);
             }
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        const long long h = (long long)height + pushed;
-        p.stack[0] = (int)(h < p.num_blocks ? h : p.num_blocks);
-    }
+    if (threadIdx.x == 0) free_height(p, height, pushed);
 }
 
 // ------------------------------------------------------------------ compact
@@ -453,15 +550,50 @@ cudaError_t launch_copy_blocks(const PageGeom& g, const int* src, const int* dst
 
 cudaError_t launch_fork(const ForkParams& p, int num_sms, cudaStream_t s) {
     if (p.n <= 0) return cudaSuccess;
-    cudaError_t e = launch_pdl(pa_fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+    // CTAs per child: enough to fill the GPU with few children, no more than a
+    // page has tiles for
+    const long long tiles = 2LL * p.g.L * p.g.Hkv;
+    long long parts = (8LL * num_sms + p.n - 1) / p.n;
+    const long long most = (tiles + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    if (parts > most) parts = most;
+    if (parts > 65535) parts = 65535;
+    cudaError_t e = launch_pdl(pa_fork_kernel, dim3((unsigned)p.n, (unsigned)parts),
+                               dim3(kCopyThreads), 0, s, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(pa_fork_copy_kernel, dim3(copy_grid(2LL * p.g.L * p.g.Hkv * p.n, num_sms)),
-                      dim3(kCopyThreads), 0, s, p);
+    return launch_pdl(pa_fork_height_kernel, dim3(1), dim3(kCopyThreads), 0, s, p);
 }
 
 cudaError_t launch_free_shared(const FreeSharedParams& p, cudaStream_t s) {
     if (p.batch <= 0) return cudaSuccess;
-    return launch_pdl(pa_free_shared_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+    const long long entries = (long long)p.batch * p.maxb;
+    if (p.batch > kFreeRows || entries > kFreeEntries)
+        return launch_pdl(pa_free_shared_large_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
+    // (a cluster's barriers cost about 1 us more than a CTA's: 24 finished rows of
+    // a 32-row table with 1,664 entries take 5.7 us in one CTA and 6.7 in eight)
+    const int ctas = entries <= 4096 ? 1 : kFreeCluster;
+    const long long ids = (entries + ctas - 1) / ctas;
+    const size_t smem = (size_t)(p.batch + 1 + ids) * sizeof(int);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            pa_free_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (kFreeRows + 1 + kFreeEntries / kFreeCluster) * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, pa_free_shared_kernel, p);
 }
 
 size_t compact_smem_bytes(long long num_blocks) {

@@ -512,15 +512,18 @@ def test_copy_blocks_bad_ids(cuda_device):
 
 
 @pytest.mark.parametrize("geom", range(len(GEOMS)))
-@pytest.mark.parametrize("rows", [6, 1500])
-def test_fork_free_compact_steps(cuda_device, geom, rows):
+@pytest.mark.parametrize("rows,wide", [(6, 0), (1500, 0), (1500, 150)])
+def test_fork_free_compact_steps(cuda_device, geom, rows, wide):
     """Random steps of forks, frees and compactions against the plain model, on
-    the device state alone; more rows than one CTA's threads too."""
+    the device state alone; more rows than one CTA's threads, and tables too large
+    for shared memory, too."""
     dev, (_, _, _, block, _) = cuda_device, GEOMS[geom]
     rng = np.random.default_rng(geom)
     first = 3 if rows < 100 else 400
     lens = [int(x) for x in rng.integers(0, 5 * block + 2, first)]
     cache, ref, rng = pages_case(dev, GEOMS[geom], geom, rows, rows + 50, lens)
+    ref.tables = np.pad(ref.tables, ((0, 0), (0, wide)), constant_values=-1)
+    assert (ref.tables.size > 8 * 24576) == (wide > 0)
     stack, tables = device_stack(ref.stack, cache.num_blocks, dev), ints(ref.tables, dev)
     ln, shares = ints(ref.lens, dev), cache.page_shares()
     used = set(range(first))
