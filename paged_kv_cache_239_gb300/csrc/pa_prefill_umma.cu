@@ -36,7 +36,8 @@ cudaError_t launch_inst(const PrefillParams& p, const CUtensorMap* tm, cudaStrea
     }
     e = launch_pdl(kern, dim3((unsigned)p.grid), dim3(C::THREADS), C::SMEM_BYTES, s, p, tm[0], tm[1], tq);
     if (e != cudaSuccess || p.grid == 1) return e;
-    return launch_pdl(pa_prefill_umma_join_kernel<D>, dim3((unsigned)p.grid, 8), dim3(256), 0, s, p);
+    return launch_pdl(pa_prefill_umma_join_kernel<D>, dim3((unsigned)p.grid, kJoinParts),
+                      dim3(256), 0, s, p);
 }
 
 }  // namespace

@@ -1065,48 +1065,52 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// Joins the parts of the pairs that the CTAs' shares cut: one group of CTAs per
-// main CTA, a warp per row.
+// Joins the parts of the pairs that the CTAs' shares cut: the CTAs (x, *) the
+// pair that main CTA x recorded, D / 4 lanes to a row.  A handful of dependent
+// accesses to L2 is all it costs, so a batch of four parts is in flight at once.
+constexpr int kJoinParts = 16;  // CTAs per pair
 template <int D>
 __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
+    constexpr int LPR = D / 4, RPC = 256 / LPR;  // lanes per row, rows per CTA and pass
+    const int lane = threadIdx.x % LPR;
     const int4 a = ld_dep(p.cut + 2 * blockIdx.x);
     const int4 e = ld_dep(p.cut + 2 * blockIdx.x + 1);
     const int pieces = e.x;
     if (pieces <= 1) return;
-    const int row0 = a.z;
-    constexpr int V = D / 32;
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < 256; r += gridDim.y * 8) {
-        const int f = row0 + r;
-        if (f >= e.z) return;
-        auto slot = [&](int k) {
-            return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? e.y : 0)) * 256 + r;
-        };
-        float m = -FLT_MAX;
-        for (int k = lane; k < pieces; k += 32) m = fmaxf(m, ld_dep(p.part_ml + 2 * slot(k)));
+    for (int r = blockIdx.y * RPC + threadIdx.x / LPR; r < 256 && a.z + r < e.z; r += kJoinParts * RPC) {
+        // (rows of part k: CTA x + k's first slot, but for k = 0)
+        const long long row0 = (long long)blockIdx.x * 512 + 256 * e.y + r;
+        auto row = [&](int k) { return k == 0 ? row0 : (long long)(blockIdx.x + k) * 512 + r; };
+        float m = -FLT_MAX, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < pieces; k0 += 4) {
+            float2 ml[4];
+            float4 x[4];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, x));
-        float l = 0.f, o[V] = {};
-        for (int k = 0; k < pieces; ++k) {
-            const float2 ml = ld_dep(reinterpret_cast<const float2*>(p.part_ml) + slot(k));
-            if (ml.y == 0.f) continue;
-            const float w = ex2_approx(ml.x - m);
-            l = fmaf(w, ml.y, l);
-            const float* src = p.part_o + slot(k) * D + lane * V;
+            for (int u = 0; u < 4; ++u) {
+                if (k0 + u >= pieces) break;
+                ml[u] = ld_dep(reinterpret_cast<const float2*>(p.part_ml) + row(k0 + u));
+                x[u] = ld_dep(reinterpret_cast<const float4*>(p.part_o) + row(k0 + u) * LPR + lane);
+            }
 #pragma unroll
-            for (int v = 0; v < V; v += 2) {
-                const float2 x = ld_dep(reinterpret_cast<const float2*>(src + v));
-                o[v] = fmaf(w, x.x, o[v]), o[v + 1] = fmaf(w, x.y, o[v + 1]);
+            for (int u = 0; u < 4; ++u) {
+                if (k0 + u >= pieces) break;
+                if (ml[u].y == 0.f) continue;  // (the part saw no key of the row)
+                const float mn = fmaxf(m, ml[u].x);
+                const float keep = ex2_approx(m - mn), w = ex2_approx(ml[u].x - mn);
+                m = mn;
+                l = fmaf(l, keep, w * ml[u].y);
+                o.x = fmaf(o.x, keep, w * x[u].x), o.y = fmaf(o.y, keep, w * x[u].y);
+                o.z = fmaf(o.z, keep, w * x[u].z), o.w = fmaf(o.w, keep, w * x[u].w);
             }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int tok = pf_div(p, f);
+        const int f = a.z + r, tok = pf_div(p, f);
         const long long orow = (long long)(a.w + tok) * p.H + a.y * p.G + (f - tok * p.G);
-        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + lane * V);
-#pragma unroll
-        for (int v = 0; v < V; v += 2) out[v / 2] = pack_bf16x2(o[v] * inv, o[v + 1] * inv);
+        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * D)[lane] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
 }
 
