@@ -918,7 +918,7 @@ int check_stack(const void* dev_stack) {
 // What both prefill calls need of the sizes: how the work is split, and where
 // the workspace holds what.
 struct PrefillShape {
-    int splits = 1, grid = 0;
+    int splits = 1, cluster = 1, grid = 0;
     size_t ml_off = 0, cut_off = 0, ws_bytes = 0;
 };
 int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads, int maxb,
@@ -950,8 +950,10 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
         sh->grid = pa::prefill_umma_grid(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
         if (sh->grid > 1) rows = (size_t)sh->grid * 2 * 256;
     } else {
-        sh->splits = pa::prefill_simt_splits(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
-        if (sh->splits > 1) rows = (size_t)sh->splits * num_tokens * num_heads;
+        sh->splits = pa::prefill_f32_splits(G, g.Hkv, batch, num_tokens, maxb, g.B, sms,
+                                            &sh->cluster);
+        const int groups = sh->splits / sh->cluster;
+        if (groups > 1) rows = (size_t)groups * num_tokens * num_heads;
     }
     if (rows == 0) return PA_OK;
     sh->ml_off = align256(rows * g.D * sizeof(float));
@@ -1156,7 +1158,7 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
     p.lens = context_lens, p.starts = query_starts;
     p.batch = batch, p.num_tokens = num_tokens;
     p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax evaluated with exp2
-    p.splits = sh.splits;
+    p.splits = sh.splits, p.cluster = sh.cluster;
     p.grid = sh.grid;
     if (sh.ws_bytes) {
         char* ws = static_cast<char*>(workspace);
@@ -1176,7 +1178,7 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
         p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
         e = pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
     } else {
-        e = pa::launch_prefill_simt(p, g.D, g.B, s);
+        e = pa::launch_prefill_f32(p, g.D, g.B, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
     return PA_OK;

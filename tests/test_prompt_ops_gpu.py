@@ -293,6 +293,37 @@ def test_prefill_future_values_do_not_reach_earlier_rows(cuda_device, dtype, d, 
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_prefill_infinite_key(cuda_device, dtype, bad):
+    """One infinite element of a cached key: a score of -inf has no weight, one of
+    +inf makes its row NaN."""
+    new, ctx, d = [40, 3], [140, 50], 64
+    pool_t, tables, q = prefill_case(cuda_device, dtype, d, 16, 6, 2, new, ctx, seed=9)
+    pool_t[int(tables[0, 2]), 0, 0, :, 5, 7] = bad   # position 37 of sequence 0
+    down = (q[:40, :, 7] * bad) < 0                  # rows to which that key is -inf
+    got = run_prefill(cuda_device, pool_t, tables, q, new, ctx)
+    assert bool(torch.isnan(got[:40][~down]).all()) and bool(down.any()) and not bool(down.all())
+    # without that key, in 64 bits; the bound is that of `R.prefill`
+    pages = torch.as_tensor(tables[0, :9].astype(np.int64), device=cuda_device)
+    k, v = pool_t[pages, :, 0].double().permute(1, 2, 0, 3, 4).reshape(2, 2, -1, d)[:, :, :140]
+    k, v = k.repeat_interleave(3, 0).clone(), v.repeat_interleave(3, 0)
+    k[:, 37] = 0
+    x = q[:40].double()
+    see = torch.arange(140, device=cuda_device) <= torch.arange(100, 140, device=cuda_device)[:, None]
+    see = see & (torch.arange(140, device=cuda_device) != 37)
+    p = torch.softmax((torch.einsum("nhd,htd->nht", x, k) * d ** -0.5)
+                      .masked_fill(~see[:, None], -float("inf")), -1)
+    size = torch.einsum("nhd,htd->nht", x.abs(), k.abs()).amax(-1, keepdim=True) * d ** -0.5
+    rel = 2 * ((d + 4) * R.U * size + 2.0 ** -22) + 2 * 148 * R.U + (2.0 ** -8 if dtype == "bf16" else 0)
+    want = torch.einsum("nht,htd->nhd", p, v)
+    bound = R.HALF_STEP[DT[dtype]] * want.abs() * (1 + rel) + rel * torch.einsum("nht,htd->nhd", p, v.abs())
+    check(got[:40][down], want[down], bound[down])
+    clean = prefill_case(cuda_device, dtype, d, 16, 6, 2, new, ctx, seed=9)[0]
+    want, bound = R.prefill(clean, q, tables, ctx, new, d ** -0.5)
+    check(got[40:], want[40:], bound[40:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prefill_large_scores(cuda_device, dtype):
     """Rows whose maximum rises by hundreds along the context."""
     new, ctx, d = [40], [700], 128
