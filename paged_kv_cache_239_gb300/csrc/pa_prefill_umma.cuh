@@ -66,11 +66,11 @@ struct PrefillCfg {
     static constexpr int OFF_Q = NS * TILE;
     static constexpr int OFF_CTRL = OFF_Q + 2 * TILE;
     // ctrl (bytes): barriers | TMEM address, abort, mark_piece, done[2] | box bits
-    // per stage | schedule | the producers' page ids | pieces [NP] | marks [3][D]
+    // per stage | schedule (72 bytes) | the producers' page ids | pieces [NP] | marks [3][D]
     // (the schedule's scratch before)
     static constexpr int NP = 4;
     static constexpr int TMEM_SLOT = 384, ABORT = 388, MARK_PIECE = 392, DONE = 396, BITS = 404,
-                         SCHED = 448, BLOCKS = 496, PIECES = 576, MARKS = 832, SCAN = MARKS;
+                         SCHED = 448, BLOCKS = 528, PIECES = 592, MARKS = 832, SCAN = MARKS;
     static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 3 * 128 * 4;
     static constexpr int THREADS = 384;
     // TMEM: S_0, S_1 (P in their first 64 columns), O_0, O_1
@@ -115,6 +115,17 @@ __device__ __forceinline__ PfSeq pf_sequence(const PrefillParams& p, int b, bool
     return s;
 }
 
+// A sequence in shared memory (16-byte aligned, 24 bytes).
+__device__ __forceinline__ void pf_keep(const PfSeq& s, unsigned char* at) {
+    *reinterpret_cast<int4*>(at) = make_int4(s.start, s.n_new, s.n, s.first_pos);
+    *reinterpret_cast<int2*>(at + 16) = make_int2(s.rows, s.tiles);
+}
+__device__ __forceinline__ PfSeq pf_kept(const unsigned char* at) {
+    const int4 a = *reinterpret_cast<const int4*>(at);
+    const int2 b = *reinterpret_cast<const int2*>(at + 16);
+    return PfSeq{a.x, a.y, a.z, a.w, b.x, b.y};
+}
+
 // x / G for 0 <= x < 2^31 (the host's multiplier: a 32-bit division costs ~30
 // instructions, and the set-up runs many).
 __device__ __forceinline__ int pf_div(const PrefillParams& p, int x) {
@@ -154,15 +165,20 @@ struct PfWalk {
 // Units of sequence b0 + lane (all lanes of the warp take part).
 template <int B>
 __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b, int lane,
-                                                  bool report) {
+                                                  bool report, PfSeq& s) {
     bool bad;
-    const PfSeq s = pf_sequence<B>(p, b, &bad);
+    s = pf_sequence<B>(p, b, &bad);
     if (bad && report) atomicOr(p.status, kStatusBadLength);
     long long u = 0;
-    if (s.tiles <= 8)
+    // (a sequence taken by the whole warp costs what about 32 pairs cost one lane)
+    const int lim = 32 * max(1, __popc(__ballot_sync(kFullMask, s.tiles > 16)));
+    if (s.tiles <= lim) {
+        int v = s.tiles * kPairUnits;
 #pragma unroll 1
-        for (int i = 0; i < s.tiles; ++i) u += kPairUnits + pf_key_tiles(p, s, i);
-    unsigned big = __ballot_sync(kFullMask, s.tiles > 8);
+        for (int i = 0; i < s.tiles; ++i) v += pf_key_tiles(p, s, i);
+        u = v;
+    }
+    unsigned big = __ballot_sync(kFullMask, s.tiles > lim);
     while (big) {
         const int f = __ffs(big) - 1;
         big &= big - 1;
@@ -181,26 +197,33 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
 }
 
 // The CTA's range of the T units, into `sched`: [0] T, [8] first unit, [16]
-// units, [24] offset within the pair, [32] b, [36] KV head, [40] pair.
+// units, [24] offset within the pair, [32] b, [36] KV head, [40] pair, [48] the
+// sequence.  Up to 32 sequences are one warp's, without barriers in between.
 template <typename C>
 __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned char* ctrl) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int NW = C::THREADS / 32;
+    const int nw = p.batch <= 32 ? 1 : C::THREADS / 32;  // warps that take part
     long long* sums = reinterpret_cast<long long*>(ctrl + C::SCAN);
     long long* out = reinterpret_cast<long long*>(ctrl + C::SCHED);
     int* outi = reinterpret_cast<int*>(ctrl + C::SCHED + 32);
+    if (warp >= nw) return;
     long long u = 0, mine = 0;
+    PfSeq s{0, 0, 0, 0, 0, 0};
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.batch; b0 += C::THREADS) {
-        u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, blockIdx.x == 0);
+    for (int b0 = 0; b0 < p.batch; b0 += nw * 32) {
+        u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, blockIdx.x == 0, s);
         mine += u;
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mine += __shfl_xor_sync(kFullMask, mine, x);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    long long T = 0;
-    for (int w = 0; w < NW; ++w) T += sums[w];
+    long long T = mine;
+    if (nw > 1) {
+        if (lane == 0) sums[warp] = mine;
+        __syncthreads();
+        T = 0;
+#pragma unroll 1
+        for (int w = 0; w < nw; ++w) T += sums[w];
+    }
     T *= p.Hkv;
     // (no more shares than units: an empty one inside a cut pair would be taken
     // for a part of it)
@@ -208,26 +231,29 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
     const long long j = blockIdx.x;
     long long lo = 0, hi = 0;
     if (j < grid) {
-        lo = pf_div64(j * T + grid - 1, grid);
-        hi = pf_div64((j + 1) * T + grid - 1, grid);
+        const long long x = pf_div64((j + (lane & 1)) * T + grid - 1, grid);
+        lo = __shfl_sync(kFullMask, x, 0), hi = __shfl_sync(kFullMask, x, 1);
     }
     long long before = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.batch; b0 += C::THREADS) {
-        if (p.batch > C::THREADS) u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, false);
+    for (int b0 = 0; b0 < p.batch; b0 += nw * 32) {
+        if (p.batch > nw * 32) u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, false, s);
         long long incl = u * p.Hkv;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
             const long long v = __shfl_up_sync(kFullMask, incl, x);
             if (lane >= x) incl += v;
         }
-        __syncthreads();
-        if (lane == 31) sums[warp] = incl;
-        __syncthreads();
         long long base = before;
-        for (int w = 0; w < NW; ++w) {
-            if (w < warp) base += sums[w];
-            before += sums[w];
+        if (nw > 1) {
+            __syncthreads();
+            if (lane == 31) sums[warp] = incl;
+            __syncthreads();
+#pragma unroll 1
+            for (int w = 0; w < nw; ++w) {
+                if (w < warp) base += sums[w];
+                before += sums[w];
+            }
         }
         const long long at = base + incl - u * p.Hkv;
         if (lo >= at && lo < at + u * p.Hkv && hi > lo) {
@@ -235,13 +261,16 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
             const long long h = pf_div64(lo - at, u);
             outi[1] = (int)h;
             out[3] = lo - at - h * u;
+            pf_keep(s, ctrl + C::SCHED + 48);
         }
     }
-    __syncthreads();
+    if (nw > 1)
+        __syncthreads();
+    else
+        __syncwarp();
     if (warp == 0 && hi > lo) {
         // the pair within the sequence and KV head
-        bool bad;
-        const PfSeq s = pf_sequence<C::B>(p, outi[0], &bad);
+        s = pf_kept(ctrl + C::SCHED + 48);
         long long off = out[3];
         int i = 0;
 #pragma unroll 1
@@ -277,8 +306,7 @@ __device__ __forceinline__ void pf_walk_begin(const PrefillParams& p, const unsi
     if (w.left <= 0) return;
     w.off = in[3], w.gpos = in[1] - in[3];
     w.b = ini[0], w.kvh = ini[1], w.i = ini[2];
-    bool bad;
-    w.s = pf_sequence<C::B>(p, w.b, &bad);
+    w.s = pf_kept(ctrl + C::SCHED + 48);
 }
 
 // The next piece with work; kvt: the pair's key tiles, gpos: the global unit of
