@@ -485,7 +485,7 @@ PA_API int pa_gather_kv(void* k_out, void* v_out, uint8_t* mask, const pa_pool* 
  * behind the last sequence are neither read nor written.  A sequence with
  * n_b > context_lens[b] or a length past its table sets PA_STATUS_BAD_LENGTH
  * and its output rows are zero; starts that break the rule above set it too,
- * and the rows they bound are unspecified.
+ * and the output is unspecified.
  * ------------------------------------------------------------------------- */
 
 /* Rotary frequencies: a host object that holds no device memory. */
@@ -619,8 +619,9 @@ PA_API int pa_copy_blocks(pa_pool* pool, const int* src_ids, const int* dst_ids,
  * Parent and child then append independently.  The children's rows must hold no
  * pages (free them first), be distinct, and not be parents in the same call.
  *   block_tables  device int32 [batch, max_blocks_per_seq]; context_lens [batch].
- * When the stack runs dry, the entries of the pages that were not to be had
- * are -1 (PA_STATUS_NO_FREE_BLOCKS).  Pairs with rows outside [0, batch), a row
+ * n <= 65536.  When the stack runs dry, the entries of the pages that were not
+ * to be had are -1 (PA_STATUS_NO_FREE_BLOCKS); so are table entries and stack
+ * ids outside the pool (PA_STATUS_BAD_BLOCK_ID).  Pairs with rows outside [0, batch), a row
  * as its own parent or a bad parent length are skipped (PA_STATUS_BAD_LENGTH).
  * Cites: no counterpart on the pages (their tables share no blocks); new pages
  * come from the free list as in mini-infer, "Python Implementation: Physical

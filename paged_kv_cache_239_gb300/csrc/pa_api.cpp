@@ -1129,7 +1129,8 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
     if (int rc = check_layer(pool, layer)) return rc;
     const pa::PoolGeom& g = pool->g;
     if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
-    if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
+    if (!std::isfinite(scale * 1.4426950408889634f))
+        return fail(PA_ERR_INVALID_ARG, "scale is not finite (times log2 e)");
     PrefillShape sh;
     if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
         return rc;
@@ -1211,6 +1212,7 @@ int pa_device_fork_sequences(pa_pool* pool, void* dev_stack, int* shares, int* b
         return rc;
     if (n < 0 || n > batch)
         return fail(PA_ERR_INVALID_ARG, "n %d outside [0, batch]: the children are distinct rows", n);
+    if (n > 65536) return fail(PA_ERR_INVALID_ARG, "n %d is above 65536", n);
     if (n == 0) return PA_OK;
     if (int rc = check_stack(dev_stack)) return rc;
     if (!shares || !parents || !children || !aligned(shares, 4) || !aligned(parents, 4) ||

@@ -150,8 +150,8 @@ __device__ __forceinline__ int fork_pages_before(const ForkParams& p, int n) {
 // Child blockIdx.x takes its parent's table: full pages by reference, the
 // partial last page (if any) as a page of its own from the stack's top, in
 // increasing order of the children.  Each CTA counts the pages that the
-// children before its own take (an n-th of a launch's reads, against a second
-// launch's latency), so that the rows and the copies run side by side; CTAs (x,
+// children before its own take (n / 256 steps at most, against a second launch's
+// latency), so that the rows and the copies run side by side; CTAs (x,
 // 0) write the rows, all of them copy the tiles of the last page.  The stack's
 // height is set by the kernel after this one, since every CTA reads it here.
 __global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams p) {
@@ -167,10 +167,15 @@ __global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams 
     const int full = f.len / p.g.B, rows = f.len % p.g.B;
     int id = -1;
     if (rows) {
-        if (rank < height)
+        if (rank < height) {
             id = ld_dep(p.stack + height - rank);
-        else if (first && threadIdx.x == 0)
+            if (id < 0 || id >= p.g.num_blocks) {
+                id = -1;
+                if (first && threadIdx.x == 0) atomicOr(p.g.status, kStatusBadBlock);
+            }
+        } else if (first && threadIdx.x == 0) {
             atomicOr(p.g.status, kStatusNoFreeBlocks);
+        }
     }
     const int* from = p.bt + (long long)f.par * p.maxb;
     if (first) {
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams 
     if (rows == 0 || id == -1) return;
     // the live rows of the partial last page
     const int old = ld_dep(from + full);
-    if (old < 0 || old >= p.g.num_blocks || id < 0 || id >= p.g.num_blocks) {
+    if (old < 0 || old >= p.g.num_blocks) {
         if (first && threadIdx.x == 0) atomicOr(p.g.status, kStatusBadBlock);
         return;
     }

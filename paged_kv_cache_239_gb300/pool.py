@@ -177,6 +177,9 @@ class BlockPool:
             out = self._empty(q.shape, self.dtype, stream)
         else:
             self._check_dense(out, (tokens, num_heads, self.head_dim), self.dtype, "out")
+        if rope is not None and rope.handle is None:  # (NULL would mean no rotation)
+            raise ValueError("the Rope is closed")
+        self._check_current()
         B.pa_norm_rope_write_kv(self.handle, layer, out, q, q_stride, k, k_stride, v, v_stride,
                                 None if rope is None else rope.handle, q_weight, k_weight, eps,
                                 block_tables, maxb, context_lens, query_starts, batch, tokens,
@@ -204,6 +207,7 @@ class BlockPool:
             out = self._empty(shape, self.dtype, stream)
         else:
             self._check_dense(out, shape, self.dtype, "out")
+        self._check_current()
         if workspace is None:  # (the call checks one that is given)
             need = self.prefill_workspace_size(batch, tokens, num_heads, maxb)
             if need:
@@ -220,6 +224,7 @@ class BlockPool:
         n = src_ids.shape[0]
         self._check_dense(src_ids, (n,), torch.int32, "src_ids")
         self._check_dense(dst_ids, (n,), torch.int32, "dst_ids")
+        self._check_current()
         B.pa_copy_blocks(self.handle, src_ids, dst_ids, n, stream)
 
     def page_shares(self) -> torch.Tensor:
@@ -236,6 +241,7 @@ class BlockPool:
         self._check_pages(stack, shares)
         self._check_dense(parents, (n,), torch.int32, "parents")
         self._check_dense(children, (n,), torch.int32, "children")
+        self._check_current()
         B.pa_device_fork_sequences(self.handle, stack, shares, block_tables, maxb, context_lens,
                                    batch, parents, children, n, stream)
 
@@ -247,6 +253,7 @@ class BlockPool:
         self._check_pages(stack, shares)
         self._check_dense(finished, (batch,),
                           torch.bool if finished.dtype is torch.bool else torch.uint8, "finished")
+        self._check_current()
         B.pa_device_free_shared(self.handle, stack, shares, block_tables, maxb, context_lens,
                                 finished, batch, stream)
 
@@ -273,6 +280,7 @@ class BlockPool:
         self._check_pages(out_stack, out_shares)
         self._check_dense(out_tables, tuple(block_tables.shape), torch.int32, "out_tables")
         self._check_dense(remap, (self.num_blocks,), torch.int32, "remap")
+        self._check_current()
         if workspace is None:
             workspace = self._empty((self.compact_workspace_size(),), torch.uint8, stream)
         B.pa_device_compact_blocks(self.handle, stack, shares, block_tables, maxb, context_lens,
@@ -290,6 +298,12 @@ class BlockPool:
             stream = torch.cuda.ExternalStream(stream, device=self.pool.device)
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.pool.device)
+
+    def _check_current(self) -> None:
+        """The calls launch on torch's current device; its kernels could not reach
+        a pool elsewhere."""
+        if self._device_index < 0 or torch.cuda.current_device() != self._device_index:
+            raise ValueError(f"the pool is on {self.pool.device}, which is not the current CUDA device")
 
     def _check_dense(self, t: torch.Tensor, shape, dtype, name: str) -> None:
         if (t.shape == shape and t.dtype is dtype and t.get_device() == self._device_index

@@ -109,7 +109,7 @@ def test_prefill_refusals(pa_lib, pool):
         B.pa_prefill_attention(**a)
 
     for kw in (dict(pool=None), dict(layer=2), dict(batch=-1), dict(num_tokens=-1), dict(num_heads=5),
-               dict(max_blocks_per_seq=0), dict(max_blocks_per_seq=1 << 28), dict(scale=math.inf),
+               dict(max_blocks_per_seq=0), dict(max_blocks_per_seq=1 << 28), dict(scale=math.inf), dict(scale=3e38),
                dict(block_tables=None), dict(context_lens=F + 1), dict(num_tokens=1 << 30)):
         refused(B, bad, call, **kw)
     call(batch=0, num_tokens=0)
@@ -133,6 +133,7 @@ def test_page_refusals(pa_lib, pool):
     for kw in (dict(pool=None), dict(dev_stack=None), dict(shares=None), dict(n=-1), dict(n=4),
                dict(block_tables=None), dict(max_blocks_per_seq=0), dict(parents=F + 1), dict(children=None)):
         refused(B, bad, B.pa_device_fork_sequences, **{**fork, **kw})
+    refused(B, bad, B.pa_device_fork_sequences, **{**fork, "batch": 70000, "n": 65537})
     B.pa_device_fork_sequences(**{**fork, "n": 0})
     free = dict(pool=pool, dev_stack=F, shares=F, block_tables=F, max_blocks_per_seq=4,
                 context_lens=F, finished=F, batch=3)
@@ -191,4 +192,28 @@ def test_wrapper_refusals(pa_lib):
     for call in calls:
         with pytest.raises(ValueError):
             call()
+    # tensors that fit, but the pool is not on the current CUDA device
+    kid, fin = ln[:1] + 1, torch.zeros(2, dtype=torch.bool)
+    for call in [lambda: pool.prefill_attention(q, 0, bt, ln, st, 0.1),
+                 lambda: pool.norm_rope_write_kv(0, q, kv, kv, bt, ln, query_starts=st),
+                 lambda: pool.copy_blocks(one, one + 1),
+                 lambda: pool.device_fork_sequences(stack, shares, bt, ln, one, kid),
+                 lambda: pool.device_free_shared(stack, shares, bt, ln, fin),
+                 lambda: pool.device_compact_blocks(stack, bt, ln)]:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+    pool.close()
+
+
+def test_closed_rope_is_refused(pa_lib):
+    """A closed Rope is not taken for "no rotation"."""
+    from paged_kv_cache_239_gb300.pool import BlockPool
+    from paged_kv_cache_239_gb300.rope import Rope
+
+    pool, rope = BlockPool(4, 16, 1, 2, 64, device="cpu"), Rope(64)
+    rope.close()
+    q, kv = torch.zeros((1, 4, 64), dtype=torch.bfloat16), torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="closed"):
+        pool.norm_rope_write_kv(0, q, kv, kv, torch.zeros((1, 1), dtype=torch.int32),
+                                torch.ones(1, dtype=torch.int32), rope=rope)
     pool.close()

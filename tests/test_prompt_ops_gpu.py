@@ -324,6 +324,48 @@ def test_prefill_infinite_key(cuda_device, dtype, bad):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,most,extra", [(40, 70, 300), (130, 3, 2000), (500, 4, 60), (1200, 1, 20)])
+def test_prefill_many_sequences(cuda_device, dtype, batch, most, extra):
+    """Batches that the schedule takes in one warp, in all warps and in several turns."""
+    rng = np.random.default_rng(batch)
+    new = [int(x) for x in rng.integers(0, most + 1, batch)]
+    ctx = [n + int(rng.integers(0, extra + 1)) for n in new]
+    pool_t, tables, q = prefill_case(cuda_device, dtype, 64, 16, 8, 2, new, ctx, seed=batch)
+    got = run_prefill(cuda_device, pool_t, tables, q, new, ctx)
+    status_is(0)
+    check(got, *R.prefill(pool_t, q, tables, ctx, new, 64 ** -0.5))
+
+
+def test_prefill_two_streams_at_once(cuda_device):
+    """Calls side by side on two streams, each with its own workspace, over one pool."""
+    dev, cases = cuda_device, []
+    pool_t, tables, q = prefill_case(dev, "bf16", 128, 16, 8, 2, [300, 200], [900, 700], seed=12)
+    cache = BlockPool(pool_t.shape[0], 16, 1, 2, 128, tensor=pool_t)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args = [(0, ints(tables[b:b + 1], dev), ints([c], dev), ints([0, n], dev), 128 ** -0.5)
+            for b, (n, c) in enumerate([(300, 900), (200, 700)])]
+    qs = [q[:300].contiguous(), q[300:].contiguous()]
+    alone = [cache.prefill_attention(x, *a) for x, a in zip(qs, args)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        cases.append([cache.prefill_attention(x, *a, stream=s) for x, a, s in zip(qs, args, streams)])
+    torch.cuda.synchronize()
+    status_is(0)
+    for outs in cases:
+        assert all(torch.equal(x, y) for x, y in zip(outs, alone))
+    cache.close()
+
+
+def test_calls_need_the_current_device(cuda_device, monkeypatch):
+    cache = BlockPool(4, 16, 1, 2, 64)
+    ids = ints([0], cuda_device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        cache.copy_blocks(ids, ids)
+    cache.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prefill_large_scores(cuda_device, dtype):
     """Rows whose maximum rises by hundreds along the context."""
     new, ctx, d = [40], [700], 128
@@ -584,6 +626,22 @@ def test_fork_free_compact_steps(cuda_device, geom, rows, wide):
         if not used:
             break
     status_is(0)
+
+
+def test_fork_bad_stack_ids(cuda_device):
+    """Ids on the stack that are no pages' do not get into a table."""
+    dev = cuda_device
+    cache, ref, _ = pages_case(dev, GEOMS[0], 2, 8, 2, [20, 21, 5])
+    stack, tables = device_stack(ref.stack, cache.num_blocks, dev), ints(ref.tables, dev)
+    top = int(stack[0])
+    good = int(stack[top - 1])
+    stack[top] = cache.num_blocks
+    ln, shares = ints(ref.lens, dev), cache.page_shares()
+    cache.device_fork_sequences(stack, shares, tables, ln, ints([0, 1], dev), ints([3, 4], dev))
+    status_is(B.PA_STATUS_BAD_BLOCK_ID)
+    assert int(tables[3, 1]) == -1 and int(tables[4, 1]) == good and int(stack[0]) == top - 2
+    assert int(tables[3, 0]) == int(tables[0, 0]) and int(ln[3]) == 20
+    cache.close()
 
 
 def test_fork_runs_dry_and_bad_rows(cuda_device):
