@@ -7,13 +7,27 @@
 // The query heads of a KV head's group share its keys, so the rows of a tile
 // are (token, head of the group) in that order, flattened: row r is token r / G,
 // head r % G, and a tile takes 64 consecutive rows whatever G is, 16 to a warp.
-// Keys and values come 32 at a time (cp.async, two stages).
+// Keys and values come 32 at a time (head_dim 128: 16), by cp.async in two stages:
+// what leaves room for three CTAs on an SM.
 //
 // TF32 keeps 11 bits of a product's factors, so x = hi + lo with hi = x rounded to
 // TF32 and lo = x - hi (exact; 12 bits, of which TF32 keeps 11): hi hi' + hi lo' +
 // lo hi' misses x x' by about 2^-22, as an fp32 product does by 2^-24, and the
-// sums are fp32.  Three m16n8k8 products take 25.5 cycles of a scheduler for 1024
-// multiply-adds, fused multiply-adds 32 and as many shared-memory operands again.
+// sums are fp32.  Three m16n8k8 products take 24 cycles of a scheduler's tensor pipe
+// for 1024 multiply-adds; fused multiply-adds take 32, and two operands from shared
+// memory for each sixteenth of them.
+//
+// What bounds it: five in six instructions are not products (splits, operand loads,
+// the softmax), and the pipe is busy about 62 % of the time.  A prompt of
+// 4096 with 32 heads on 8: head_dim 64 1.13 ms, 128 2.23 ms (2.38 with tiles of 32
+// keys and two CTAs per SM), 61 TFLOP/s of the formula; with fused multiply-adds
+// it ran at 12.
+//
+// Few row tiles: each is split over the keys, up to eight ways in a cluster that
+// joins its parts through distributed shared memory (a prompt of 128: 8.7 us; the
+// same joined by a second launch 12.5), and beyond that in several clusters, whose
+// parts a second launch joins (4 tokens over 30,000 keys 26 us; all 64 parts joined
+// by the launch, 52).
 //
 // The order of the summed index is free in a product, so it is chosen to suit the
 // fragments: a thread's four neighbouring elements of q and k are its columns of
@@ -24,8 +38,9 @@
 // inf * 0 and inf - inf would make NaN of what a row sees as an infinite value, or
 // does not see at all.  Values that are not finite are zeroed in shared memory and
 // remembered by column and position, and put into the rows that see them at the
-// end; a warp whose scores come out not finite sums that tile's plainly.  (What TF32 would round to infinity, the last 2^-12 of the range, is
-// taken the same way; such a value is cut by as much.)
+// end; a warp whose scores come out not finite sums that tile's plainly.  (What
+// TF32 would round to infinity, the last 2^-12 of the range, is taken the same
+// way; such a value is cut by as much.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -41,10 +56,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int BM = 64, BN = 32, kThreads = 128;
+constexpr int BM = 64, kThreads = 128;
+constexpr int key_tile(int D) { return D == 128 ? 16 : 32; }  // keys per tile
 
 template <int D>
 struct F32Cfg {
+    static constexpr int BN = key_tile(D);
     static constexpr int LQ = D + 16, LV = D + 4;   // row strides (floats) of q and k; v
     static constexpr int STAGE = BN * (LQ + LV);    // floats
     static constexpr int SMEM = (BM * LQ + 2 * STAGE) * 4 + 3 * D * 4;
@@ -104,10 +121,11 @@ struct Joined {
 };
 
 template <int D, int B>
-__global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const PrefillParams p) {
+__global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
     using C = F32Cfg<D>;
+    constexpr int BN = C::BN;
     extern __shared__ __align__(16) float smem[];
     float* sq = smem;
     float* ring = sq + BM * C::LQ;
@@ -116,10 +134,11 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
-    // ---- the tile: sequence and first row of the grid's last tiles first (a prompt's
-    // last rows see most) ----
+    // ---- the tile: sequence and first row; the last tiles first, of all KV heads (a
+    // prompt's last rows see most: what starts late is short) ----
+    const int kvh = blockIdx.x % p.Hkv;
     if (warp == 0) {
-        int left = gridDim.x - 1 - blockIdx.x, found = -1, row0 = 0;
+        int left = gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv, found = -1, row0 = 0;
         for (int b0 = 0; b0 < p.batch && found < 0; b0 += 32) {
             const int b = b0 + lane;
             int tiles = 0;
@@ -127,8 +146,7 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
                 const int s0 = ld_dep(p.starts + b), s1 = ld_dep(p.starts + b + 1);
                 const int n = ld_dep(p.lens + b);
                 const bool good = s0 >= 0 && s1 >= s0 && s1 <= p.num_tokens;
-                if ((!good || n < 0 || n > p.maxb * B) && blockIdx.x == 0 && blockIdx.y == 0 &&
-                    blockIdx.z == 0)
+                if ((!good || n < 0 || n > p.maxb * B) && blockIdx.x == 0 && blockIdx.y == 0)
                     atomicOr(p.status, kStatusBadLength);
                 if (good) tiles = (int)(((long long)(s1 - s0) * p.G + BM - 1) / BM);
             }
@@ -152,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
     __syncthreads();
     const int b = s_at[0], row0 = s_at[1];
     if (b < 0) return;
-    const int kvh = blockIdx.y;
     const int start = ld_dep(p.starts + b);
     const int n_new = ld_dep(p.starts + b + 1) - start;
     int n = ld_dep(p.lens + b);
@@ -166,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
     const int see = n > 0 ? first_pos + (row0 + rows - 1) / p.G + 1 : 0;
     const int key_tiles = (see + BN - 1) / BN;
     const int per = (key_tiles + p.splits - 1) / p.splits;
-    const int kt0 = min((int)blockIdx.z * per, key_tiles), kt1 = min(kt0 + per, key_tiles);
+    const int kt0 = min((int)blockIdx.y * per, key_tiles), kt1 = min(kt0 + per, key_tiles);
 
     // ---- copies: q once; k and v a tile ahead, thread = 16-byte chunk of rows ----
     constexpr int CPR = D / 4, RPP = kThreads / CPR;  // chunks per row, rows per pass
@@ -182,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
     }
     const float* kb = static_cast<const float*>(p.k_base) + p.tile_off + (long long)kvh * p.s_head + 4 * cc;
     const float* vb = static_cast<const float*>(p.v_base) + p.tile_off + (long long)kvh * p.s_head + 4 * cc;
-    constexpr int PAGES = BN / B;  // 1 or 2 per tile
+    constexpr int PAGES = BN > B ? BN / B : 1;  // 1 or 2 per tile
     int page[2], ids[2];           // the next tile's pages (-1: none); ids as read, one tile ahead
     auto look_up = [&](int kt) {
 #pragma unroll
@@ -209,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
             for (int r = 0; r < BN; r += RPP) {
                 const int key = r + cr, blk = PAGES == 1 || key < B ? page[0] : page[1];
                 const bool in = blk >= 0 && kt * BN + key < n;
-                const long long off = in ? (long long)blk * p.s_blk + (long long)(key % B) * D : 0;
+                const int row = (BN < B ? kt * BN + key : key) % B;
+                const long long off = in ? (long long)blk * p.s_blk + row * D : 0;
                 cp16(k_at + r * C::LQ * 4, kb + off, in);
                 cp16(v_at + r * C::LV * 4, vb + off, in);
             }
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2) pa_prefill_f32_kernel(const Prefi
         if (groups == 1) {
             reinterpret_cast<float4*>(p.out)[orow * CPR + cc] = j.out();
         } else {
-            const long long prow = (long long)(blockIdx.z / p.cluster) * p.num_tokens * p.H + orow;
+            const long long prow = (long long)(blockIdx.y / p.cluster) * p.num_tokens * p.H + orow;
             reinterpret_cast<float4*>(p.part_o)[prow * CPR + cc] = j.o;
             if (cc == 0) reinterpret_cast<float2*>(p.part_ml)[prow] = make_float2(j.m, j.l);
         }
@@ -487,10 +505,10 @@ cudaError_t launch_inst(const PrefillParams& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          F32Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    const long long tiles = (long long)p.num_tokens * p.G / BM + p.batch;
-    if (tiles > 0x7fffffffLL || p.Hkv > 65535) return cudaErrorInvalidConfiguration;
+    const long long ctas = ((long long)p.num_tokens * p.G / BM + p.batch) * p.Hkv;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles, p.Hkv, p.splits);
+    cfg.gridDim = dim3((unsigned)ctas, p.splits);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = F32Cfg<D>::SMEM;
     cfg.stream = s;
@@ -498,8 +516,8 @@ cudaError_t launch_inst(const PrefillParams& p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = p.cluster;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.z = 1;
+    attr[1].val.clusterDim.y = p.cluster;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, p);
@@ -523,7 +541,7 @@ int prefill_f32_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int 
                        int* cluster) {
     const long long tiles = ((long long)num_tokens * G / BM + batch) * Hkv;
     const long long want = tiles > 0 ? 2LL * num_sms / tiles : 1;
-    const long long most = ((long long)maxb * B + BN - 1) / BN;
+    const long long most = ((long long)maxb * B + 31) / 32;
     const long long n = want < most ? want : most;
     *cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
     return n >= 16 ? (int)(n < 256 ? n : 256) / 8 * 8 : *cluster;
