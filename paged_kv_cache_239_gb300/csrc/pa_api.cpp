@@ -950,7 +950,7 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
         sh->grid = pa::prefill_umma_grid(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
         if (sh->grid > 1) rows = (size_t)sh->grid * 2 * 256;
     } else {
-        sh->splits = pa::prefill_f32_splits(G, g.Hkv, batch, num_tokens, maxb, g.B, sms,
+        sh->splits = pa::prefill_f32_splits(G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms,
                                             &sh->cluster);
         const int groups = sh->splits / sh->cluster;
         if (groups > 1) rows = (size_t)groups * num_tokens * num_heads;

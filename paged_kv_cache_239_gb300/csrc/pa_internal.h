@@ -186,8 +186,8 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, int D, int num_
                              cudaStream_t s);
 bool prefill_supported(int dtype, int D, int B);
 // fp32: the splits of the contexts that a call's size asks for.
-int prefill_f32_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms,
-                       int* cluster);
+int prefill_f32_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
+                       int num_sms, int* cluster);
 cudaError_t launch_prefill_f32(const PrefillParams& p, int D, int B, cudaStream_t s);
 // bf16: the persistent grid; `tmaps` points to the pool's two CUtensorMap.
 int prefill_umma_grid(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms);

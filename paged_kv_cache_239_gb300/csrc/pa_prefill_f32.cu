@@ -47,6 +47,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -534,17 +536,28 @@ bool prefill_supported(int dtype, int D, int B) {
     return (dtype == 0 || dtype == 1) && (D == 64 || D == 128) && (B == 16 || B == 32);
 }
 
-// Splits of the contexts: two CTAs per SM where the row tiles alone do not give
-// them, each with two key tiles at least.  Up to eight are a cluster, which joins
-// its parts by itself; more are clusters of eight, whose parts a second launch joins.
-int prefill_f32_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms,
-                       int* cluster) {
+// Parts of each context (the host knows the tables' width, not the lengths).  Up to
+// eight are a cluster, which joins them by itself: as many as give every SM a CTA,
+// and up to eight CTAs where each part keeps three key tiles, since a prompt's row
+// tiles see few or many keys and short parts even that out (500 tokens of 16 heads
+// behind 7,300: 1 part 1250 us, 2 936, 4 670, 8 607); parts of less than three
+// tiles do not pay for the join once they share an SM (4 sequences of up to 130
+// tokens: 4 parts 20.7 us, 8 25.8).  More than eight take a second launch: where
+// two CTAs per SM ask for 16 and each has a tile (4 tokens over 30,000 keys: 152
+// parts 26 us, 256 33).
+int prefill_f32_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
+                       int num_sms, int* cluster) {
     const long long tiles = ((long long)num_tokens * G / BM + batch) * Hkv;
-    const long long want = tiles > 0 ? 2LL * num_sms / tiles : 1;
-    const long long most = ((long long)maxb * B + 31) / 32;
-    const long long n = want < most ? want : most;
-    *cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
-    return n >= 16 ? (int)(n < 256 ? n : 256) / 8 * 8 : *cluster;
+    const long long keys = ((long long)maxb * B + key_tile(D) - 1) / key_tile(D);  // tiles
+    if (tiles <= 0) return *cluster = 1;
+    const long long one = num_sms / tiles;  // parts that get an SM each
+    const long long wide = std::min({2 * num_sms / tiles, keys, 256LL});
+    if (wide >= 16) {
+        *cluster = 8;
+        return (int)wide / 8 * 8;
+    }
+    const long long n = std::min({8 * num_sms / tiles, keys, std::max(one, keys / 3)});
+    return *cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
 }
 
 cudaError_t launch_prefill_f32(const PrefillParams& p, int D, int B, cudaStream_t s) {
