@@ -89,34 +89,41 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
     pdl_wait();
     using C = Chunk<T>;
     constexpr int E = C::E;
-    constexpr int LPR = D / E;       // lanes per row
+    constexpr int LPR = D / E / 2;   // lanes per row, two chunks each
     constexpr int RPW = 32 / LPR;    // rows per warp and pass
-    constexpr int U = 4;             // passes in flight
+    constexpr int U = 2;             // passes in flight
     const int lane = threadIdx.x & 31;
     const unsigned w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     const int t = (int)(w / (unsigned)p.splits);
     const int split = (int)(w % (unsigned)p.splits);
     if (t >= p.num_tokens) return;
-    const int c = lane % LPR;        // this lane's chunk of its row
-    const int sub = lane / LPR;
+    // this lane's chunks of its row: a pair's elements lie both in them, and its angles
+    // are l E .. l E + E - 1 (what does not turn is dealt out behind what does)
+    const int l = lane % LPR, sub = lane / LPR;
+    const int half = p.rotary / E / 2;
+    const bool turns = l < half;
+    const int c0 = INTERLEAVED ? 2 * l : turns ? l : 2 * l;
+    const int c1 = INTERLEAVED || !turns ? c0 + 1 : l + half;
     const int rows = p.H + 2 * p.Hkv;
     const int step = p.splits * RPW;
 
-    // This lane's chunk of row r (queries, keys, values in that order).
-    auto load = [&](int r) {
-        if (r >= rows) return make_uint4(0, 0, 0, 0);
+    // This lane's chunks of row r (queries, keys, values in that order).
+    auto load = [&](int r, uint4 (&to)[2]) {
+        to[0] = to[1] = make_uint4(0, 0, 0, 0);
+        if (r >= rows) return;
         const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.Hkv;
         const T* src = is_q ? static_cast<const T*>(p.q) + (long long)t * p.q_stride + (long long)r * D
                        : is_k ? static_cast<const T*>(p.k) + (long long)t * p.k_stride +
                                     (long long)(r - p.H) * D
                               : static_cast<const T*>(p.v) + (long long)t * p.v_stride +
                                     (long long)(r - p.H - p.Hkv) * D;
-        return ld_dep(reinterpret_cast<const uint4*>(src) + c);
+        to[0] = ld_dep(reinterpret_cast<const uint4*>(src) + c0);
+        to[1] = ld_dep(reinterpret_cast<const uint4*>(src) + c1);
     };
     // the first rows are on their way while the token's place is looked up
-    uint4 raw[U];
+    uint4 raw[U][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = load(split * RPW + sub + u * step);
+    for (int u = 0; u < U; ++u) load(split * RPW + sub + u * step, raw[u]);
 
     // ---- where the token stands ----
     int b = t, s0 = t, n_new = 1;
@@ -138,93 +145,89 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
     }
     const long long slot = (long long)blk * p.s_blk + p.tile_off + (long long)(pos % p.B) * D;
     const bool norm = p.q_weight != nullptr;
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+    uint4 wq[2], wk[2];
+    wq[0] = wq[1] = wk[0] = wk[1] = make_uint4(0, 0, 0, 0);
     if (norm) {
-        wq = ld_dep(static_cast<const uint4*>(p.q_weight) + c);
-        wk = ld_dep(static_cast<const uint4*>(p.k_weight) + c);
+        wq[0] = ld_dep(static_cast<const uint4*>(p.q_weight) + c0);
+        wq[1] = ld_dep(static_cast<const uint4*>(p.q_weight) + c1);
+        wk[0] = ld_dep(static_cast<const uint4*>(p.k_weight) + c0);
+        wk[1] = ld_dep(static_cast<const uint4*>(p.k_weight) + c1);
     }
 
     // ---- this lane's sines ----
-    constexpr int NF = INTERLEAVED ? E / 2 : E;
-    const int rc = p.rotary / E;     // chunks that turn
-    const bool turns = c < rc;
-    float cs[NF], sn[NF];
+    float cs[E], sn[E];
     if (turns) {
-        const int f0 = INTERLEAVED ? c * (E / 2) : (c % (rc / 2)) * E;
 #pragma unroll
-        for (int k = 0; k < NF; ++k) {
-            const unsigned long long x = (unsigned long long)pos * p.freq[f0 + k];
+        for (int k = 0; k < E; ++k) {
+            const unsigned long long x = (unsigned long long)pos * p.freq[l * E + k];
             const float half_turns = (float)(int)(x >> 32) * 4.656612873077393e-10f;  // 2^-31
             sincospif(half_turns, &sn[k], &cs[k]);
             sn[k] *= p.amplitude, cs[k] *= p.amplitude;
         }
     }
-    // halves: the partner chunk, and the sign of its sine's term
-    const int partner = turns ? (c < rc / 2 ? lane + rc / 2 : lane - rc / 2) : lane;
-    if (!INTERLEAVED && c < rc / 2) {
-#pragma unroll
-        for (int k = 0; k < NF; ++k) sn[k] = -sn[k];
-    }
 
     for (int r0 = split * RPW; r0 < rows; r0 += U * step) {
-        uint4 next[U];
+        uint4 next[U][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = load(r0 + sub + (U + u) * step);
+        for (int u = 0; u < U; ++u) load(r0 + sub + (U + u) * step, next[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = r0 + sub + u * step;
             if (r0 + u * step >= rows) break;  // (the whole warp)
             const bool is_q = r < p.H, is_k = !is_q && r < p.H + p.Hkv;
-            float x[E];
-            C::unpack(raw[u], x);
+            float x[2][E];
+            C::unpack(raw[u][0], x[0]);
+            C::unpack(raw[u][1], x[1]);
             if (norm) {
                 float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < E; k += 2) {
-                    const float2 v = make_float2(x[k], x[k + 1]);
-                    s2 = fma2(v, v, s2);
-                }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < E; k += 2) {
+                        const float2 v = make_float2(x[h][k], x[h][k + 1]);
+                        s2 = fma2(v, v, s2);
+                    }
                 float ss = s2.x + s2.y;
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
                 const float rs = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-                float wv[E];
-                C::unpack(is_q ? wq : wk, wv);
 #pragma unroll
-                for (int k = 0; k < E; k += 2) {
-                    const float2 v = mul2(mul2(make_float2(x[k], x[k + 1]), make_float2(rs, rs)),
-                                          make_float2(wv[k], wv[k + 1]));
-                    x[k] = v.x, x[k + 1] = v.y;
-                }
-            }
-            if constexpr (INTERLEAVED) {
-                if (turns) {  // (the rest passes as it is, be it infinite)
+                for (int h = 0; h < 2; ++h) {
+                    float wv[E];
+                    C::unpack(is_q ? wq[h] : wk[h], wv);
 #pragma unroll
-                    for (int k = 0; k < NF; ++k) {
-                        const float a = x[2 * k], d = x[2 * k + 1];
-                        x[2 * k] = a * cs[k] - d * sn[k];
-                        x[2 * k + 1] = a * sn[k] + d * cs[k];
+                    for (int k = 0; k < E; k += 2) {
+                        const float2 v = mul2(mul2(make_float2(x[h][k], x[h][k + 1]), make_float2(rs, rs)),
+                                              make_float2(wv[k], wv[k + 1]));
+                        x[h][k] = v.x, x[h][k + 1] = v.y;
                     }
                 }
-            } else {
+            }
+            if (turns) {  // (the rest passes as it is, be it infinite)
 #pragma unroll
                 for (int k = 0; k < E; ++k) {
-                    const float o = __shfl_sync(kFullMask, x[k], partner);
-                    if (turns) x[k] = x[k] * cs[k] + o * sn[k];
+                    float& a = INTERLEAVED ? x[2 * k / E][2 * k % E] : x[0][k];
+                    float& d = INTERLEAVED ? x[2 * k / E][2 * k % E + 1] : x[1][k];
+                    const float y = a * cs[k] - d * sn[k];
+                    d = a * sn[k] + d * cs[k];
+                    a = y;
                 }
             }
             if (r >= rows) continue;
             if (is_q) {
-                reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + ((long long)t * p.H + r) * D)[c] =
-                    good ? C::pack(x) : make_uint4(0, 0, 0, 0);
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + ((long long)t * p.H + r) * D);
+                dst[c0] = good ? C::pack(x[0]) : make_uint4(0, 0, 0, 0);
+                dst[c1] = good ? C::pack(x[1]) : make_uint4(0, 0, 0, 0);
             } else if (blk >= 0) {
                 const int h = is_k ? r - p.H : r - p.H - p.Hkv;
-                T* dst = static_cast<T*>(is_k ? p.k_base : p.v_base) + slot + (long long)h * p.s_head;
-                reinterpret_cast<uint4*>(dst)[c] = is_k ? C::pack(x) : raw[u];
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(is_k ? p.k_base : p.v_base) + slot +
+                                                      (long long)h * p.s_head);
+                dst[c0] = is_k ? C::pack(x[0]) : raw[u][0];
+                dst[c1] = is_k ? C::pack(x[1]) : raw[u][1];
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = next[u];
+        for (int u = 0; u < U; ++u) raw[u][0] = next[u][0], raw[u][1] = next[u][1];
     }
 }
 
@@ -241,7 +244,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p_in, int dtype, int D, int n
                              cudaStream_t s) {
     NormRopeParams p = p_in;
     const int elt = dtype == 1 ? 2 : 4;
-    const int rpw = 32 / (D * elt / 16);
+    const int rpw = 64 / (D * elt / 16);
     const long long groups = (p.H + 2LL * p.Hkv + rpw - 1) / rpw;
     // warps per token: one, unless that leaves SMs without eight warps
     long long splits = (8LL * num_sms + p.num_tokens - 1) / p.num_tokens;
