@@ -565,7 +565,8 @@ PA_API int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const vo
  *   out[t][h] = softmax_s(scale * q[t][h] . K_s) V_s over s <= position of t,
  * rows resolved through the block table as in pa_decode_attention, fp32 scores
  * and sums.  What lies in the cache at positions a row does not see (future
- * tokens, rows past the context), be it NaN, does not reach that row.
+ * tokens, rows past the context), be it NaN, does not reach that row; a value
+ * that is not finite makes its column of every row that sees it not finite.
  *   out, q        device [num_tokens, num_heads, head_dim] of the pool dtype,
  *                 contiguous, 16-byte aligned; they must not overlap.
  *   workspace     at least pa_prefill_workspace_size() bytes, 256-byte aligned

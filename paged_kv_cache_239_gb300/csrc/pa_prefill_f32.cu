@@ -109,8 +109,7 @@ struct Joined {
     __device__ __forceinline__ void add(float2 ml, float4 x) {
         if (ml.y == 0.f) return;  // (the part saw no key of the row)
         const float mn = fmaxf(m, ml.x);
-        // (above zero: a row shows an infinite value however small its weight)
-        const float keep = fmaxf(ex2_approx(m - mn), 1.2e-38f), w = fmaxf(ex2_approx(ml.x - mn), 1.2e-38f);
+        const float keep = ex2_approx(m - mn), w = ex2_approx(ml.x - mn);
         m = mn;
         l = fmaf(l, keep, w * ml.y);
         o.x = fmaf(o.x, keep, w * x.x), o.y = fmaf(o.y, keep, w * x.y);

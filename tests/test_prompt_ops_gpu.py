@@ -366,6 +366,28 @@ def test_calls_need_the_current_device(cuda_device, monkeypatch):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,ctx", [([4], [9000]), ([300], [1200]), ([3] * 9, [700] * 9)])
+def test_prefill_infinite_values_of_tiny_weight(cuda_device, dtype, new, ctx):
+    """Scores so far apart that most weights are below the smallest number, where 0 *
+    inf is NaN: a value that is infinite shows as not finite in every row that sees
+    it, also where the keys are taken in parts, and in no other column."""
+    d = 128
+    pool_t, tables, q = prefill_case(cuda_device, dtype, d, 16, 8, 2, new, ctx, seed=13)
+    for b, c in enumerate(ctx):
+        for i in range(7, c - max(new), 97):
+            pool_t[int(tables[b, i // 16]), 1, 0, :, i % 16, i % d] = float("inf")
+    got = run_prefill(cuda_device, pool_t, tables, q, new, ctx, scale=4.0).float()
+    status_is(0)
+    start = 0
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        cols = sorted({i % d for i in range(7, c - max(new), 97)})
+        rest = [x for x in range(d) if x not in cols]
+        assert not bool(torch.isfinite(got[start:start + n][..., cols]).any())
+        assert bool(torch.isfinite(got[start:start + n][..., rest]).all())
+        start += n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prefill_large_scores(cuda_device, dtype):
     """Rows whose maximum rises by hundreds along the context."""
     new, ctx, d = [40], [700], 128
