@@ -38,6 +38,25 @@
 // V outside the context are zeroed in shared memory, and values that are not
 // finite are zeroed and remembered by column and position, to be put back into
 // the rows that see them at the output.
+//
+// What bounds it.  Long prompts: a pair's tile is 4 x 8 MMAs of 128 x 128 x 16, 2048
+// cycles of the tensor pipe, and takes about 2750, since S(i + 1) waits for the
+// softmax of S(i) to leave the columns that P stands in, with 512 columns for two
+// row tiles' S and O (the exponentials, 2048 cycles of the special-function units,
+// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 379 us, 1.45 PFLOP/s of
+// the causal half (75 % of a large library product's burst rate).  Measured and
+// slower there: two threads to a row 450 us; two issuing threads 480; P handed over
+// in halves 409 (in three parts, as here, 400 by the same clock).  Without the
+// exponentials it would take 383.  Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to
+// 131,000: 169 us, 5.6 TB/s (83 % of a plain copy's rate), in shares cut to the tile.
+// Short calls: latency; one token over 100 keys takes 8.9 us, of which 2.5 go to
+// the schedule (its code is fetched by every SM), 2.5 to the first K tile and its
+// scores, and 2.5 to the join's launch; 8 chunks of up to 513 tokens with 16 heads
+// on 2 of 64: 27 us, of which 11 are those, 9 five to seven tiles.
+//
+// The shares charge a pair kPairUnits tiles: a tile costs about 2,930 cycles and a
+// pair 9,500 more (Q, the first scores, the output).  With 2 the last CTA of a batch
+// of short prompts ends after 802,000 cycles, with 3 after 728,000.
 #pragma once
 
 #include <cfloat>
@@ -86,7 +105,7 @@ struct PrefillCfg {
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
-constexpr int kPairUnits = 3;
+constexpr int kPairUnits = 3;  // (see above)
 
 // A sequence as the schedule sees it.
 struct PfSeq {
