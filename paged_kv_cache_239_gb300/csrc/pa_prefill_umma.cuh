@@ -1115,7 +1115,10 @@ __global__ void __launch_bounds__(384, 1)
 // Joins the parts of the pairs that the CTAs' shares cut: the CTAs (x, *) the
 // pair that main CTA x recorded, D / 4 lanes to a row.  A handful of dependent
 // accesses to L2 is all it costs, so a batch of four parts is in flight at once.
-constexpr int kJoinParts = 16;  // CTAs per pair
+// (CTAs per pair: for 32 sequences with 5 tokens over up to 2,000, and for 8 chunks
+// of up to 513, a call takes 17.2 and 27.2 us with 4, 17.7 and 26.7 with 8, 18.7 and
+// 27.0 with 16, 21.1 and 29.0 with 32; two rows in flight with 8: 18.3 and 27.1.)
+constexpr int kJoinParts = 8;
 template <int D>
 __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const PrefillParams p) {
     pdl_trigger();
