@@ -217,7 +217,8 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
 
 // The CTA's range of the T units, into `sched`: [0] T, [8] first unit, [16]
 // units, [24] offset within the pair, [32] b, [36] KV head, [40] pair, [48] the
-// sequence.  Up to 32 sequences are one warp's, without barriers in between.
+// sequence, all for warp 0.  Up to 32 sequences are that warp's, without barriers in
+// between.
 template <typename C>
 __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned char* ctrl) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -314,6 +315,7 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
         if (lane == 0) out[3] = off, outi[2] = i;
     }
     if (threadIdx.x == 0) out[0] = T, out[1] = lo, out[2] = hi - lo;
+    __syncwarp();
 }
 
 template <typename C>
@@ -582,12 +584,14 @@ __global__ void __launch_bounds__(384, 1)
         prefetch_tensormap(&tmv);
         prefetch_tensormap(&tmq);
     }
-    pdl_wait();
-    pf_schedule<C>(p, ctrl);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    // (the K producer alone needs the schedule: with few sequences the other warps are
+    // at their first wait, their code fetched, when it hands out the first piece)
+    pf_schedule<C>(p, ctrl);
     auto wait = [&](int bar, uint32_t parity) {
         return pf_wait(bar0 + 8 * bar, parity, abort_all, p.status);
     };
