@@ -536,6 +536,13 @@ __device__ __forceinline__ bool pf_unclean(const PfPiece& pc, int kt) {
     return 128 * (kt + 1) - 1 > pc.pair_pos;
 }
 
+// Where column d of row `row` of the partials is: 32 rows' 8 columns lie together,
+// so that a warp (one row per lane) stores whole lines (a pair's part of 64 columns:
+// 4,200 cycles row by row).
+__device__ __forceinline__ long long pf_part_at(long long row, int D, int d) {
+    return (row >> 5) * 32 * D + (d >> 3) * 256 + ((int)row & 31) * 8 + (d & 7);
+}
+
 // What a column's remembered values (first positions of a NaN, +inf, -inf) add
 // to the output of a row at `pos`.
 __device__ __forceinline__ float poison(const int* marks, int D, int d, int pos) {
@@ -1080,13 +1087,13 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                 } else if (live) {
-                    float* out = p.part_o + part * D + c;
+                    float* out = p.part_o + pf_part_at(part, D, c);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t v[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * h + k]);
-                        store32(out + 8 * h, v);
+                        store32(out + 256 * h, v);
                     }
                 }
             }
@@ -1099,7 +1106,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (pc.whole())
                         static_cast<__nv_bfloat16*>(p.out)[orow * D + d] = __float2bfloat16(v);
                     else
-                        p.part_o[part * D + d] = v;
+                        p.part_o[pf_part_at(part, D, d)] = v;
                 }
             }
             if (!pc.whole() && live) p.part_ml[2 * part] = m, p.part_ml[2 * part + 1] = l;
@@ -1117,54 +1124,84 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // Joins the parts of the pairs that the CTAs' shares cut: the CTAs (x, *) the
-// pair that main CTA x recorded, D / 4 lanes to a row.  A handful of dependent
-// accesses to L2 is all it costs, so a batch of four parts is in flight at once.
-// (CTAs per pair: for 32 sequences with 5 tokens over up to 2,000, and for 8 chunks
-// of up to 513, a call takes 17.2 and 27.2 us with 4, 17.7 and 26.7 with 8, 18.7 and
-// 27.0 with 16, 21.1 and 29.0 with 32; two rows in flight with 8: 18.3 and 27.1.)
-constexpr int kJoinParts = 8;
+// pair that main CTA x recorded, a warp 8 columns of 32 rows.  Dependent accesses to
+// L2 are all it costs, so four parts are in flight at once, and where a pair has few
+// rows and many parts up to eight warps take every eighth part each.
+constexpr int kJoinParts = 8;  // CTAs per pair
+struct PfJoin {
+    float m = -FLT_MAX, l = 0.f;
+    float o[8] = {};
+    __device__ __forceinline__ void add(float2 ml, const float (&x)[8]) {
+        if (ml.y == 0.f) return;  // (the part saw no key of the row)
+        const float mn = fmaxf(m, ml.x);
+        const float keep = ex2_approx(m - mn), w = ex2_approx(ml.x - mn);
+        m = mn;
+        l = fmaf(l, keep, w * ml.y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = fmaf(o[k], keep, w * x[k]);
+    }
+};
 template <int D>
 __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
-    constexpr int LPR = D / 4, RPC = 256 / LPR;  // lanes per row, rows per CTA and pass
-    const int lane = threadIdx.x % LPR;
+    __shared__ float s_part[8][10][32];  // per warp: columns, maximum and sum of 32 rows
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int4 a = ld_dep(p.cut + 2 * blockIdx.x);
     const int4 e = ld_dep(p.cut + 2 * blockIdx.x + 1);
-    const int pieces = e.x;
+    const int pieces = e.x, rows = min(256, e.z - a.z);
     if (pieces <= 1) return;
-    for (int r = blockIdx.y * RPC + threadIdx.x / LPR; r < 256 && a.z + r < e.z; r += kJoinParts * RPC) {
+    const int units = (rows + 31) / 32 * (D / 8);
+    int ways = 1;  // warps to a unit; above 1 there is a warp for each
+    if (pieces > 4)
+        while (ways < 8 && 2 * ways * units <= kJoinParts * 8) ways *= 2;
+    const int way = warp % ways;
+    for (int u = (blockIdx.y * 8 + warp) / ways; u < units || ways > 1; u += kJoinParts * 8) {
+        const int r = u / (D / 8) * 32 + lane, d = u % (D / 8) * 8;
         // (rows of part k: CTA x + k's first slot, but for k = 0)
         const long long row0 = (long long)blockIdx.x * 512 + 256 * e.y + r;
         auto row = [&](int k) { return k == 0 ? row0 : (long long)(blockIdx.x + k) * 512 + r; };
-        float m = -FLT_MAX, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < pieces; k0 += 4) {
+        PfJoin j;
+        for (int k0 = way; k0 < pieces && r < rows; k0 += 4 * ways) {
             float2 ml[4];
-            float4 x[4];
+            float x[4][8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (k0 + u >= pieces) break;
-                ml[u] = ld_dep(reinterpret_cast<const float2*>(p.part_ml) + row(k0 + u));
-                x[u] = ld_dep(reinterpret_cast<const float4*>(p.part_o) + row(k0 + u) * LPR + lane);
+            for (int k = 0; k < 4; ++k) {
+                if (k0 + k * ways >= pieces) break;
+                const long long at = row(k0 + k * ways);
+                ml[k] = ld_dep(reinterpret_cast<const float2*>(p.part_ml) + at);
+                const float4* o = reinterpret_cast<const float4*>(p.part_o + pf_part_at(at, D, d));
+                *reinterpret_cast<float4*>(x[k]) = ld_dep(o);
+                *reinterpret_cast<float4*>(x[k] + 4) = ld_dep(o + 1);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (k0 + u >= pieces) break;
-                if (ml[u].y == 0.f) continue;  // (the part saw no key of the row)
-                const float mn = fmaxf(m, ml[u].x);
-                const float keep = ex2_approx(m - mn), w = ex2_approx(ml[u].x - mn);
-                m = mn;
-                l = fmaf(l, keep, w * ml[u].y);
-                o.x = fmaf(o.x, keep, w * x[u].x), o.y = fmaf(o.y, keep, w * x[u].y);
-                o.z = fmaf(o.z, keep, w * x[u].z), o.w = fmaf(o.w, keep, w * x[u].w);
+            for (int k = 0; k < 4; ++k)
+                if (k0 + k * ways < pieces) j.add(ml[k], x[k]);
+        }
+        if (ways > 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s_part[warp][k][lane] = j.o[k];
+            s_part[warp][8][lane] = j.m, s_part[warp][9][lane] = j.l;
+            __syncthreads();
+            if (way != 0) return;
+            for (int w = warp + 1; w < warp + ways; ++w) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = s_part[w][k][lane];
+                j.add(make_float2(s_part[w][8][lane], s_part[w][9][lane]), x);
             }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int f = a.z + r, tok = pf_div(p, f);
-        const long long orow = (long long)(a.w + tok) * p.H + a.y * p.G + (f - tok * p.G);
-        reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * D)[lane] =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (r < rows) {
+            const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
+            const int f = a.z + r, tok = pf_div(p, f);
+            const long long orow = (long long)(a.w + tok) * p.H + a.y * p.G + (f - tok * p.G);
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = pack_bf16x2(j.o[2 * k] * inv, j.o[2 * k + 1] * inv);
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D + d) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        if (ways > 1) return;
     }
 }
 
