@@ -1167,16 +1167,16 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
         p.part_ml = reinterpret_cast<float*>(ws + sh.ml_off);
         if (sh.grid) p.cut = reinterpret_cast<int4*>(ws + sh.cut_off);
     }
+    // division by G: with s = ceil(log2 G) and m = ceil(2^(31 + s) / G), x m
+    // >> (31 + s) is exact for x < 2^31 (m G - 2^(31 + s) < G <= 2^s)
+    p.div_shift = 31;
+    while ((1LL << (p.div_shift - 31)) < p.G) ++p.div_shift;
+    p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (g.dtype == 1) {
         if (int rc = pool_tmaps(pool)) return rc;
         p.slot_blk = pool->tma_slots[0];
         p.slot_layer = pool->tma_slots[1];
-        // division by G: with s = ceil(log2 G) and m = ceil(2^(31 + s) / G), x m
-        // >> (31 + s) is exact for x < 2^31 (m G - 2^(31 + s) < G <= 2^s)
-        p.div_shift = 31;
-        while ((1LL << (p.div_shift - 31)) < p.G) ++p.div_shift;
-        p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
         e = pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
     } else {
         e = pa::launch_prefill_f32(p, g.D, g.B, s);

@@ -131,9 +131,12 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
     float* sq = smem;
     float* ring = sq + BM * C::LQ;
     int* marks = reinterpret_cast<int*>(ring + 2 * C::STAGE);  // first NaN, +inf, -inf per column
-    __shared__ int s_at[2];
+    __shared__ int s_at[5];  // sequence, first row, first token, new tokens, context
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    auto token = [&](int row) {  // row / G (the host's multiplier, for rows below 2^31)
+        return (int)(((unsigned long long)(unsigned)row * p.div_mul) >> p.div_shift);
+    };
 
     // ---- the tile: sequence and first row; the last tiles first, of all KV heads (a
     // prompt's last rows see most: what starts late is short) ----
@@ -142,10 +145,10 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
         int left = gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv, found = -1, row0 = 0;
         for (int b0 = 0; b0 < p.batch && found < 0; b0 += 32) {
             const int b = b0 + lane;
-            int tiles = 0;
+            int tiles = 0, s0 = 0, s1 = 0, n = 0;
             if (b < p.batch) {
-                const int s0 = ld_dep(p.starts + b), s1 = ld_dep(p.starts + b + 1);
-                const int n = ld_dep(p.lens + b);
+                s0 = ld_dep(p.starts + b), s1 = ld_dep(p.starts + b + 1);
+                n = ld_dep(p.lens + b);
                 const bool good = s0 >= 0 && s1 >= s0 && s1 <= p.num_tokens;
                 if ((!good || n < 0 || n > p.maxb * B) && blockIdx.x == 0 && blockIdx.y == 0)
                     atomicOr(p.status, kStatusBadLength);
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
                 const int f = __ffs(hit) - 1;
                 found = b0 + f;
                 row0 = (left - (__shfl_sync(kFullMask, incl, f) - __shfl_sync(kFullMask, tiles, f))) * BM;
+                if (lane == f) s_at[2] = s0, s_at[3] = s1 - s0, s_at[4] = n;
             }
             left -= __shfl_sync(kFullMask, incl, 31);
         }
@@ -171,9 +175,8 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
     __syncthreads();
     const int b = s_at[0], row0 = s_at[1];
     if (b < 0) return;
-    const int start = ld_dep(p.starts + b);
-    const int n_new = ld_dep(p.starts + b + 1) - start;
-    int n = ld_dep(p.lens + b);
+    const int start = s_at[2], n_new = s_at[3];
+    int n = s_at[4];
     if (n < n_new || n > p.maxb * B) {
         if (tid == 0) atomicOr(p.status, kStatusBadLength);
         n = 0;
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
     const int rows = (int)min((long long)BM, (long long)n_new * p.G - row0);
     const int first_pos = n - n_new;
     // keys: this split's part of the tile's [0, last visible + 1)
-    const int see = n > 0 ? first_pos + (row0 + rows - 1) / p.G + 1 : 0;
+    const int see = n > 0 ? first_pos + token(row0 + rows - 1) + 1 : 0;
     const int key_tiles = (see + BN - 1) / BN;
     const int per = (key_tiles + p.splits - 1) / p.splits;
     const int kt0 = min((int)blockIdx.y * per, key_tiles), kt1 = min(kt0 + per, key_tiles);
@@ -191,13 +194,6 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
     const int cc = tid % CPR, cr = tid / CPR;
     const uint32_t q_at = smem_addr(sq) + (uint32_t)(cr * C::LQ + 4 * cc) * 4;
     const float* q = static_cast<const float*>(p.q);
-    for (int r = 0; r < BM; r += RPP) {
-        const int f = row0 + r + cr;
-        const bool live = r + cr < rows;
-        const int tok = live ? f / p.G : 0;
-        cp16(q_at + r * C::LQ * 4,
-             live ? q + ((long long)(start + tok) * p.H + kvh * p.G + f - tok * p.G) * D + 4 * cc : q, live);
-    }
     const float* kb = static_cast<const float*>(p.k_base) + p.tile_off + (long long)kvh * p.s_head + 4 * cc;
     const float* vb = static_cast<const float*>(p.v_base) + p.tile_off + (long long)kvh * p.s_head + 4 * cc;
     constexpr int PAGES = BN > B ? BN / B : 1;  // 1 or 2 per tile
@@ -235,7 +231,14 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    look_up(kt0);
+    look_up(kt0);  // (under the addresses of q)
+    for (int r = 0; r < BM; r += RPP) {
+        const int f = row0 + r + cr;
+        const bool live = r + cr < rows;
+        const int tok = live ? token(f) : 0;
+        cp16(q_at + r * C::LQ * 4,
+             live ? q + ((long long)(start + tok) * p.H + kvh * p.G + f - tok * p.G) * D + 4 * cc : q, live);
+    }
     copy(kt0);
 
     // this thread's rows: g and g + 8 of the warp's 16
@@ -244,14 +247,14 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int r = 16 * warp + g + 8 * h;
-        pos[h] = r < rows ? first_pos + (row0 + r) / p.G : -1;
+        pos[h] = r < rows ? first_pos + token(row0 + r) : -1;
     }
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-    const int tile_pos = first_pos + row0 / p.G;  // the tile's first row's position
+    const int tile_pos = first_pos + token(row0);  // the tile's first row's position
     const float* qw = sq + (16 * warp + g) * C::LQ + 4 * t;
 
     for (int kt = kt0; kt < kt1; ++kt) {
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
         l[h] += __shfl_xor_sync(kFullMask, l[h], 2);
         const int r = 16 * warp + g + 8 * h;
         if (r >= rows) continue;
-        const int f = row0 + r, tok = f / p.G;
+        const int f = row0 + r, tok = token(f);
         const float inv = p.cluster > 1 ? 1.f : l[h] == 0.f ? 0.f : 1.f / l[h];
         float* out = p.cluster > 1
                          ? part + r * LO
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
     const int rank = (int)cluster.block_rank();
     const int groups = p.splits / p.cluster;
     for (int x = rank * (kThreads / CPR) + cr; x < rows; x += p.cluster * (kThreads / CPR)) {
-        const int f = row0 + x, tok = f / p.G;
+        const int f = row0 + x, tok = token(f);
         const long long orow = (long long)(start + tok) * p.H + kvh * p.G + f - tok * p.G;
         Joined j;
 #pragma unroll
