@@ -445,21 +445,17 @@ __global__ void __launch_bounds__(kThreads, 3) pa_prefill_f32_kernel(const Prefi
         const int f = row0 + x, tok = token(f);
         const long long orow = (long long)(start + tok) * p.H + kvh * p.G + f - tok * p.G;
         Joined j;
+        float2 ml[8];
+        float4 v[8];
 #pragma unroll
-        for (int z0 = 0; z0 < 8; z0 += 4) {
-            if (z0 >= p.cluster) break;
-            float2 ml[4];
-            float4 v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int z = min(z0 + u, p.cluster - 1);
-                ml[u] = *cluster.map_shared_rank(part_ml + x, z);
-                v[u] = *cluster.map_shared_rank(reinterpret_cast<float4*>(part + x * LO) + cc, z);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (z0 + u < p.cluster) j.add(ml[u], v[u]);
+        for (int z = 0; z < 8; ++z) {
+            if (z >= p.cluster) break;
+            ml[z] = *cluster.map_shared_rank(part_ml + x, z);
+            v[z] = *cluster.map_shared_rank(reinterpret_cast<float4*>(part + x * LO) + cc, z);
         }
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+            if (z < p.cluster) j.add(ml[z], v[z]);
         if (groups == 1) {
             reinterpret_cast<float4*>(p.out)[orow * CPR + cc] = j.out();
         } else {
