@@ -572,7 +572,10 @@ PA_API int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const vo
  *   workspace     at least pa_prefill_workspace_size() bytes, 256-byte aligned
  *                 (may be NULL when that is 0); concurrent calls need separate
  *                 ones.
- * head_dim 64 or 128, block_size 16 or 32, any GQA group.  A bad table entry
+ * head_dim 64 or 128, block_size 16 or 32, any GQA group.  On bf16 pools short
+ * calls run on mma.sync and long ones on tcgen05; pa_pool_set_decode_kernel with
+ * PA_DECODE_TENSOR_CORES or PA_DECODE_TCGEN05 forces either (the workspace size
+ * follows).  A bad table entry
  * sets PA_STATUS_BAD_BLOCK_ID and its tokens get no weight (none left: a zero
  * row).
  * Cites: as pa_decode_attention ("vllmini", "The CUDA Block Kernel"), for more

@@ -23,7 +23,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["pa_api.cpp", "pa_aux.cu", "pa_decode_bf16.cu", "pa_decode_f32.cu",
            "pa_decode_noalloc.cu", "pa_alloc.cu", "pa_decode_mma.cu",
            "pa_decode_mma_wide.cu", "pa_decode_umma.cu", "pa_rope.cu",
-           "pa_prefill_f32.cu", "pa_prefill_umma.cu", "pa_pages.cu"]
+           "pa_prefill_mma.cu", "pa_prefill_umma.cu", "pa_pages.cu"]
 
 
 def _nvcc() -> str:

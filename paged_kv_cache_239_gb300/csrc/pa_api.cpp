@@ -946,11 +946,16 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
     if (int rc = num_sms_current(&sms)) return rc;
     const int G = num_heads / g.Hkv;
     size_t rows = 0;  // rows of partials
-    if (g.dtype == 1) {
+    const bool mma = g.dtype == 0 || (pool->decode_kernel == PA_DECODE_AUTO ||
+                                              pool->decode_kernel == PA_DECODE_CUDA_CORES
+                                          ? pa::prefill_mma_preferred(G, g.Hkv, batch, num_tokens, maxb, g.D,
+                                                                      g.B, sms)
+                                          : pool->decode_kernel == PA_DECODE_TENSOR_CORES);
+    if (!mma) {
         sh->grid = pa::prefill_umma_grid(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
         if (sh->grid > 1) rows = (size_t)sh->grid * 2 * 256;
     } else {
-        sh->splits = pa::prefill_f32_splits(G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms,
+        sh->splits = pa::prefill_mma_splits(g.dtype, G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms,
                                             &sh->cluster);
         const int groups = sh->splits / sh->cluster;
         if (groups > 1) rows = (size_t)groups * num_tokens * num_heads;
@@ -1173,13 +1178,13 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
     while ((1LL << (p.div_shift - 31)) < p.G) ++p.div_shift;
     p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (g.dtype == 1) {
+    if (sh.grid) {
         if (int rc = pool_tmaps(pool)) return rc;
         p.slot_blk = pool->tma_slots[0];
         p.slot_layer = pool->tma_slots[1];
         e = pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
     } else {
-        e = pa::launch_prefill_f32(p, g.D, g.B, s);
+        e = pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
     return PA_OK;

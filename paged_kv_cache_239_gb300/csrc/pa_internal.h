@@ -126,8 +126,8 @@ struct NormRopeParams {
     unsigned long long freq[kMaxRotaryPairs];  // turns per position, as fractions of 2^64
 };
 
-// Attention of several new tokens per sequence (see pa_prefill_umma.cuh for
-// bf16 pools, pa_prefill_f32.cu for fp32).
+// Attention of several new tokens per sequence (see pa_prefill_umma.cuh for long
+// calls on bf16 pools, pa_prefill_mma.cu for short ones and for fp32).
 struct PrefillParams {
     void* out;               // [num_tokens, H, D], pool dtype
     const void* q;           // [num_tokens, H, D], pool dtype
@@ -143,8 +143,8 @@ struct PrefillParams {
     float qscale;            // softmax scale * log2(e)
     float *part_o, *part_ml;
     unsigned* status;
-    int splits, cluster;     // fp32: parts of each context; of them a cluster's
-    int grid;                // bf16: persistent CTAs, and per CTA two int4: the
+    int splits, cluster;     // mma.sync: parts of each context; of them a cluster's
+    int grid;                // tcgen05: persistent CTAs, and per CTA two int4: the
     int4* cut;               // pair whose first part it holds while others go on
     int slot_blk, slot_layer;  // tensor-map dimensions of the pool's axes
     unsigned div_mul;        // x / G = x * div_mul >> div_shift for x < 2^31
@@ -185,10 +185,13 @@ struct CompactParams {
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, int D, int num_sms,
                              cudaStream_t s);
 bool prefill_supported(int dtype, int D, int B);
-// fp32: the splits of the contexts that a call's size asks for.
-int prefill_f32_splits(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
+// mma.sync: the splits of the contexts that a call's size asks for.
+int prefill_mma_splits(int dtype, int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
                        int num_sms, int* cluster);
-cudaError_t launch_prefill_f32(const PrefillParams& p, int D, int B, cudaStream_t s);
+// Whether a call on a bf16 pool takes the mma.sync kernel.
+bool prefill_mma_preferred(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
+                           int num_sms);
+cudaError_t launch_prefill_mma(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s);
 // bf16: the persistent grid; `tmaps` points to the pool's two CUtensorMap.
 int prefill_umma_grid(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms);
 cudaError_t launch_prefill_umma(const PrefillParams& p, const void* tmaps, int D, int B,

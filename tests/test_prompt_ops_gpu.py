@@ -186,6 +186,24 @@ def test_norm_rope_bad_inputs(cuda_device):
 # ----------------------------------------------------------------- prefill
 
 
+KERNEL = ["auto"]  # what run_prefill asks for on bf16 pools
+
+
+def pytest_generate_tests(metafunc):
+    if metafunc.function.__name__.startswith("test_prefill_"):
+        metafunc.parametrize("prefill_kernel", ["auto", "tensor_cores", "tcgen05"], indirect=True)
+
+
+@pytest.fixture(autouse=True)
+def prefill_kernel(request):
+    KERNEL[0] = getattr(request, "param", "auto")
+    params = request.node.callspec.params if hasattr(request.node, "callspec") else {}
+    if KERNEL[0] != "auto" and params.get("dtype") == "f32":
+        pytest.skip("one kernel serves fp32 pools")
+    yield
+    KERNEL[0] = "auto"
+
+
 def prefill_case(dev, dtype, d, block, h, hkv, new, ctx, seed=0, layers=1, layer=0, fill=None, maxb=None):
     """Pool (unused rows `fill`), tables and q of a ragged batch."""
     dt = DT[dtype]
@@ -209,6 +227,7 @@ def prefill_case(dev, dtype, d, block, h, hkv, new, ctx, seed=0, layers=1, layer
 def run_prefill(dev, pool_t, tables, q, new, ctx, scale=None, layer=0, pad=2):
     nb, _, layers, hkv, block, d = pool_t.shape
     cache = BlockPool(nb, block, layers, hkv, d, tensor=pool_t)
+    cache.set_decode_kernel(KERNEL[0])
     t = q.shape[0]
     qp = torch.cat((q, torch.full((pad,) + q.shape[1:], float("nan"), dtype=q.dtype, device=dev)))
     out = torch.full_like(qp, 7.0)
