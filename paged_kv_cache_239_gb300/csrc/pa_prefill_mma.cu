@@ -666,29 +666,31 @@ bool prefill_supported(int dtype, int D, int B) {
 }
 
 // Whether a call on a bf16 pool takes this kernel: the shorter of both estimates, in
-// us.  This one starts in 4 and takes 0.85 us of an SM for 64 rows x 64 keys of
-// head_dim 64 (2 of 128); the tcgen05 kernel and its join take 9, and 1.45 us for 256
+// us.  This one starts in 4 and takes 0.75 us of an SM for 64 rows x 64 keys of
+// head_dim 64 (1.7 of 128); the tcgen05 kernel and its join take 9, and 1.45 us for 256
 // rows x 128 keys, three such more per 256 rows.  (Measured, this / tcgen05: one token
-// over 100 keys, 16 heads on 2 of 64, 5.0 / 9.0; a prompt of 128 6.6 / 9.8, of 512 12.3
-// / 14.2, of 1,024 27.6 / 17.8; 32 sequences of 5 tokens over 2,000 23.2 / 21.6; 32
-// heads on 8 of 128: a prompt of 128 10.2 / 12.2, of 512 32.2 / 20.6.)
+// over 100 keys, 16 heads on 2 of 64, 4.8 / 8.9; a prompt of 128 6.6 / 9.7, of 512 11.9
+// / 14.3, of 1,024 19.0 / 17.9; 32 sequences of 5 tokens over 2,000 18.7 / 21.6; 32
+// heads on 8 of 128: 8 sequences of one token over 1,000 13.1 / 19.6, a prompt of 128
+// 10.1 / 12.0, of 512 22.1 / 20.7, 8 of 128 24.1 / 14.8.)
 bool prefill_mma_preferred(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
                            int num_sms) {
     const double keys = (double)maxb * B, rows = (double)num_tokens * G;
-    const double here = 4 + (rows / 64 + batch) * Hkv * (keys / 64) * (D == 64 ? 0.85 : 2.0) / num_sms;
+    const double here = 4 + (rows / 64 + batch) * Hkv * (keys / 64) * (D == 64 ? 0.75 : 1.7) / num_sms;
     const double there = 9 + (rows / 256 + batch) * Hkv * (3 + keys / 128) * 1.45 / num_sms;
     return here < there;
 }
 
 // Parts of each context (the host knows the tables' width, not the lengths).  Up to
-// eight are a cluster, which joins them by itself: as many as give every SM a CTA,
-// and up to eight CTAs where each part keeps three key tiles, since a prompt's row
-// tiles see few or many keys and short parts even that out (500 tokens of 16 heads
-// behind 7,300: 1 part 1250 us, 2 936, 4 670, 8 607); parts of less than three
-// tiles do not pay for the join once they share an SM (4 sequences of up to 130
-// tokens: 4 parts 20.7 us, 8 25.8).  More than eight take a second launch: where
-// two CTAs per SM ask for 16 and each has a tile (4 tokens over 30,000 keys: 152
-// parts 26 us, 256 33).
+// eight are a cluster, which joins them by itself: of 1, 2, 4 and 8 the one with the
+// shortest estimate.  A part takes its key tiles and 2.5 more (start, join); an SM's
+// share of them takes 0.62 of their times' sum, for three run at once, and half a part
+// more until all have ended.  (fp32, 1 / 2 / 4 / 8 parts: 500 tokens of 16 heads behind
+// 7,300, 125 row tiles, 1191 / 889 / 630 / 565 us; 4 sequences of up to 130 tokens, 38 row
+// tiles of 14 key tiles, 29.6 / 22.6 / 18.4 / 21.2; 24 of up to 212 behind 2,000 - 2,800, 672
+// row tiles, 1076 / 858 / 876 / 952.)  More than eight take a second launch: where two
+// CTAs per SM ask for 16 and each has a tile (4 tokens over 30,000 keys: 152 parts 26
+// us, 256 33).
 int prefill_mma_splits(int dtype, int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
                        int num_sms, int* cluster) {
     const int BN = dtype == 1 ? (D == 64 ? CoreBf16<64>::BN : CoreBf16<128>::BN)
@@ -696,14 +698,18 @@ int prefill_mma_splits(int dtype, int G, int Hkv, int batch, int num_tokens, int
     const long long tiles = ((long long)num_tokens * G / BM + batch) * Hkv;
     const long long keys = ((long long)maxb * B + BN - 1) / BN;  // tiles
     if (tiles <= 0) return *cluster = 1;
-    const long long one = num_sms / tiles;  // parts that get an SM each
     const long long wide = std::min({2 * num_sms / tiles, keys, 256LL});
     if (wide >= 16) {
         *cluster = 8;
         return (int)wide / 8 * 8;
     }
-    const long long n = std::min({8 * num_sms / tiles, keys, std::max(one, keys / 3)});
-    return *cluster = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
+    double best = 0;
+    for (int n = 1; n <= 8 && n <= keys; n *= 2) {
+        const double share = (double)tiles * n / num_sms;
+        const double time = ((double)keys / n + 2.5) * std::max(1.0, 0.62 * share + 0.5);
+        if (n == 1 || time < best) best = time, *cluster = n;
+    }
+    return *cluster;
 }
 
 cudaError_t launch_prefill_mma(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s) {
