@@ -1,5 +1,5 @@
 // pa_prefill_umma.cuh -- attention of several new tokens per sequence over a
-// bf16 paged cache on the 5th-generation tensor cores.
+// bf16 paged cache on the 5th-generation tensor cores: the calls that are not short.
 //
 //   out_t = sum_{s <= p_t} softmax_s(scale q_t . k_s) v_s,
 //   p_t = context_lens[b] - n_b + i for the i-th of sequence b's n_b new tokens.
@@ -43,16 +43,16 @@
 // cycles of the tensor pipe, and takes about 2750, since S(i + 1) waits for the
 // softmax of S(i) to leave the columns that P stands in, with 512 columns for two
 // row tiles' S and O (the exponentials, 2048 cycles of the special-function units,
-// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 379 us, 1.45 PFLOP/s of
-// the causal half (75 % of a large library product's burst rate).  Measured and
-// slower there: two threads to a row 450 us; two issuing threads 480; P handed over
-// in halves 409 (in three parts, as here, 400 by the same clock).  Without the
-// exponentials it would take 383.  Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to
-// 131,000: 169 us, 5.6 TB/s (83 % of a plain copy's rate), in shares cut to the tile.
-// Short calls: latency; one token over 100 keys takes 8.9 us, of which 2.5 go to
-// the schedule (its code is fetched by every SM), 2.5 to the first K tile and its
-// scores, and 2.5 to the join's launch; 8 chunks of up to 513 tokens with 16 heads
-// on 2 of 64: 27 us, of which 11 are those, 9 five to seven tiles.
+// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 371 us, 1.48 PFLOP/s of
+// the causal half (77 % of a large library product's burst rate).  Measured and
+// slower, at a time when this form took 400: two threads to a row 450; two issuing
+// threads 480; P handed over in halves 409.  Without the exponentials it took 383.
+// Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 167
+// us, 5.6 TB/s (84 % of a plain copy's rate), in shares cut to the tile.  Short calls:
+// latency (pa_prefill_mma.cu takes the shortest); one token over 100 keys takes 8.9 us,
+// of which 2.5 go to the schedule (its code is fetched by every SM), 2.5 to the first
+// K tile and its scores, and 2.5 to the join's launch; 8 chunks of up to 513 tokens
+// with 16 heads on 2 of 64: 25 us, of which 9 are five to seven tiles.
 //
 // The shares charge a pair kPairUnits tiles: a tile costs about 2,930 cycles and a
 // pair 9,500 more (Q, the first scores, the output).  With 2 the last CTA of a batch
