@@ -573,9 +573,8 @@ PA_API int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const vo
  *                 (may be NULL when that is 0); concurrent calls need separate
  *                 ones.
  * head_dim 64 or 128, block_size 16 or 32, any GQA group.  On bf16 pools short
- * calls run on mma.sync and long ones on tcgen05; pa_pool_set_decode_kernel with
- * PA_DECODE_TENSOR_CORES or PA_DECODE_TCGEN05 forces either (the workspace size
- * follows).  A bad table entry
+ * calls run on mma.sync and long ones on tcgen05 (see pa_pool_set_prefill_kernel).
+ * A bad table entry
  * sets PA_STATUS_BAD_BLOCK_ID and its tokens get no weight (none left: a zero
  * row).
  * Cites: as pa_decode_attention ("vllmini", "The CUDA Block Kernel"), for more
@@ -586,6 +585,19 @@ PA_API int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, i
                                 const int* context_lens, const int* query_starts, int batch,
                                 int num_tokens, int num_heads, float scale, void* workspace,
                                 size_t workspace_bytes, pa_stream_t stream);
+
+/* Which kernel a pool's prefill attention uses.  PA_PREFILL_AUTO (default): fp32
+ * pools mma.sync (TF32 products of split operands); bf16 pools mma.sync for calls
+ * that its short start makes faster, by an estimate from the sizes, else tcgen05.
+ * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at the call.
+ * The workspace size follows the choice.
+ * Cites: no counterpart on the pages (a choice among this library's kernels). */
+enum {
+    PA_PREFILL_AUTO = 0,
+    PA_PREFILL_MMA = 1,
+    PA_PREFILL_TCGEN05 = 2
+};
+PA_API int pa_pool_set_prefill_kernel(pa_pool* pool, int kind);
 
 /* Workspace bytes of pa_prefill_attention for these sizes on the current
  * device (0 when nothing is split).

@@ -27,6 +27,9 @@ PA_DECODE_AUTO = 0
 PA_DECODE_CUDA_CORES = 1
 PA_DECODE_TENSOR_CORES = 2
 PA_DECODE_TCGEN05 = 3
+PA_PREFILL_AUTO = 0
+PA_PREFILL_MMA = 1
+PA_PREFILL_TCGEN05 = 2
 
 PA_DTYPE_F32 = 0
 PA_DTYPE_BF16 = 1
@@ -88,6 +91,7 @@ _SIGNATURES = {
     "pa_pool_destroy": ([_P], _I),
     "pa_pool_block_bytes": ([_P, _PSZ], _I),
     "pa_pool_set_decode_kernel": ([_P, _I], _I),
+    "pa_pool_set_prefill_kernel": ([_P, _I], _I),
     "pa_decode_kernel_choice": ([_P, _I, _PI], _I),
     "pa_pool_seed_free_stack": ([_P, _P, _I], _I),
     "pa_alloc_block": ([_P, _PI], _I),
@@ -456,6 +460,10 @@ def pa_prefill_attention(out, q, pool: int, layer: int, block_tables, max_blocks
         _ptr(out), _ptr(q), pool, layer, _ptr(block_tables), max_blocks_per_seq,
         _ptr(context_lens), _ptr(query_starts), batch, num_tokens, num_heads, scale,
         _ptr(workspace), workspace_bytes, _stream(stream)), "pa_prefill_attention")
+
+
+def pa_pool_set_prefill_kernel(pool: int, kind: int) -> None:
+    _check(lib().pa_pool_set_prefill_kernel(pool, kind), "pa_pool_set_prefill_kernel")
 
 
 def pa_prefill_workspace_size(pool: int, batch: int, num_tokens: int, num_heads: int,

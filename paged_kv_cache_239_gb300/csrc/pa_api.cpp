@@ -23,6 +23,7 @@ struct pa_pool {
     std::vector<unsigned char> in_use;  // 1 while a block is handed out
     bool on_device = false;             // the stack is held in a device copy
     int decode_kernel = PA_DECODE_AUTO;
+    int prefill_kernel = PA_PREFILL_AUTO;
     // tensor maps of the bf16 pool (K, V) for the tensor-core kernel, encoded
     // on first use
     mutable CUtensorMap tmaps[2];
@@ -940,17 +941,23 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
                     "no prefill kernel for dtype=%d head_dim=%d block_size=%d (built: head_dim "
                     "64/128, block_size 16/32)",
                     g.dtype, g.D, g.B);
+    int kind;
+    {
+        std::lock_guard<std::mutex> lock(pool->mu);
+        kind = pool->prefill_kernel;
+    }
+    if (g.dtype != 1 && kind == PA_PREFILL_TCGEN05)
+        return fail(PA_ERR_UNSUPPORTED, "the tcgen05 prefill kernel serves bf16 pools");
     *sh = PrefillShape();
     if (batch == 0 || num_tokens == 0) return PA_OK;
     int sms = 0;
     if (int rc = num_sms_current(&sms)) return rc;
     const int G = num_heads / g.Hkv;
     size_t rows = 0;  // rows of partials
-    const bool mma = g.dtype == 0 || (pool->decode_kernel == PA_DECODE_AUTO ||
-                                              pool->decode_kernel == PA_DECODE_CUDA_CORES
-                                          ? pa::prefill_mma_preferred(G, g.Hkv, batch, num_tokens, maxb, g.D,
-                                                                      g.B, sms)
-                                          : pool->decode_kernel == PA_DECODE_TENSOR_CORES);
+    const bool mma = kind == PA_PREFILL_AUTO
+                         ? g.dtype == 0 || pa::prefill_mma_preferred(G, g.Hkv, batch, num_tokens, maxb,
+                                                                     g.D, g.B, sms)
+                         : kind == PA_PREFILL_MMA;
     if (!mma) {
         sh->grid = pa::prefill_umma_grid(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
         if (sh->grid > 1) rows = (size_t)sh->grid * 2 * 256;
@@ -1111,6 +1118,15 @@ int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const void* q, 
     }
     e = pa::launch_norm_rope(p, g.dtype, g.D, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "pa_norm_rope_write_kv launch");
+    return PA_OK;
+}
+
+int pa_pool_set_prefill_kernel(pa_pool* pool, int kind) {
+    if (int rc = check_pool(pool)) return rc;
+    if (kind < PA_PREFILL_AUTO || kind > PA_PREFILL_TCGEN05)
+        return fail(PA_ERR_INVALID_ARG, "unknown prefill kernel %d", kind);
+    std::lock_guard<std::mutex> lock(pool->mu);
+    pool->prefill_kernel = kind;
     return PA_OK;
 }
 

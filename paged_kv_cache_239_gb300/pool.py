@@ -17,6 +17,7 @@ from . import binding as B
 
 _DECODE_KERNELS = {"auto": B.PA_DECODE_AUTO, "cuda_cores": B.PA_DECODE_CUDA_CORES,
                    "tensor_cores": B.PA_DECODE_TENSOR_CORES, "tcgen05": B.PA_DECODE_TCGEN05}
+_PREFILL_KERNELS = {"auto": B.PA_PREFILL_AUTO, "mma": B.PA_PREFILL_MMA, "tcgen05": B.PA_PREFILL_TCGEN05}
 
 
 class BlockPool:
@@ -185,6 +186,10 @@ class BlockPool:
                                 block_tables, maxb, context_lens, query_starts, batch, tokens,
                                 num_heads, stream)
         return out
+
+    def set_prefill_kernel(self, kind: str) -> None:
+        """'auto' (default), 'mma' or 'tcgen05' (bf16 pools)."""
+        B.pa_pool_set_prefill_kernel(self.handle, _PREFILL_KERNELS[kind])
 
     def prefill_workspace_size(self, batch: int, num_tokens: int, num_heads: int,
                                max_blocks_per_seq: int) -> int:

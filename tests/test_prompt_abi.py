@@ -119,6 +119,13 @@ def test_prefill_refusals(pa_lib, pool):
     refused(B, B.PA_ERR_UNSUPPORTED, B.pa_prefill_workspace_size, odd, 1, 1, 2, 4)
     B.pa_pool_destroy(odd)
     assert B.pa_prefill_workspace_size(pool, 0, 0, 4, 4) == 0
+    for kind in (-1, 3):
+        refused(B, bad, B.pa_pool_set_prefill_kernel, pool, kind)
+    refused(B, bad, B.pa_pool_set_prefill_kernel, None, B.PA_PREFILL_AUTO)
+    wide = B.pa_pool_create(F, 4, 1, 2, 16, 64, B.PA_DTYPE_F32)
+    B.pa_pool_set_prefill_kernel(wide, B.PA_PREFILL_TCGEN05)
+    refused(B, B.PA_ERR_UNSUPPORTED, call, pool=wide)
+    B.pa_pool_destroy(wide)
 
 
 def test_page_refusals(pa_lib, pool):

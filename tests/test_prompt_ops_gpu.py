@@ -191,7 +191,7 @@ KERNEL = ["auto"]  # what run_prefill asks for on bf16 pools
 
 def pytest_generate_tests(metafunc):
     if metafunc.function.__name__.startswith("test_prefill_"):
-        metafunc.parametrize("prefill_kernel", ["auto", "tensor_cores", "tcgen05"], indirect=True)
+        metafunc.parametrize("prefill_kernel", ["auto", "mma", "tcgen05"], indirect=True)
 
 
 @pytest.fixture(autouse=True)
@@ -227,7 +227,7 @@ def prefill_case(dev, dtype, d, block, h, hkv, new, ctx, seed=0, layers=1, layer
 def run_prefill(dev, pool_t, tables, q, new, ctx, scale=None, layer=0, pad=2):
     nb, _, layers, hkv, block, d = pool_t.shape
     cache = BlockPool(nb, block, layers, hkv, d, tensor=pool_t)
-    cache.set_decode_kernel(KERNEL[0])
+    cache.set_prefill_kernel(KERNEL[0])
     t = q.shape[0]
     qp = torch.cat((q, torch.full((pad,) + q.shape[1:], float("nan"), dtype=q.dtype, device=dev)))
     out = torch.full_like(qp, 7.0)
