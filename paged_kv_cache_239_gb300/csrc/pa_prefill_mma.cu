@@ -668,8 +668,8 @@ bool prefill_supported(int dtype, int D, int B) {
 // Whether a call on a bf16 pool takes this kernel: the shorter of both estimates, in
 // us.  This one starts in 4 and takes 0.75 us of an SM for 64 rows x 64 keys of
 // head_dim 64 (1.7 of 128); the tcgen05 kernel and its join take 9 (12 where
-// every 256 rows' keys are cut among SMs), and 1.45 us for 256 rows x 128 keys, three
-// such more per 256 rows.  (Measured, this / tcgen05: one token
+// every 256 rows' keys are cut among SMs), and 1.45 us for 256 rows x 128 keys (0.95
+// for up to 128 rows of 64), three such more per 256 rows.  (Measured, this / tcgen05: one token
 // over 100 keys, 16 heads on 2 of 64, 4.8 / 8.9; a prompt of 128 6.6 / 9.7, of 512 11.9
 // / 14.3, of 1,024 19.0 / 17.9; 32 sequences of 5 tokens over 2,000 18.7 / 21.6; 32
 // heads on 8 of 128: 8 sequences of one token over 1,000 13.1 / 19.6, a prompt of 128
@@ -679,7 +679,8 @@ bool prefill_mma_preferred(int G, int Hkv, int batch, int num_tokens, int maxb, 
     const double keys = (double)maxb * B, rows = (double)num_tokens * G;
     const double here = 4 + (rows / 64 + batch) * Hkv * (keys / 64) * (D == 64 ? 0.75 : 1.7) / num_sms;
     const double pairs = (rows / 256 + batch) * Hkv;
-    const double there = (pairs < num_sms ? 12 : 9) + pairs * (3 + keys / 128) * 1.45 / num_sms;
+    const double tile = D == 64 && rows <= 128.0 * batch ? 0.95 : 1.45;
+    const double there = (pairs < num_sms ? 12 : 9) + pairs * (3 + keys / 128) * tile / num_sms;
     return here < there;
 }
 

@@ -10,10 +10,10 @@ namespace pa {
 
 namespace {
 
-template <int D, int B>
-cudaError_t launch_inst(const PrefillParams& p, const CUtensorMap* tm, cudaStream_t s) {
+template <int D, int B, bool TURNS>
+cudaError_t launch_turns(const PrefillParams& p, const CUtensorMap* tm, cudaStream_t s) {
     using C = PrefillCfg<D, B>;
-    auto kern = pa_prefill_umma_kernel<D, B>;
+    auto kern = pa_prefill_umma_kernel<D, B, TURNS>;
     static std::mutex mu;
     static unsigned long long done_mask = 0;
     int dev = 0;
@@ -38,6 +38,16 @@ cudaError_t launch_inst(const PrefillParams& p, const CUtensorMap* tm, cudaStrea
     if (e != cudaSuccess || p.grid == 1) return e;
     return launch_pdl(pa_prefill_umma_join_kernel<D>, dim3((unsigned)p.grid, kJoinParts),
                       dim3(256), 0, s, p);
+}
+
+// Calls with 128 rows to a sequence on average, or fewer, take the kernel in which
+// both softmax groups serve a single row tile in turns (3 - 5 tokens over 4 long
+// contexts: 152 us, 167 without); it has more code, which costs calls of many pairs
+// of row tiles 5 - 15 %, so they take the one without.
+template <int D, int B>
+cudaError_t launch_inst(const PrefillParams& p, const CUtensorMap* tm, cudaStream_t s) {
+    return (long long)p.num_tokens * p.G <= 128LL * p.batch ? launch_turns<D, B, true>(p, tm, s)
+                                                            : launch_turns<D, B, false>(p, tm, s);
 }
 
 }  // namespace

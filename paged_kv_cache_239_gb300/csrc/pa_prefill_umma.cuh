@@ -29,7 +29,11 @@
 //    exchange between threads: S from tensor memory, running maximum (raised,
 //    and O rescaled, only when a score exceeds it by more than 2^8: any
 //    reference point gives the same normalised result), P as bf16 over S's own
-//    columns, sums in fp32, and at the end of a piece O / l to the output.
+//    columns, sums in fp32, and at the end of a piece O / l to the output.  A pair
+//    with one row tile and several key tiles is served by both groups in turns, each
+//    with an S and an O of its own: the chain S, softmax, P V of one tile, which is
+//    longer than its K and V take to arrive, runs under the other group's; at the end
+//    both groups learn the other's sums, and each joins half of the columns.
 // P in bf16: its rounding (2^-9 relative on average over many keys) is of the
 // size of the output's own; the sum l takes the weights before that rounding.
 //
@@ -43,12 +47,13 @@
 // cycles of the tensor pipe, and takes about 2750, since S(i + 1) waits for the
 // softmax of S(i) to leave the columns that P stands in, with 512 columns for two
 // row tiles' S and O (the exponentials, 2048 cycles of the special-function units,
-// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 371 us, 1.48 PFLOP/s of
-// the causal half (77 % of a large library product's burst rate).  Measured and
+// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 366 us, 1.50 PFLOP/s of
+// the causal half (78 % of a large library product's burst rate).  Measured and
 // slower, at a time when this form took 400: two threads to a row 450; two issuing
 // threads 480; P handed over in halves 409.  Without the exponentials it took 383.
-// Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 167
-// us, 5.6 TB/s (84 % of a plain copy's rate), in shares cut to the tile.  Short calls:
+// Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 152
+// us, 6.2 TB/s (92 % of a plain copy's rate; 167 us without turns), in shares cut to
+// the tile.  Short calls:
 // latency (pa_prefill_mma.cu takes the shortest); one token over 100 keys takes 8.9 us,
 // of which 2.5 go to the schedule (its code is fetched by every SM), 2.5 to the first
 // K tile and its scores, and 2.5 to the join's launch; 8 chunks of up to 513 tokens
@@ -85,7 +90,7 @@ struct PrefillCfg {
     static constexpr int OFF_Q = NS * TILE;
     static constexpr int OFF_CTRL = OFF_Q + 2 * TILE;
     // ctrl (bytes): barriers | TMEM address, abort, mark_piece, done[2] | box bits
-    // per stage | schedule (72 bytes) | the producers' page ids | pieces [NP] | marks [3][D]
+    // of eight tiles | schedule (72 bytes) | the producers' page ids | pieces [NP] | marks [3][D]
     // (the schedule's scratch before)
     static constexpr int NP = 4;
     static constexpr int TMEM_SLOT = 384, ABORT = 388, MARK_PIECE = 392, DONE = 396, BITS = 404,
@@ -100,7 +105,8 @@ struct PrefillCfg {
                          S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6,  // three parts, [part][row tile]
                          PV_DONE = Q_FULL + 12, FINAL = Q_FULL + 14,
                          V_LOOK = Q_FULL + 15, V_CLEAN = Q_FULL + 16,
-                         PC_FULL = Q_FULL + 17, PC_EMPTY = PC_FULL + NP, NBAR = PC_EMPTY + NP;
+                         PC_FULL = Q_FULL + 17, PC_EMPTY = PC_FULL + NP,
+                         X_SUMS = PC_EMPTY + NP, X_READ = X_SUMS + 1, NBAR = X_READ + 1;
     static_assert(NBAR * 8 <= TMEM_SLOT && NS <= 11, "ctrl layout");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
@@ -173,6 +179,8 @@ struct alignas(16) PfPiece {
     int n, pair_pos, b, flags;  // context; position of the pair's first row; sequence
     __device__ __forceinline__ bool whole() const { return flags & 1; }
     __device__ __forceinline__ bool first() const { return flags & 2; }
+    // one row tile and several key tiles: both softmax groups serve it in turns
+    __device__ __forceinline__ bool turns() const { return nj == 1 && kt1 - kt0 >= 4; }
 };
 
 struct PfWalk {
@@ -550,7 +558,7 @@ __device__ __forceinline__ float poison(const int* marks, int D, int d, int pos)
     return n || (a && b) ? NAN : a ? INFINITY : b ? -INFINITY : 0.f;
 }
 
-template <int D, int B>
+template <int D, int B, bool TURNS>
 __global__ void __launch_bounds__(384, 1)
     pa_prefill_umma_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv,
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(384, 1)
     volatile int* abort_all = reinterpret_cast<volatile int*>(ctrl + C::ABORT);
     PfPiece* pieces = reinterpret_cast<PfPiece*>(ctrl + C::PIECES);
     volatile int* mark_piece = reinterpret_cast<volatile int*>(ctrl + C::MARK_PIECE);
-    volatile int* done = reinterpret_cast<volatile int*>(ctrl + C::DONE);  // pieces, per softmax group
+    volatile int* done = reinterpret_cast<volatile int*>(ctrl + C::DONE);  // pieces, per softmax group's warp
     volatile int* box_bits = reinterpret_cast<volatile int*>(ctrl + C::BITS);
     int* marks = reinterpret_cast<int*>(ctrl + C::MARKS);
     const int warp = threadIdx.x >> 5;
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < C::NBAR; ++i) {
             const bool p_full = i >= C::P_FULL && i < C::P_FULL + 6;
             const bool pc_empty = i >= C::PC_EMPTY && i < C::PC_EMPTY + C::NP;
-            mbar_init(bar0 + 8 * i, p_full ? 4 : pc_empty ? 11 : 1);
+            mbar_init(bar0 + 8 * i, p_full ? 4 : pc_empty ? 11 : i >= C::X_SUMS ? 8 : 1);
         }
         *abort_all = 0, *mark_piece = -1, done[0] = 0, done[1] = 0;
         fence_mbar_init();
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(384, 1)
                     // cost the warp several times the instructions)
                     if (elect_one()) {
                         const uint32_t fb = bar0 + 8 * (C::KV_FULL + stage);
-                        if (kv) box_bits[stage] = (int)vmask;
+                        if (!kv) box_bits[(seq >> 1) & 7] = (int)vmask;
                         mbar_arrive_expect_tx(fb, (uint32_t)__popc(vmask) * C::NH * 2048u);
                         const int4 lo = *reinterpret_cast<const int4*>(blocks);
                         const int4 hi = *reinterpret_cast<const int4*>(blocks + 4);
@@ -740,8 +748,8 @@ __global__ void __launch_bounds__(384, 1)
                 int seq = 0, npj[2] = {0, 0}, nqj[2] = {0, 0}, nclean = 0;
                 bool ok = true;
                 auto stage_full = [&](int s) { return wait(C::KV_FULL + s % C::NS, (s / C::NS) & 1); };
-                auto score = [&](int j, int s) {  // S_j = Q_j K^T, K in stage s
-                    const uint64_t a = dQ + (uint64_t)((j * C::TILE) >> 4);
+                auto score = [&](int j, int q, int s) {  // S_j = Q_q K^T, K in stage s
+                    const uint64_t a = dQ + (uint64_t)((q * C::TILE) >> 4);
                     const uint64_t b = dK + (uint64_t)(((s % C::NS) * C::TILE) >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
@@ -763,20 +771,28 @@ __global__ void __launch_bounds__(384, 1)
                         ok = wait(C::Q_FULL + j, nqj[j] & 1);
                         ++nqj[j];
                     }
-                    if (!ok || !(ok = stage_full(seq))) break;
-                    tc_fence_after();
-                    if (pf_unclean(pc, pc.kt0)) mbar_arrive(bar0 + 8 * C::V_LOOK);
+                    if (!ok) break;
+                    // in turns, tile i is group i % 2's, and S runs two tiles ahead
+                    const bool turns = TURNS && pc.turns();
+                    const int ahead = turns ? 2 : 1;
 #pragma unroll 1
-                    for (int j = 0; j < pc.nj; ++j) {
-                        score(j, seq);
-                        if (nk == 1) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
+                    for (int i = 0; i < ahead && ok; ++i) {
+                        if (!(ok = stage_full(seq + 2 * i))) break;
+                        tc_fence_after();
+                        if (i == 0 && pf_unclean(pc, pc.kt0)) mbar_arrive(bar0 + 8 * C::V_LOOK);
+#pragma unroll 1
+                        for (int j = 0; j < pc.nj; ++j) {
+                            score(turns ? i : j, j, seq + 2 * i);
+                            if (nk == 1) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
+                        }
+                        umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 2 * i) % C::NS));
                     }
-                    umma_commit(bar0 + 8 * (C::KV_EMPTY + seq % C::NS));
 #pragma unroll 1
                     for (int i = 0; i < nk && ok; ++i, seq += 2) {
                         const uint64_t v = dV + (uint64_t)((((seq + 1) % C::NS) * C::TILE) >> 4);
 #pragma unroll 1
                         for (int j = 0; j < pc.nj && ok; ++j) {
+                            const int g = turns ? i & 1 : j;
                             // by the parts of P as they come: the exponentials of
                             // the rest are still under way
                             if (j == 0) {
@@ -786,29 +802,29 @@ __global__ void __launch_bounds__(384, 1)
                             }
 #pragma unroll
                             for (int part = 0; part < 3; ++part) {
-                                if (!ok || !(ok = wait(C::P_FULL + 2 * part + j, npj[j] & 1))) break;
+                                if (!ok || !(ok = wait(C::P_FULL + 2 * part + g, npj[g] & 1))) break;
                                 tc_fence_after();
 #pragma unroll
                                 for (int k = part ? 2 + 2 * part : 0; k < 4 + 2 * part; ++k)
-                                    umma_bf16_ts(tmem + C::O_COL + j * D, tmem + j * 128 + k * 8,
+                                    umma_bf16_ts(tmem + C::O_COL + g * D, tmem + g * 128 + k * 8,
                                                  v + (uint64_t)(k * (2048 >> 4)), IDV,
-                                                 (i > 0 || k > 0) ? 1u : 0u);
+                                                 (i >= ahead || k > 0) ? 1u : 0u);
                             }
                             if (!ok) break;
-                            ++npj[j];
-                            umma_commit(bar0 + 8 * (C::PV_DONE + j));
+                            ++npj[g];
+                            umma_commit(bar0 + 8 * (C::PV_DONE + g));
                             if (j == pc.nj - 1)
                                 umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 1) % C::NS));
-                            if (i + 1 < nk) {
-                                if (j == 0) {
-                                    if (!(ok = stage_full(seq + 2))) break;
-                                    if (pf_unclean(pc, pc.kt0 + i + 1)) mbar_arrive(bar0 + 8 * C::V_LOOK);
-                                }
+                            // (one look asked for at a time)
+                            if (j == 0 && i + 1 < nk && pf_unclean(pc, pc.kt0 + i + 1))
+                                mbar_arrive(bar0 + 8 * C::V_LOOK);
+                            if (i + ahead < nk) {
+                                const int ks = seq + 2 * ahead;
+                                if (j == 0 && !(ok = stage_full(ks))) break;
                                 tc_fence_after();
-                                score(j, seq + 2);
-                                if (i + 2 == nk) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
-                                if (j == pc.nj - 1)
-                                    umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 2) % C::NS));
+                                score(g, j, ks);
+                                if (i + ahead + 1 == nk) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
+                                if (j == pc.nj - 1) umma_commit(bar0 + 8 * (C::KV_EMPTY + ks % C::NS));
                             }
                         }
                     }
@@ -921,7 +937,7 @@ __global__ void __launch_bounds__(384, 1)
                         if (mark_at != piece) {
                             // (the softmax warps may still be reading the last marks)
 #pragma unroll 1
-                            for (int n = 0; (done[0] < piece - 1 || done[1] < piece - 1) && !*abort_all &&
+                            for (int n = 0; (done[0] < 4 * (piece - 1) || done[1] < 4 * (piece - 1)) && !*abort_all &&
                                             n < (1 << 24); ++n)
                                 __nanosleep(100);
 #pragma unroll 1
@@ -967,8 +983,8 @@ __global__ void __launch_bounds__(384, 1)
         // that -inf stays -inf)
         const float qs = fmaxf(fabsf(p.qscale), FLT_MIN);
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        int seq = 0, ns = 0;                       // V stage; tiles of this row tile so far
-        int piece = 0;
+        int seq = 0, ns = 0;                       // K stage; tiles of this row tile so far
+        int piece = 0, nturns = 0;
         bool ok = true;
         while (ok) {
             const int slot = np % C::NP;
@@ -980,34 +996,35 @@ __global__ void __launch_bounds__(384, 1)
             if (pc.nj == 0) break;
             ++piece;
             const int nk = pc.kt1 - pc.kt0;
-            if (j >= pc.nj) {
+            const bool turns = TURNS && pc.turns();
+            if (j >= pc.nj && !turns) {
                 seq += 2 * nk;
-                if (r == 0) done[j] = piece;
+                if (lane == 0) atomicAdd(const_cast<int*>(done) + j, 1);
                 continue;
             }
-            const int f = pc.row0 + 128 * j + r;
+            const int f = pc.row0 + (turns ? 0 : 128 * j) + r;
+            const int i0 = turns ? j : 0, step = turns ? 2 : 1;
             const bool live = f < pc.rows;
             const int tok = pf_div(p, f);
             const int pos = live ? pc.first_pos + tok : -1;
             float m = -FLT_MAX;   // reference point of the exponentials (scaled, base 2)
             float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int i = 0; i < nk; ++i, seq += 2, ++ns) {
+            for (int i = i0; i < nk; i += step, ++ns) {
                 const int t0 = (pc.kt0 + i) * C::TT;
-                const int vstage = (seq + 1) % C::NS;
-                // (V's arrival carries the tile's box bits)
-                ok = wait(C::KV_FULL + vstage, ((seq + 1) / C::NS) & 1) && wait(C::S_FULL + j, ns & 1);
+                ok = wait(C::S_FULL + j, ns & 1);
                 ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const unsigned bits = (unsigned)box_bits[vstage] & 0xffu;
+                // (with S, so its K, arrived; eight tiles are kept, the ring holds four)
+                const unsigned bits = (unsigned)box_bits[((seq >> 1) + i) & 7] & 0xffu;
                 // keys 0 .. lim of the tile are the row's, in pages that are there
                 const int lim = pos - t0;
                 const bool masked = __any_sync(kFullMask, lim < 127) || bits != 0xffu;
                 // settles the row's reference point: 0, it stays; 1, raised, the
                 // sum and O scaled down; -1, stop
                 auto raise = [&](float mt) {
-                    if (i == 0) {
+                    if (i == i0) {
                         m = mt;
                         return 1;
                     }
@@ -1050,29 +1067,73 @@ __global__ void __launch_bounds__(384, 1)
                 if (!ok) break;
             }
             if (!ok) break;
+            seq += 2 * nk;
             // ------------------------------------------------ the piece's output
             ok = __all_sync(kFullMask, wait(C::PV_DONE + j, (ns - 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            const float l = l2.x + l2.y;
-            const float inv = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            float l = l2.x + l2.y;
             const long long orow =
                 live ? (long long)(pc.start + tok) * p.H + pc.kvh * p.G + (f - tok * p.G) : 0;
-            const long long part = ((long long)blockIdx.x * 2 + (pc.first() ? 0 : 1)) * C::ROWS + 128 * j + r;
+            const long long part = ((long long)blockIdx.x * 2 + (pc.first() ? 0 : 1)) * C::ROWS +
+                                   (turns ? 0 : 128 * j) + r;
+            // In turns, each group has the sums of its own tiles: both learn the other's
+            // maxima and sums, through the rows that a second row tile would have in the
+            // workspace, and each joins and writes half of the columns.
+            float w0 = 1.f, w1 = 0.f;
+            const int col0 = turns ? j * (D / 2) : 0;
+            if (turns) {
+                float2* ml = reinterpret_cast<float2*>(p.part_ml) + part;
+                __stcg(ml + 128 * j, make_float2(m, l));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar0 + 8 * C::X_SUMS);
+                if (!(ok = __all_sync(kFullMask, wait(C::X_SUMS, nturns & 1)))) break;
+                tc_fence_after();
+                const float2 other = __ldcg(ml + 128 * (1 - j));
+                const float top = fmaxf(m, other.x);
+                const float mine = ex2_approx(m - top), theirs = ex2_approx(other.x - top);
+                w0 = j == 0 ? mine : theirs, w1 = j == 0 ? theirs : mine;
+                m = top, l = fmaf(l, mine, other.y * theirs);
+            }
+            const float inv = pc.whole() ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            w0 *= inv, w1 *= inv;
             float oall[D / 32][32];  // (all loads in flight at once)
+            if (turns) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) tmem_ld32(o_col + 32 * c, oall[c]);
+                for (int c = 0; c < D / 64; ++c) {
+                    tmem_ld32(trow + C::O_COL + col0 + 32 * c, oall[c]);
+                    tmem_ld32(trow + C::O_COL + D + col0 + 32 * c, oall[D / 64 + c]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) tmem_ld32(o_col + 32 * c, oall[c]);
+            }
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) tmem_loaded32(oall[c]);
+            if (turns) {
+                // (the other group's O may be overwritten once both have it)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar0 + 8 * C::X_READ);
+                if (!(ok = __all_sync(kFullMask, wait(C::X_READ, nturns & 1)))) break;
+                tc_fence_after();
+                ++nturns;
+            }
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float (&o)[32] = oall[c / 32];
+            for (int c = 0; c < D / 32; ++c) {
+                float (&o)[32] = oall[c];
+                if (c >= D / 64 && turns) break;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= inv;
+                for (int k = 0; k < 32; ++k) {
+                    o[k] *= w0;
+                    if (c < D / 64 && turns) o[k] = fmaf(oall[D / 64 + c % (D / 64)][k], w1, o[k]);
+                }
+                const int col = col0 + 32 * c;
                 if (live && pc.whole()) {
                     // (whole sectors per thread: the rows of a warp lie apart)
-                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D + c;
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + orow * D + col;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t v[8];
@@ -1087,7 +1148,7 @@ __global__ void __launch_bounds__(384, 1)
                         }
                     }
                 } else if (live) {
-                    float* out = p.part_o + pf_part_at(part, D, c);
+                    float* out = p.part_o + pf_part_at(part, D, col);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t v[8];
@@ -1100,7 +1161,7 @@ __global__ void __launch_bounds__(384, 1)
             if (live && *mark_piece == piece) {
                 // values that are not finite, into the rows that see them
 #pragma unroll 1
-                for (int d = 0; d < D; ++d) {
+                for (int d = col0; d < (turns ? col0 + D / 2 : D); ++d) {
                     const float v = poison(marks, D, d, pos);
                     if (v == 0.f) continue;
                     if (pc.whole())
@@ -1109,12 +1170,11 @@ __global__ void __launch_bounds__(384, 1)
                         p.part_o[pf_part_at(part, D, d)] = v;
                 }
             }
-            if (!pc.whole() && live) p.part_ml[2 * part] = m, p.part_ml[2 * part + 1] = l;
-            if (j == 0)  // (all have read the marks)
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-            else
-                asm volatile("bar.sync 2, 128;" ::: "memory");
-            if (r == 0) done[j] = piece;
+            // (in turns, group 0's rows hold its own sums until both have read them)
+            if (!pc.whole() && live && !(turns && j == 1))
+                p.part_ml[2 * part] = m, p.part_ml[2 * part + 1] = l;
+            __syncwarp();  // (all of the warp have read the marks)
+            if (lane == 0) atomicAdd(const_cast<int*>(done) + j, 1);
         }
         if (!ok) *abort_all = 1;
     }

@@ -385,6 +385,30 @@ def test_calls_need_the_current_device(cuda_device, monkeypatch):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,h,hkv", [(128, 8, 2), (64, 6, 2), (64, 16, 1)])
+def test_prefill_few_rows_long_contexts(cuda_device, dtype, d, h, hkv):
+    """Contexts of several key tiles behind a handful of rows: pages that are missing,
+    maxima that rise along the context, values that only the last rows see."""
+    new, ctx, at = [9, 1, 5, 8], [1200, 513, 777, 2050], 6
+    pool_t, tables, q = prefill_case(cuda_device, dtype, d, 16, h, hkv, new, ctx, seed=15, fill=float("nan"))
+    for j in range(ctx[0] // 16):
+        pool_t[int(tables[0, j]), 0] *= 1 + j / 8
+    tables[2, 3], tables[2, 20] = -1, 10 ** 6     # pages of sequence 2 that are not there
+    clean, bound = R.prefill(pool_t, q, tables, ctx, new, d ** -0.5)
+    got = run_prefill(cuda_device, pool_t, tables, q, new, ctx)
+    status_is(B.PA_STATUS_BAD_BLOCK_ID)
+    check(got, clean, bound)
+    pos = ctx[0] - new[0] + at
+    pool_t[int(tables[0, pos // 16]), 1, 0, :, pos % 16, d - 1] = -float("inf")
+    got = run_prefill(cuda_device, pool_t, tables, q, new, ctx)
+    status_is(B.PA_STATUS_BAD_BLOCK_ID)
+    check(got[:at], clean[:at], bound[:at])
+    check(got[9:], clean[9:], bound[9:])
+    check(got[at:9, :, :d - 1], clean[at:9, :, :d - 1], bound[at:9, :, :d - 1])
+    assert not bool(torch.isfinite(got[at:9, :, d - 1]).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("new,ctx", [([4], [9000]), ([300], [1200]), ([3] * 9, [700] * 9)])
 def test_prefill_infinite_values_of_tiny_weight(cuda_device, dtype, new, ctx):
     """Scores so far apart that most weights are below the smallest number, where 0 *
