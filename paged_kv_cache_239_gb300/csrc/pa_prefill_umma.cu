@@ -29,9 +29,9 @@ cudaError_t launch_turns(const PrefillParams& p, const CUtensorMap* tm, cudaStre
             done_mask |= bit;
         }
     }
-    CUtensorMap tq{};  // (not used for groups that do not divide 128)
-    if (128 % p.G == 0) {
-        e = encode_heads_tmap(&tq, p.q, D, p.H, p.num_tokens, p.G, 128 / p.G);
+    CUtensorMap tq{};  // (not used for groups above 64 that do not divide 128)
+    if (128 % p.G == 0 || p.G <= 64) {
+        e = encode_heads_tmap(&tq, p.q, D, p.H, p.num_tokens, p.G, 128 % p.G == 0 ? 128 / p.G : 1);
         if (e != cudaSuccess) return e;
     }
     e = launch_pdl(kern, dim3((unsigned)p.grid), dim3(C::THREADS), C::SMEM_BYTES, s, p, tm[0], tm[1], tq);

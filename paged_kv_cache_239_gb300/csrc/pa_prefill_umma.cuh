@@ -838,12 +838,14 @@ __global__ void __launch_bounds__(384, 1)
             // ============================================== Q rows (warp 2)
             // Groups that divide 128: a tile is 128 / G tokens' heads, one box of
             // the 3-D tensor map (columns, heads, tokens) per half; what it holds
-            // past the sequence belongs to rows that are not written.  Other
-            // groups: row by row.
+            // past the sequence belongs to rows that are not written.  Other groups of
+            // up to 64: one box per token that lies whole in the tile (the swizzle goes
+            // by the address, so a box may start at any row), the rest row by row.
             constexpr int CPR = D / 8;               // 16-byte chunks per row
             constexpr int RPI = 32 / CPR;            // rows per pass
             const int c = lane % CPR;
             const bool boxes = 128 % p.G == 0;
+            const bool tokens = p.G <= 64 && p.qscale >= 0.f;  // (at least one whole in a tile)
             int nqj[2] = {0, 0}, vseq = 1, nlook = 0, piece = 0, mark_at = -1;
             bool ok = true;
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
@@ -868,15 +870,19 @@ __global__ void __launch_bounds__(384, 1)
                         continue;
                     }
                     const uint32_t dst = tile + (c >> 3) * C::HALF;
-                    int tok = pf_div(p, f0 + lane / CPR), g = (f0 + lane / CPR) - tok * p.G;
+                    // the tile's whole tokens, from row r0 to r1, as boxes
+                    const int tok0 = pf_div(p, f0 + p.G - 1);
+                    const int r0 = tokens ? tok0 * p.G - f0 : 128;
+                    const int whole = tokens ? pf_div(p, 128 - r0) : 0, r1 = r0 + whole * p.G;
 #pragma unroll 4
-                    for (int r = lane / CPR; r < 128; r += RPI) {
+                    for (int x = lane / CPR; x < r0 + 128 - r1; x += RPI) {
+                        const int r = x < r0 ? x : x + r1 - r0;
                         const bool live = f0 + r < pc.rows;
+                        const int tok = pf_div(p, f0 + r), g = f0 + r - tok * p.G;
                         cp_async16(dst + sw128(r, c),
                                    live ? q + ((long long)(pc.start + tok) * p.H + pc.kvh * p.G + g) * D + 8 * c
                                         : q,
                                    live);
-                        for (g += RPI; g >= p.G; g -= p.G) ++tok;
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     if (p.qscale < 0.f) {  // S = -Q K^T, and the softmax scales by |scale|
@@ -891,7 +897,16 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(fb);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(fb, (uint32_t)(whole * p.G) * D * 2u);
+#pragma unroll 1
+                        for (int t = 0; t < whole; ++t)
+#pragma unroll
+                            for (int h = 0; h < C::NH; ++h)
+                                tma_load_3d(tile + h * C::HALF + (r0 + t * p.G) * 128, &tmq, fb, 64 * h,
+                                            pc.kvh * p.G, pc.start + tok0 + t);
+                    }
+                    __syncwarp();
                 }
                 // V of the piece's last tiles: rows past the context are zeroed,
                 // values that are not finite zeroed and remembered
