@@ -104,8 +104,8 @@ struct PrefillCfg {
     static constexpr int KV_FULL = 0, KV_EMPTY = NS, Q_FULL = 2 * NS, Q_EMPTY = Q_FULL + 2,
                          S_FULL = Q_FULL + 4, P_FULL = Q_FULL + 6,  // three parts, [part][row tile]
                          PV_DONE = Q_FULL + 12, FINAL = Q_FULL + 14,
-                         V_LOOK = Q_FULL + 15, V_CLEAN = Q_FULL + 16,
-                         PC_FULL = Q_FULL + 17, PC_EMPTY = PC_FULL + NP,
+                         V_LOOK = Q_FULL + 15, V_CLEAN = Q_FULL + 17,  // two each, in turns
+                         PC_FULL = Q_FULL + 19, PC_EMPTY = PC_FULL + NP,
                          X_SUMS = PC_EMPTY + NP, X_READ = X_SUMS + 1, NBAR = X_READ + 1;
     static_assert(NBAR * 8 <= TMEM_SLOT && NS <= 11, "ctrl layout");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -745,8 +745,14 @@ __global__ void __launch_bounds__(384, 1)
                 const uint64_t dK = umma_desc_sw128(sbase, 0, 1024);
                 const uint64_t dV = umma_desc_sw128(sbase, C::HALF, 1024);
                 const uint64_t dQ = umma_desc_sw128(sbase + C::OFF_Q, 0, 1024);
-                int seq = 0, npj[2] = {0, 0}, nqj[2] = {0, 0}, nclean = 0;
+                int seq = 0, npj[2] = {0, 0}, nqj[2] = {0, 0}, nclean = 0, nlook = 0;
                 bool ok = true;
+                // asks for the look over V of tile i; up to two are asked for before the
+                // first is waited for, and V's stage held K(i - 2) or what came before it
+                auto look = [&](int i) {
+                    if (i < pc.kt1 - pc.kt0 && pf_unclean(pc, pc.kt0 + i))
+                        mbar_arrive(bar0 + 8 * (C::V_LOOK + (nlook++ & 1)));
+                };
                 auto stage_full = [&](int s) { return wait(C::KV_FULL + s % C::NS, (s / C::NS) & 1); };
                 auto score = [&](int j, int q, int s) {  // S_j = Q_q K^T, K in stage s
                     const uint64_t a = dQ + (uint64_t)((q * C::TILE) >> 4);
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(384, 1)
                     for (int i = 0; i < ahead && ok; ++i) {
                         if (!(ok = stage_full(seq + 2 * i))) break;
                         tc_fence_after();
-                        if (i == 0 && pf_unclean(pc, pc.kt0)) mbar_arrive(bar0 + 8 * C::V_LOOK);
+                        if (i == 0) look(0), look(1);
 #pragma unroll 1
                         for (int j = 0; j < pc.nj; ++j) {
                             score(turns ? i : j, j, seq + 2 * i);
@@ -798,7 +804,7 @@ __global__ void __launch_bounds__(384, 1)
                             if (j == 0) {
                                 ok = stage_full(seq + 1);
                                 if (ok && pf_unclean(pc, pc.kt0 + i))
-                                    ok = wait(C::V_CLEAN, nclean++ & 1);
+                                    ok = wait(C::V_CLEAN + (nclean & 1), (nclean >> 1) & 1), ++nclean;
                             }
 #pragma unroll
                             for (int part = 0; part < 3; ++part) {
@@ -815,9 +821,7 @@ __global__ void __launch_bounds__(384, 1)
                             umma_commit(bar0 + 8 * (C::PV_DONE + g));
                             if (j == pc.nj - 1)
                                 umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 1) % C::NS));
-                            // (one look asked for at a time)
-                            if (j == 0 && i + 1 < nk && pf_unclean(pc, pc.kt0 + i + 1))
-                                mbar_arrive(bar0 + 8 * C::V_LOOK);
+                            if (j == 0) look(i + 2);
                             if (i + ahead < nk) {
                                 const int ks = seq + 2 * ahead;
                                 if (j == 0 && !(ok = stage_full(ks))) break;
@@ -908,23 +912,36 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     __syncwarp();
                 }
-                // V of the piece's last tiles: rows past the context are zeroed,
-                // values that are not finite zeroed and remembered
+                // V of the piece's last tiles: rows that none of the pair's see are zeroed,
+                // of the others the values that are not finite, which are remembered.  (Asked
+                // for two tiles ahead: it takes 2000 cycles and more beside the softmax, and
+                // asked for one ahead the last product waited 2000 - 4400 for it.)
                 ++piece;
+                const int last = pc.first_pos + pf_div(p, min(pc.rows, pc.row0 + 256) - 1);
 #pragma unroll 1
                 for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt, vseq += 2) {
                     if (!pf_unclean(pc, kt)) continue;
                     const int t0 = kt * C::TT, stage = vseq % C::NS;
-                    // (not before the tile's S is issued: a wait may be no more than
-                    // one phase ahead of its barrier)
-                    ok = __all_sync(kFullMask, wait(C::V_LOOK, nlook++ & 1) &&
+                    // (not before it is asked for: a wait may be no more than one phase
+                    // ahead of its barrier)
+                    ok = __all_sync(kFullMask, wait(C::V_LOOK + (nlook & 1), (nlook >> 1) & 1) &&
                                                    wait(C::KV_FULL + stage, (vseq / C::NS) & 1));
                     if (!ok) break;
+                    const int clean = C::V_CLEAN + (nlook++ & 1);
                     uint32_t odd = 0;
 #pragma unroll 1
                     for (int r = lane; r < 128; r += 32) {
                         unsigned char* vrow = smem + stage * C::TILE + r * 128;
                         if (t0 + r <= pc.pair_pos) continue;
+                        if (t0 + r > last) {
+#pragma unroll
+                            for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    *reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
                         // 0 * x summed up is NaN as soon as one x is not finite
                         __nv_bfloat162 z[4];
 #pragma unroll
@@ -934,16 +951,12 @@ __global__ void __launch_bounds__(384, 1)
                         for (int h = 0; h < C::NH; ++h)
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
-                                uint4* at = reinterpret_cast<uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
-                                if (t0 + r >= pc.n) {
-                                    *at = make_uint4(0, 0, 0, 0);
-                                } else {
-                                    const uint4 v = *at;
-                                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                                const uint4 v =
+                                    *reinterpret_cast<const uint4*>(vrow + h * C::HALF + ((k + r) & 7) * 16);
+                                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        z[e] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]), zero, z[e]);
-                                }
+                                for (int e = 0; e < 4; ++e)
+                                    z[e] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u[e]), zero, z[e]);
                             }
                         const float2 f = __bfloat1622float2(__hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3])));
                         if (f.x + f.y != 0.f) odd |= 1u << (r >> 5);
@@ -979,7 +992,7 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar0 + 8 * C::V_CLEAN);
+                    if (lane == 0) mbar_arrive(bar0 + 8 * clean);
                 }
             }
             if (*abort_all && lane == 0)  // copies in flight land before the CTA can exit
