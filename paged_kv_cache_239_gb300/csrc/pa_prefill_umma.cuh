@@ -772,12 +772,6 @@ __global__ void __launch_bounds__(384, 1)
                     ++np;
                     if (pc.nj == 0) break;
                     const int nk = pc.kt1 - pc.kt0;
-#pragma unroll 1
-                    for (int j = 0; j < pc.nj && ok; ++j) {
-                        ok = wait(C::Q_FULL + j, nqj[j] & 1);
-                        ++nqj[j];
-                    }
-                    if (!ok) break;
                     // in turns, tile i is group i % 2's, and S runs two tiles ahead
                     const bool turns = TURNS && pc.turns();
                     const int ahead = turns ? 2 : 1;
@@ -788,9 +782,15 @@ __global__ void __launch_bounds__(384, 1)
                         if (i == 0) look(0), look(1);
 #pragma unroll 1
                         for (int j = 0; j < pc.nj; ++j) {
+                            if (i == 0) {
+                                if (!(ok = wait(C::Q_FULL + j, nqj[j] & 1))) break;
+                                ++nqj[j];
+                                tc_fence_after();
+                            }
                             score(turns ? i : j, j, seq + 2 * i);
                             if (nk == 1) umma_commit(bar0 + 8 * (C::Q_EMPTY + j));
                         }
+                        if (!ok) break;
                         umma_commit(bar0 + 8 * (C::KV_EMPTY + (seq + 2 * i) % C::NS));
                     }
 #pragma unroll 1
