@@ -42,7 +42,7 @@ cudaError_t launch_turns(const PrefillParams& p, const CUtensorMap* tm, cudaStre
 
 // Calls with 128 rows to a sequence on average, or fewer, take the kernel in which
 // both softmax groups serve a single row tile in turns (3 - 5 tokens over 4 long
-// contexts: 152 us, 167 without); it has more code, which costs calls of many pairs
+// contexts: 150 us, 167 without); it has more code, which costs calls of many pairs
 // of row tiles 5 - 15 %, so they take the one without.
 template <int D, int B>
 cudaError_t launch_inst(const PrefillParams& p, const CUtensorMap* tm, cudaStream_t s) {

@@ -44,17 +44,17 @@
 // the rows that see them at the output.
 //
 // What bounds it.  Long prompts: a pair's tile is 4 x 8 MMAs of 128 x 128 x 16, 2048
-// cycles of the tensor pipe, and takes about 2750, since S(i + 1) waits for the
+// cycles of the tensor pipe, and takes about 2700, since S(i + 1) waits for the
 // softmax of S(i) to leave the columns that P stands in, with 512 columns for two
 // row tiles' S and O (the exponentials, 2048 cycles of the special-function units,
-// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 366 us, 1.50 PFLOP/s of
-// the causal half (78 % of a large library product's burst rate).  Measured and
+// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 353 - 357 us, 1.55 PFLOP/s
+// of the causal half (81 % of a large library product's burst rate).  Measured and
 // slower, at a time when this form took 400: two threads to a row 450; two issuing
 // threads 480; P handed over in halves 409.  Without the exponentials it took 383.
-// Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 152
-// us, 6.2 TB/s (92 % of a plain copy's rate; 167 us without turns), in shares cut to
+// Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 150
+// us, 6.3 TB/s (94 % of a plain copy's rate; 167 us without turns), in shares cut to
 // the tile.  Short calls:
-// latency (pa_prefill_mma.cu takes the shortest); one token over 100 keys takes 8.9 us,
+// latency (pa_prefill_mma.cu takes the shortest); one token over 100 keys takes 8.7 us,
 // of which 2.5 go to the schedule (its code is fetched by every SM), 2.5 to the first
 // K tile and its scores, and 2.5 to the join's launch; 8 chunks of up to 513 tokens
 // with 16 heads on 2 of 64: 25 us, of which 9 are five to seven tiles.
