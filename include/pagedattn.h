@@ -637,7 +637,8 @@ PA_API int pa_copy_blocks(pa_pool* pool, const int* src_ids, const int* dst_ids,
  *   block_tables  device int32 [batch, max_blocks_per_seq]; context_lens [batch].
  * n <= 65536.  When the stack runs dry, the entries of the pages that were not
  * to be had are -1 (PA_STATUS_NO_FREE_BLOCKS); so are table entries and stack
- * ids outside the pool (PA_STATUS_BAD_BLOCK_ID).  Pairs with rows outside [0, batch), a row
+ * ids outside the pool (PA_STATUS_BAD_BLOCK_ID; a parent's partial page that is
+ * such an entry takes no page from the stack).  Pairs with rows outside [0, batch), a row
  * as its own parent or a bad parent length are skipped (PA_STATUS_BAD_LENGTH).
  * Cites: no counterpart on the pages (their tables share no blocks); new pages
  * come from the free list as in mini-infer, "Python Implementation: Physical

@@ -115,13 +115,14 @@ pa_copy_blocks_kernel(const PageGeom g, const int* src, const int* dst, const in
 
 // --------------------------------------------------------------------- fork
 
-// A pair of a fork: the parent's row and length, or par = -1 where it is to be
-// skipped (flagged by `report`).
+// A pair of a fork: the parent's row, length and partial last page (-1 where it has
+// none, or one that is no page and so holds nothing to copy), or par = -1 where the
+// pair is to be skipped (both flagged by `report`).
 struct ForkPair {
-    int par, chi, len;
+    int par, chi, len, old;
 };
 __device__ __forceinline__ ForkPair fork_pair(const ForkParams& p, int i, bool report) {
-    ForkPair f{ld_dep(p.parents + i), ld_dep(p.children + i), 0};
+    ForkPair f{ld_dep(p.parents + i), ld_dep(p.children + i), 0, -1};
     bool good = f.par >= 0 && f.par < p.batch && f.chi >= 0 && f.chi < p.batch && f.par != f.chi;
     if (good) {
         f.len = ld_dep(p.lens + f.par);
@@ -130,6 +131,12 @@ __device__ __forceinline__ ForkPair fork_pair(const ForkParams& p, int i, bool r
     if (!good) {
         f.par = -1;
         if (report) atomicOr(p.g.status, kStatusBadLength);
+    } else if (f.len % p.g.B) {
+        f.old = ld_dep(p.bt + (long long)f.par * p.maxb + f.len / p.g.B);
+        if (f.old < 0 || f.old >= p.g.num_blocks) {
+            f.old = -1;
+            if (report) atomicOr(p.g.status, kStatusBadBlock);
+        }
     }
     return f;
 }
@@ -139,12 +146,7 @@ __device__ __forceinline__ int fork_pages_before(const ForkParams& p, int n) {
     int mine = 0;
     for (int i0 = 0; i0 < n; i0 += blockDim.x) {
         const int i = i0 + threadIdx.x;
-        bool need = false;
-        if (i < n) {
-            const ForkPair f = fork_pair(p, i, false);
-            need = f.par >= 0 && f.len % p.g.B != 0;
-        }
-        mine += __syncthreads_count(need);
+        mine += __syncthreads_count(i < n && fork_pair(p, i, false).old >= 0);
     }
     return mine;
 }
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams 
     if (f.par < 0) return;
     const int full = f.len / p.g.B, rows = f.len % p.g.B;
     int id = -1;
-    if (rows) {
+    if (f.old >= 0) {
         if (rank < height) {
             id = ld_dep(p.stack + height - rank);
             if (id < 0 || id >= p.g.num_blocks) {
@@ -199,18 +201,13 @@ __global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams 
         }
         if (threadIdx.x == 0) p.lens[f.chi] = f.len;
     }
-    if (rows == 0 || id == -1) return;
+    if (id == -1) return;
     // the live rows of the partial last page
-    const int old = ld_dep(from + full);
-    if (old < 0 || old >= p.g.num_blocks) {
-        if (first && threadIdx.x == 0) atomicOr(p.g.status, kStatusBadBlock);
-        return;
-    }
     const int tiles = 2 * p.g.L * p.g.Hkv;
     const int chunks = rows * (p.g.tile_bytes / p.g.B / 16);
     for (int t = blockIdx.y * (kCopyThreads / 32) + (threadIdx.x >> 5); t < tiles;
          t += gridDim.y * (kCopyThreads / 32))
-        if (old != id) warp_copy_tile(p.g, t, old, id, chunks, lane);
+        if (f.old != id) warp_copy_tile(p.g, t, f.old, id, chunks, lane);
 }
 
 __global__ void __launch_bounds__(kCopyThreads) pa_fork_height_kernel(const ForkParams p) {

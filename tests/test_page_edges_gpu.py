@@ -1,0 +1,103 @@
+"""Page operations at their edges: forks of rows whose partial page is missing, forks
+of many rows."""
+import numpy as np
+import pytest
+import torch
+
+import prompt_reference as R
+from paged_kv_cache_239_gb300 import binding as B
+from paged_kv_cache_239_gb300.pool import BlockPool
+
+pytestmark = pytest.mark.gpu
+
+def ints(x, dev):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)
+
+
+def stack_of(ids, nb, dev):
+    s = np.full(nb + 1, -1, np.int32)
+    s[0], s[1:1 + len(ids)] = len(ids), ids
+    return ints(s, dev)
+
+
+# --------------------------------------------------------------------- fork
+
+
+def fork_state(dev, nb, free, tables, lens):
+    pool_t = torch.randn((nb, 2, 2, 1, 16, 8), generator=torch.Generator(device=dev).manual_seed(5), device=dev)
+    cache = BlockPool(nb, 16, 2, 1, 8, tensor=pool_t)
+    return cache, stack_of(free, nb, dev), cache.page_shares(), ints(tables, dev), ints(lens, dev)
+
+
+@pytest.mark.parametrize("bad", [-1, -7, 12, 1 << 30])
+def test_fork_of_a_missing_partial_page(cuda_device, bad):
+    """A parent whose partial page is no page has nothing to copy: its child's entry is
+    -1, not the id of a page that was never written for it, and no page is taken."""
+    dev = cuda_device
+    tables = np.full((8, 3), -1, np.int32)
+    tables[0, :2], tables[1, :2], tables[2, 0] = (3, bad), (4, 5), bad
+    cache, stack, shares, bt, ln = fork_state(dev, 12, [9, 10, 11], tables, [20, 30, 5, 0, 0, 0, 0, 0])
+    before = cache.pool.clone()
+    cache.device_fork_sequences(stack, shares, bt, ln, ints([0, 1, 2, 1], dev), ints([3, 4, 5, 6], dev))
+    assert B.pa_get_status() == B.PA_STATUS_BAD_BLOCK_ID
+    want = tables.copy()
+    want[3, 0], want[4, :2], want[6, :2] = 3, (4, 11), (4, 10)   # the good pairs take 11 and 10
+    assert np.array_equal(bt.cpu().numpy(), want)
+    assert ln.tolist() == [20, 30, 5, 20, 30, 5, 30, 0]
+    assert stack[:2].tolist() == [1, 9]
+    assert shares.tolist() == [0, 0, 0, 1, 2] + [0] * 7
+    before[11, ..., :14, :] = before[5, ..., :14, :]
+    before[10, ..., :14, :] = before[5, ..., :14, :]
+    assert torch.equal(cache.pool, before)
+    cache.close()
+
+
+def test_fork_of_a_fork_that_ran_dry(cuda_device):
+    """What a dry stack left without a page stays without one in the forks of it, also
+    when there are free pages again."""
+    dev = cuda_device
+    tables = np.full((4, 2), -1, np.int32)
+    tables[0] = 1, 2
+    cache, stack, shares, bt, ln = fork_state(dev, 8, [], tables, [20, 0, 0, 0])
+    cache.device_fork_sequences(stack, shares, bt, ln, ints([0], dev), ints([1], dev))
+    assert B.pa_get_status() == B.PA_STATUS_NO_FREE_BLOCKS and bt[1].tolist() == [1, -1]
+    stack = stack_of([6, 7], 8, dev)
+    cache.device_fork_sequences(stack, shares, bt, ln, ints([1], dev), ints([2], dev))
+    assert B.pa_get_status() == B.PA_STATUS_BAD_BLOCK_ID
+    assert bt[2].tolist() == [1, -1] and stack[:3].tolist() == [2, 6, 7] and int(ln[2]) == 20
+    cache.close()
+
+
+@pytest.mark.parametrize("n", [257, 8192])
+def test_fork_many_children(cuda_device, n):
+    """Children whose pages are counted in several steps, bad partial pages among their parents'."""
+    dev, block, parents = cuda_device, 4, 64
+    rng = np.random.default_rng(n)
+    rows, nb = parents + n, parents * 3 + n + 5
+    lens = np.zeros(rows, np.int32)
+    lens[:parents] = rng.integers(0, 3 * block + 1, parents)
+    tables = np.full((rows, 3), -1, np.int32)
+    for b in range(parents):
+        for j in range(R.cdiv(int(lens[b]), block)):
+            tables[b, j] = 3 * b + j
+        if b % 9 == 0 and lens[b] % block:
+            tables[b, lens[b] // block] = -1
+    free = [int(x) for x in rng.permutation(np.arange(parents * 3, nb))]
+    pool_t = torch.randn((nb, 2, 1, 1, block, 4), device=dev)
+    cache = BlockPool(nb, block, 1, 1, 4, tensor=pool_t)
+    par, chi = rng.integers(0, parents, n), parents + rng.permutation(n)
+    want_t, want_p, left = tables.copy(), pool_t.clone(), list(free)
+    want_s = np.zeros(nb, np.int32)
+    for p, c in zip(par, chi):
+        full, part = divmod(int(lens[p]), block)
+        want_t[c, :full] = tables[p, :full]
+        want_s[tables[p, :full]] += 1
+        if part and tables[p, full] >= 0:
+            want_t[c, full] = left.pop()
+            want_p[want_t[c, full], ..., :part, :] = want_p[int(tables[p, full]), ..., :part, :]
+    bt, ln, stack, shares = ints(tables, dev), ints(lens, dev), stack_of(free, nb, dev), cache.page_shares()
+    cache.device_fork_sequences(stack, shares, bt, ln, ints(par, dev), ints(chi, dev))
+    assert B.pa_get_status() == B.PA_STATUS_BAD_BLOCK_ID
+    assert np.array_equal(bt.cpu().numpy(), want_t) and np.array_equal(shares.cpu().numpy(), want_s)
+    assert int(stack[0]) == len(left) and torch.equal(cache.pool, want_p)
+    cache.close()
