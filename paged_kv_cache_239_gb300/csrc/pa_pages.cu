@@ -577,12 +577,12 @@ cudaError_t launch_free_shared(const FreeSharedParams& p, cudaStream_t s) {
     const int ctas = entries <= 4096 ? 1 : kFreeCluster;
     const long long ids = (entries + ctas - 1) / ctas;
     const size_t smem = (size_t)(p.batch + 1 + ids) * sizeof(int);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            pa_free_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (kFreeRows + 1 + kFreeEntries / kFreeCluster) * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
-    }
+    // (always, and the same for all calls: the kernel's static shared memory counts toward the
+    // 48 KiB that go without it, and the limit is the function's, not the call's)
+    const cudaError_t e = cudaFuncSetAttribute(
+        pa_free_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (kFreeRows + 1 + kFreeEntries / kFreeCluster) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kPlanThreads);

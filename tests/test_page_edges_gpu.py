@@ -1,5 +1,9 @@
-"""Page operations at their edges: forks of rows whose partial page is missing, forks
-of many rows."""
+"""Page operations at their edges: forks of rows whose partial page is missing,
+forks of many rows, shared frees at the sizes where the shared-memory limit turns."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,9 @@ from paged_kv_cache_239_gb300 import binding as B
 from paged_kv_cache_239_gb300.pool import BlockPool
 
 pytestmark = pytest.mark.gpu
+
+REPO = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
 
 def ints(x, dev):
     return torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)
@@ -101,3 +108,35 @@ def test_fork_many_children(cuda_device, n):
     assert np.array_equal(bt.cpu().numpy(), want_t) and np.array_equal(shares.cpu().numpy(), want_s)
     assert int(stack[0]) == len(left) and torch.equal(cache.pool, want_p)
     cache.close()
+
+
+# -------------------------------------------------------------- shared free
+
+FREE_ALONE = """
+import sys
+sys.path.insert(0, {repo!r})
+import torch
+from paged_kv_cache_239_gb300 import binding as B
+from paged_kv_cache_239_gb300.pool import BlockPool
+rows, width = {rows}, {width}
+cache = BlockPool(rows, 1, 1, 1, 4, dtype=torch.float32)
+i32 = dict(dtype=torch.int32, device="cuda")
+tables = torch.full((rows, width), -1, **i32)
+tables[:, 0] = torch.arange(rows, **i32)
+stack = torch.full((rows + 1,), -1, **i32)
+stack[0] = 0
+done = torch.ones(rows, dtype=torch.uint8, device="cuda")
+cache.device_free_shared(stack, cache.page_shares(), tables, torch.ones(rows, **i32), done)
+assert stack.tolist() == [rows] + list(range(rows)), stack
+assert bool((tables == -1).all()) and B.pa_get_status() == 0
+print("freed")
+"""
+
+
+@pytest.mark.parametrize("rows,width", [(256, 375), (64, 1523), (128, 758), (256, 376), (128, 768)])
+def test_free_shared_as_the_first_call(cuda_device, rows, width):
+    """Tables whose places take about 48 KiB of shared memory, which is what a kernel gets
+    without asking for more: in a process of their own, so that no call asked before."""
+    run = subprocess.run([sys.executable, "-c", FREE_ALONE.format(repo=REPO, rows=rows, width=width)],
+                         capture_output=True, text=True, timeout=300, cwd=REPO)
+    assert run.returncode == 0 and "freed" in run.stdout, run.stderr[-2000:]
