@@ -1292,8 +1292,9 @@ int pa_device_compact_blocks(pa_pool* pool, const void* dev_stack, const int* sh
     if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
         return rc;
     const long long nb = pool->g.num_blocks;
-    if (nb > 786432)
-        return fail(PA_ERR_UNSUPPORTED, "compaction is built for up to 786432 blocks, not %lld", nb);
+    if (nb > pa::kCompactMaxBlocks)
+        return fail(PA_ERR_UNSUPPORTED, "compaction is built for up to %lld blocks, not %lld",
+                    pa::kCompactMaxBlocks, nb);
     if (int rc = check_stack(dev_stack)) return rc;
     if (!out_stack || !remap || !aligned(out_stack, 4) || !aligned(remap, 4) ||
         !aligned(shares, 4) || !aligned(out_shares, 4) || !aligned(out_tables, 4))

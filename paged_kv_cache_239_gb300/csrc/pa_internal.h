@@ -201,7 +201,8 @@ cudaError_t launch_copy_blocks(const PageGeom& g, const int* src, const int* dst
                                int num_sms, cudaStream_t s);
 cudaError_t launch_fork(const ForkParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_free_shared(const FreeSharedParams& p, cudaStream_t s);
-size_t compact_smem_bytes(long long num_blocks);
+// The largest pool whose map of free ids fits a CTA's shared memory.
+constexpr long long kCompactMaxBlocks = 786432;
 cudaError_t launch_compact(const CompactParams& p, int num_sms, cudaStream_t s);
 
 // Returns cudaErrorNotSupported (without launching) when no kernel is built

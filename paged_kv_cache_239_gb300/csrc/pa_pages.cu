@@ -600,15 +600,19 @@ cudaError_t launch_free_shared(const FreeSharedParams& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, pa_free_shared_kernel, p);
 }
 
-size_t compact_smem_bytes(long long num_blocks) {
+constexpr size_t compact_smem_bytes(long long num_blocks) {
     return (size_t)(num_blocks / 32 + 1) * 8;
 }
+static_assert(compact_smem_bytes(kCompactMaxBlocks) + 1024 <= 232448, "shared memory");
 
 cudaError_t launch_compact(const CompactParams& p, int num_sms, cudaStream_t s) {
     const long long nb = p.g.num_blocks;
     const size_t smem = compact_smem_bytes(nb);
+    // (the same for all calls: the limit is the function's, and another thread's call with a
+    // smaller pool may come between this one's limit and its launch)
     cudaError_t e = cudaFuncSetAttribute(pa_compact_plan_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)compact_smem_bytes(kCompactMaxBlocks));
     if (e != cudaSuccess) return e;
     const long long items = nb > (long long)p.batch * p.maxb ? nb : (long long)p.batch * p.maxb;
     long long grid = (items + kPlanThreads - 1) / kPlanThreads;

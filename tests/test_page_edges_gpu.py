@@ -1,8 +1,11 @@
 """Page operations at their edges: forks of rows whose partial page is missing,
-forks of many rows, shared frees at the sizes where the shared-memory limit turns."""
+shared frees at the sizes where the shared-memory limit turns, compactions of pools
+of different sizes side by side."""
+import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -140,3 +143,41 @@ def test_free_shared_as_the_first_call(cuda_device, rows, width):
     run = subprocess.run([sys.executable, "-c", FREE_ALONE.format(repo=REPO, rows=rows, width=width)],
                          capture_output=True, text=True, timeout=300, cwd=REPO)
     assert run.returncode == 0 and "freed" in run.stdout, run.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ compact
+
+
+def test_compact_pools_of_two_sizes_side_by_side(cuda_device, tmp_path):
+    """Two host threads compact pools whose maps take little and much shared memory: the
+    one's launch does not take the other's limit away."""
+    dev, n, results, start = cuda_device, 20000, {}, threading.Barrier(2)
+    so = tmp_path / "loop.so"
+    subprocess.run(["gcc", "-std=c11", "-O2", "-shared", "-fPIC", "-I", os.path.join(REPO, "include"),
+                    os.path.join(REPO, "tests", "c_abi", "pa_compact_loop.c"), "-o", str(so)], check=True)
+    loop = ctypes.CDLL(str(so)).compact_loop
+    call = ctypes.cast(B.lib().pa_device_compact_blocks, ctypes.c_void_p)
+    p = ctypes.c_void_p
+
+    def work(nb):
+        torch.cuda.set_device(dev)
+        cache = BlockPool(nb, 1, 1, 1, 4, tensor=torch.zeros((nb, 2, 1, 1, 1, 4), device=dev))
+        stack, bt, ln = stack_of([nb - 1], nb, dev), ints([[0]], dev), ints([1], dev)
+        out_stack, out_bt, _, remap = cache.device_compact_blocks(stack, bt, ln)
+        ws = torch.empty(cache.compact_workspace_size(), dtype=torch.uint8, device=dev)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        start.wait(60)
+        results[nb] = loop(call, n, p(cache.handle), *(p(t.data_ptr()) for t in (stack, bt, ln, out_stack, out_bt,
+                                                                                  remap, ws)),
+                           ctypes.c_size_t(ws.numel()), p(side.cuda_stream))
+        side.synchronize()
+        cache.close()
+
+    threads = [threading.Thread(target=work, args=(nb,)) for nb in (4, 200000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert results == {4: B.PA_OK, 200000: B.PA_OK}
+    assert B.pa_get_status() == 0
