@@ -563,8 +563,12 @@ PA_API int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const vo
  * Causal attention of the new tokens over the cache, which holds them already
  * (prompts, chunks of prompts behind a cached prefix, a few tokens to verify):
  *   out[t][h] = softmax_s(scale * q[t][h] . K_s) V_s over s <= position of t,
- * rows resolved through the block table as in pa_decode_attention, fp32 scores
- * and sums.  What lies in the cache at positions a row does not see (future
+ * rows resolved through the block table as in pa_decode_attention.  Scores,
+ * statistics and sums are fp32.  The products' factors are those of the tensor
+ * cores: on fp32 pools each in two TF32 parts (a product is off by 2^-22 at most, an
+ * output by as much as with plain fp32 products), on bf16 pools the weights rounded
+ * to bf16 before their product with V (the sum they are divided by takes them before).
+ * What lies in the cache at positions a row does not see (future
  * tokens, rows past the context), be it NaN, does not reach that row; a value
  * that is not finite makes its column of every row that sees it not finite.
  *   out, q        device [num_tokens, num_heads, head_dim] of the pool dtype,

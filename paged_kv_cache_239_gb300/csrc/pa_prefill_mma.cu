@@ -15,20 +15,25 @@
 // fp32 (tiles of 32 keys, 16 at head_dim 128: what leaves room for three CTAs on an
 // SM).  TF32 keeps 11 bits of a product's factors, so x = hi + lo with hi = x
 // rounded to TF32 and lo = x - hi (exact; 12 bits, of which TF32 keeps 11): hi hi' +
-// hi lo' + lo hi' misses x x' by about 2^-22, as an fp32 product does by 2^-24, and
-// the sums are fp32.  Three m16n8k8 products take 24 cycles of a scheduler's tensor
-// pipe for 1024 multiply-adds; fused multiply-adds take 32, and two operands from
-// shared memory for each sixteenth of them.  The order of the summed index is free in
-// a product, so it is chosen to suit the fragments: a thread's four neighbouring
-// elements of q and k are its columns of two steps, a thread's scores of
-// neighbouring keys are its columns of P, and its four neighbouring columns of v
-// belong to four tiles of O.  Every operand is read as float4, with strides that
-// keep eight lanes on 32 banks.
+// hi lo' + lo hi' misses x x' by 2^-22 at most, with either sign.  The tensor core's sums
+// are fp32, but cut off toward zero: a sum that runs through it loses the same way at
+// every step.  So none runs long there: the small products of a score have a sum of their
+// own, and P V of a tile starts from zero and is added to O by ordinary, rounded additions.
+// (A prompt of 4096 is off by 4.4e-7 of its output's size at head_dim 128, 3.8e-7 at 64,
+// plain fp32 products and exp by 5.4e-7 and 4.9e-7; with O as the products' running sum
+// 4.3e-6, all of it one-sided and growing with the context, for 7 % less time at 128, 1 %
+// at 64.  The product lo lo', or rounding lo, changes none of these figures.)  Three
+// m16n8k8 products take 24 cycles of a scheduler's tensor pipe for 1024 multiply-adds;
+// fused multiply-adds take 32, and two operands from shared memory for each sixteenth
+// of them.  The order of the summed index is free in a product, so it is chosen to suit
+// the fragments: a thread's four neighbouring elements of q and k are its columns of two
+// steps, a thread's scores of neighbouring keys are its columns of P, and its four
+// neighbouring columns of v belong to four tiles of O.  Every operand is read as float4,
+// with strides that keep eight lanes on 32 banks.
 //   Five in six instructions are not products (splits, operand loads, the softmax),
-// and the pipe is busy about 62 % of the time: a prompt of 4096 with 32 heads on 8
-// takes 1.09 ms at head_dim 64 and 2.13 ms at 128 (a seventh more with tiles of 32 keys
-// and two CTAs per SM), 64 TFLOP/s of the formula; with fused multiply-adds it ran at
-// 12.
+// and the pipe is busy about 60 % of the time: a prompt of 4096 with 32 heads on 8
+// takes 1.12 ms at head_dim 64 and 2.30 ms at 128, 61 and 60 TFLOP/s of the formula; with
+// fused multiply-adds it ran at 12.
 //
 // bf16 (tiles of 64 keys, 32 at head_dim 128): operands by ldmatrix from rows whose
 // 16-byte chunks are permuted by the row, so that no two lanes share a bank.  P is
@@ -38,10 +43,10 @@
 // over 100 keys: 5.0 us, the launch, four dependent loads and two tiles).
 //
 // Few row tiles: each is split over the keys, up to eight ways in a cluster that
-// joins its parts through distributed shared memory (fp32, a prompt of 128: 7.2 us; with
-// a second launch for the join 12.5), and beyond that in several clusters, whose parts
-// a second launch joins (4 tokens over 30,000 keys 24 us; with 64 parts all joined by
-// the launch, 52).
+// joins its parts through distributed shared memory (fp32, a prompt of 128 with 16 heads on 2
+// of 64: 8.1 us, where a second launch for the join took 5 more), and beyond that in several
+// clusters, whose parts a second launch joins (4 tokens over 30,000 keys 30 us; 49 with
+// 64 parts).
 //
 // inf * 0 and inf - inf would make NaN of what a row sees as an infinite value, or
 // does not see at all.  Values that are not finite (bf16: in tiles that some row does
@@ -141,13 +146,15 @@ struct CoreF32 {
     }
     static __device__ __forceinline__ void clamp(float& x) { x = fminf(fmaxf(x, -kTop), kTop); }
 
-    // S = Q K^T: s[i] the 8 keys from 8 i, this warp's 16 rows
+    // S = Q K^T: s[i] the 8 keys from 8 i, this warp's 16 rows.  The small products have a
+    // sum of their own: cut off at its last bit they lose 2^-12 of what they lose at s's.
     static __device__ __forceinline__ void scores(float (&s)[BN / 8][4], const unsigned char* sq,
                                                   const unsigned char* k, int warp, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const float* qw = reinterpret_cast<const float*>(sq) + (16 * warp + g) * LQ + 4 * t;
         const float* sk = reinterpret_cast<const float*>(k);
-#pragma unroll 2
+        float small[BN / 8][4] = {};
+#pragma unroll 4
         for (int d = 0; d < D; d += 16) {
             uint32_t ah[2][4], al[2][4];
 #pragma unroll
@@ -167,13 +174,17 @@ struct CoreF32 {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int i = 0; i < BN / 8; ++i) mma8(s[i], al[u], bh[i][2 * u], bh[i][2 * u + 1]);
+                for (int i = 0; i < BN / 8; ++i) mma8(small[i], al[u], bh[i][2 * u], bh[i][2 * u + 1]);
 #pragma unroll
-                for (int i = 0; i < BN / 8; ++i) mma8(s[i], ah[u], bl[i][2 * u], bl[i][2 * u + 1]);
+                for (int i = 0; i < BN / 8; ++i) mma8(small[i], ah[u], bl[i][2 * u], bl[i][2 * u + 1]);
 #pragma unroll
                 for (int i = 0; i < BN / 8; ++i) mma8(s[i], ah[u], bh[i][2 * u], bh[i][2 * u + 1]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < BN / 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[i][k] += small[i][k];
         // x - hi is NaN for an infinite x: scores that are not finite are summed plainly
         float z = 0.f;
 #pragma unroll
@@ -198,31 +209,39 @@ struct CoreF32 {
         }
     }
 
-    // O += P V: step i sums over keys 8 i + (2 t, 2 t + 1)
+    // O += P V: step i sums over keys 8 i + (2 t, 2 t + 1); the tile's sum starts from zero
     static __device__ __forceinline__ void values(float (&o)[D / 8][4], const float (&s)[BN / 8][4],
                                                   const unsigned char* v, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const float* sv = reinterpret_cast<const float*>(v);
+        uint32_t ah[BN / 8][4], al[BN / 8][4];
 #pragma unroll
         for (int i = 0; i < BN / 8; ++i) {
-            uint32_t ah[4], al[4];
-            split(s[i][0], ah[0], al[0]), split(s[i][2], ah[1], al[1]);
-            split(s[i][1], ah[2], al[2]), split(s[i][3], ah[3], al[3]);
-            const float* v0 = sv + (8 * i + 2 * t) * LV + 4 * g;
+            split(s[i][0], ah[i][0], al[i][0]), split(s[i][2], ah[i][1], al[i][1]);
+            split(s[i][1], ah[i][2], al[i][2]), split(s[i][3], ah[i][3], al[i][3]);
+        }
 #pragma unroll
-            for (int d = 0; d < D; d += 32) {
+        for (int d = 0; d < D; d += 32) {
+            float part[4][4] = {};
+#pragma unroll
+            for (int i = 0; i < BN / 8; ++i) {
+                const float* v0 = sv + (8 * i + 2 * t) * LV + 4 * g;
                 const float4 x = lds4(v0 + d), y = lds4(v0 + LV + d);
                 const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
                 uint32_t bh[4][2], bl[4][2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) split(xs[e], bh[e][0], bl[e][0]), split(ys[e], bh[e][1], bl[e][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma8(o[d / 8 + e], al, bh[e][0], bh[e][1]);
+                for (int e = 0; e < 4; ++e) mma8(part[e], al[i], bh[e][0], bh[e][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma8(o[d / 8 + e], ah, bl[e][0], bl[e][1]);
+                for (int e = 0; e < 4; ++e) mma8(part[e], ah[i], bl[e][0], bl[e][1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma8(o[d / 8 + e], ah, bh[e][0], bh[e][1]);
+                for (int e = 0; e < 4; ++e) mma8(part[e], ah[i], bh[e][0], bh[e][1]);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[d / 8 + e][k] += part[e][k];
         }
     }
 };
@@ -688,11 +707,11 @@ bool prefill_mma_preferred(int G, int Hkv, int batch, int num_tokens, int maxb, 
 // eight are a cluster, which joins them by itself: of 1, 2, 4 and 8 the one with the
 // shortest estimate.  A part takes its key tiles and 2.5 more (start, join); an SM's
 // share of them takes 0.62 of their times' sum, for three run at once, and half a part
-// more until all have ended.  (fp32, 1 / 2 / 4 / 8 parts: 500 tokens of 16 heads behind
-// 7,300, 125 row tiles, 1191 / 889 / 630 / 565 us; 4 sequences of up to 130 tokens, 38 row
-// tiles of 14 key tiles, 29.6 / 22.6 / 18.4 / 21.2; 24 of up to 212 behind 2,000 - 2,800, 672
-// row tiles, 1076 / 858 / 876 / 952.)  More than eight take a second launch: where two
-// CTAs per SM ask for 16 and each has a tile (4 tokens over 30,000 keys: 152 parts 26
+// more until all have ended.  (fp32, 1 / 2 / 4 / 8 parts: 500 tokens of 16 heads of 128
+// behind 7,300, 125 row tiles, 1460 / 954 / 707 / 677 us; 4 sequences of up to 130 tokens, 38
+// row tiles of 14 key tiles, 29.0 / 22.6 / 18.6 / 21.6; 24 of up to 212 behind 2,000 - 2,800, 672
+// row tiles, 917 / 781 / 779 / 843.)  More than eight take a second launch: where two
+// CTAs per SM ask for 16 and each has a tile (4 tokens over 30,000 keys: 152 parts 30
 // us, 256 33).
 int prefill_mma_splits(int dtype, int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
                        int num_sms, int* cluster) {

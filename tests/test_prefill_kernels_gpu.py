@@ -245,3 +245,33 @@ def test_serving_run(cuda_device, kernel, d, h, hkv, monkeypatch):
 
     monkeypatch.setattr(ops, "BlockPool", Forced)
     ops.test_serving_run(cuda_device, "bf16", d, h, hkv)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,hkv,new,ctx", [(8, 2, [2048], [4096]), (16, 4, [700, 600], [3000, 5000]),
+                                           (16, 2, [4], [60000])])
+def test_f32_sums_do_not_drift(cuda_device, d, h, hkv, new, ctx):
+    """fp32 outputs over thousands of keys are off by what roundings to nearest leave, not by
+    a share that grows with the context (a sum kept in the tensor core's accumulator is
+    cut toward zero at every step).
+
+    The drift is the mean of error * sign, relative to the mean magnitude: random errors
+    leave nothing of it.  Inside one tile of at most 32 keys 12 products are summed in the
+    tensor core and each cut by at most 2^-23, half on average: 12 * 2^-24.  Scores are
+    cut D / 8 times, on average by 2^-25 of themselves, which moves an output by as much
+    for scores of size 1: D / 8 * 2^-25.  Errors of either sign beside it: an addition
+    to O per tile, 2^-24 each, grows by its root (at most 16 of them at 4,096 keys unsplit),
+    the exponent's rounding and ex2 (2^-22): 2^-20 in all."""
+    dev = cuda_device
+    pool_t, tables, q = ragged(dev, d, 16, h, hkv, new, ctx, 30)
+    pool_t, q = pool_t.float(), q.float() / 1.5
+    cache = BlockPool(pool_t.shape[0], 16, 1, hkv, d, tensor=pool_t)
+    got = cache.prefill_attention(q, 0, ints(tables, dev), ints(ctx, dev), ints(R.starts_of(new), dev), d ** -0.5)
+    want, _ = R.prefill(pool_t, q, tables, ctx, new, d ** -0.5)
+    err = got.double() - want
+    drift = (err * want.sign()).mean() / want.abs().mean()
+    limit = 12 * 2.0 ** -24 + d / 8 * 2.0 ** -25
+    assert abs(drift.item()) <= limit, f"drift {drift.item():.2e}, limit {limit:.2e}"
+    rms = (err.pow(2).mean() / want.pow(2).mean()).sqrt().item()
+    assert rms <= limit + 2.0 ** -20, f"rms {rms:.2e}"
+    cache.close()
