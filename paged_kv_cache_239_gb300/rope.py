@@ -22,8 +22,12 @@ class Rope:
     times over ``original_len`` positions are divided by ``factor``, those that
     turn ``high`` times or more are kept, the rest blended).  ``frequencies``
     (rotary_dim / 2 numbers, radians per position) replaces all of these.
-    ``amplitude`` scales the rotated elements; YaRN's is 0.1 ln(factor) + 1, with
-    'parts', low 1 and high 32.
+    ``amplitude`` scales the rotated elements.
+
+    The blend of 'parts' is linear in the turns, as in YaRN's formula (low 1, high 32,
+    amplitude 0.1 ln(factor) + 1).  Models are also trained with a blend that is linear
+    in the pair's index j, between the pairs that turn ``high`` and ``low`` times: other
+    numbers in between, which such a model needs given as ``frequencies``.
     """
 
     def __init__(self, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
