@@ -482,7 +482,8 @@ PA_API int pa_gather_kv(void* k_out, void* v_out, uint8_t* mask, const pa_pool* 
  * last n_b of its context_lens[b]; the i-th stands at position
  * context_lens[b] - n_b + i.  query_starts: device int32 [batch + 1], from 0,
  * not decreasing, at most num_tokens at the end (n_b = 0 is fine).  Rows
- * behind the last sequence are neither read nor written.  A sequence with
+ * behind the last sequence (of the num_tokens, which must be there) are not
+ * written, and what they hold reaches nothing.  A sequence with
  * n_b > context_lens[b] or a length past its table sets PA_STATUS_BAD_LENGTH
  * and its output rows are zero; starts that break the rule above set it too,
  * and the output is unspecified.
@@ -593,6 +594,11 @@ PA_API int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, i
 /* Which kernel a pool's prefill attention uses.  PA_PREFILL_AUTO (default): fp32
  * pools mma.sync (TF32 products of split operands); bf16 pools mma.sync for calls
  * that its short start makes faster, by an estimate from the sizes, else tcgen05.
+ * The lengths are on the device: the estimate, and how an fp32 or mma.sync call is
+ * split, take every context to be as long as the table is wide.  With a table much
+ * wider than the contexts of a short call, force PA_PREFILL_MMA (one token over 100
+ * keys, 16 heads on 2 of 64: 5.0 us in a table of 7 blocks; in one of 8,192 11.1 by
+ * choice, 8.2 by force).
  * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at the call.
  * The workspace size follows the choice.
  * Cites: no counterpart on the pages (a choice among this library's kernels). */

@@ -154,8 +154,10 @@ __device__ __forceinline__ int fork_pages_before(const ForkParams& p, int n) {
 // Child blockIdx.x takes its parent's table: full pages by reference, the
 // partial last page (if any) as a page of its own from the stack's top, in
 // increasing order of the children.  Each CTA counts the pages that the
-// children before its own take (n / 256 steps at most, against a second launch's
-// latency), so that the rows and the copies run side by side; CTAs (x,
+// children before its own take, so that the rows and the copies run side by side and
+// no launch comes before them: n / 256 steps at most per CTA, n^2 / 512 in the grid, which
+// is nothing for a batch's children and all there is to it for tens of thousands
+// (pages of 4 KiB: 128 children 6.0 us, 1,024 12.4, 8,192 137, 65,536 7.0 ms).  CTAs (x,
 // 0) write the rows, all of them copy the tiles of the last page.  The stack's
 // height is set by the kernel after this one, since every CTA reads it here.
 __global__ void __launch_bounds__(kCopyThreads) pa_fork_kernel(const ForkParams p) {

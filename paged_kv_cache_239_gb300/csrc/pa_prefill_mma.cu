@@ -31,7 +31,7 @@
 // neighbouring columns of v belong to four tiles of O.  Every operand is read as float4,
 // with strides that keep eight lanes on 32 banks.
 //   Five in six instructions are not products (splits, operand loads, the softmax),
-// and the pipe is busy about 60 % of the time: a prompt of 4096 with 32 heads on 8
+// and the pipe is busy 56 % of the time: a prompt of 4096 with 32 heads on 8
 // takes 1.12 ms at head_dim 64 and 2.30 ms at 128, 61 and 60 TFLOP/s of the formula; with
 // fused multiply-adds it ran at 12.
 //
@@ -693,6 +693,11 @@ bool prefill_supported(int dtype, int D, int B) {
 // / 14.3, of 1,024 19.0 / 17.9; 32 sequences of 5 tokens over 2,000 18.7 / 21.6; 32
 // heads on 8 of 128: 8 sequences of one token over 1,000 13.1 / 19.6, a prompt of 128
 // 10.1 / 12.0, of 512 22.1 / 20.7, 8 of 128 24.1 / 14.8.)
+//   The lengths are on the device, so the tables' width stands for them here and in the
+// splits below.  In a table of 8,192 blocks, far wider than the contexts, short calls
+// take tcgen05 where this kernel is the faster: one token over 100 keys 8.2 / 11.1 (of
+// 128: 7.9 / 13.0), 8 of one token over 1,000 8.6 / 13.8 (17.3 / 18.6), a prompt of 128 7.8
+// / 12.3 (but 17.0 / 13.2); fp32, cut finer than its keys ask for, 9.3 in place of 6.0.
 bool prefill_mma_preferred(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
                            int num_sms) {
     const double keys = (double)maxb * B, rows = (double)num_tokens * G;

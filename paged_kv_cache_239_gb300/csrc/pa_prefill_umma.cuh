@@ -47,8 +47,9 @@
 // cycles of the tensor pipe, and takes about 2700, since S(i + 1) waits for the
 // softmax of S(i) to leave the columns that P stands in, with 512 columns for two
 // row tiles' S and O (the exponentials, 2048 cycles of the special-function units,
-// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 353 - 357 us, 1.55 PFLOP/s
-// of the causal half (81 % of a large library product's burst rate).  Measured and
+// run beside).  A prompt of 8192 with 32 heads on 8 of 128: 353 - 358 us in a graph of
+// such calls on warm caches, 1.54 PFLOP/s of the causal half (80 % of a large library
+// product's burst rate); 382 - 386, 1.43 PFLOP/s, as a call among others.  Measured and
 // slower, at a time when this form took 400: two threads to a row 450; two issuing
 // threads 480; P handed over in halves 409.  Without the exponentials it took 383.
 // Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 150
