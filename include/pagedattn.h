@@ -561,6 +561,26 @@ PA_API int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const vo
                                  int num_tokens, int num_heads, pa_stream_t stream);
 
 /*
+ * pa_norm_rope_write_kv for tokens that are not in the order of their positions (a drafted
+ * tree's: branches side by side in the cache, positions by depth): token t is rotated at
+ * positions[t] and its key and value go to slots[t] = page * block_size + row, both as
+ * pa_device_plan_tokens writes them.
+ *   positions     device int32 [num_tokens], >= 0 (PA_STATUS_BAD_LENGTH: the token's query
+ *                 is zero and nothing of it is stored).
+ *   slots         device int64 [num_tokens], 8-byte aligned, no two the same.  A
+ *                 negative one is no token: nothing of it is written.  A page outside
+ *                 the pool sets PA_STATUS_BAD_BLOCK_ID; that key and value are not stored.
+ * The other arguments as there.
+ * Cites: as pa_norm_rope_write_kv.
+ */
+PA_API int pa_norm_rope_write_kv_slots(pa_pool* pool, int layer, void* q_out, const void* q,
+                                       int64_t q_stride, const void* k, int64_t k_stride,
+                                       const void* v, int64_t v_stride, const pa_rope* rope,
+                                       const void* q_weight, const void* k_weight, float eps,
+                                       const int* positions, const int64_t* slots, int num_tokens,
+                                       int num_heads, pa_stream_t stream);
+
+/*
  * Causal attention of the new tokens over the cache, which holds them already
  * (prompts, chunks of prompts behind a cached prefix, a few tokens to verify):
  *   out[t][h] = softmax_s(scale * q[t][h] . K_s) V_s over s <= position of t,
@@ -590,6 +610,34 @@ PA_API int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, i
                                 const int* context_lens, const int* query_starts, int batch,
                                 int num_tokens, int num_heads, float scale, void* workspace,
                                 size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_prefill_attention with a mask for each new token in place of the causal order: the i-th
+ * of sequence b's n_b new tokens sees the context_lens[b] - n_b tokens before them and
+ * the new tokens j < n_b whose bits are set in its mask (its ancestors in a tree of drafted
+ * tokens, and itself).
+ *   tree_masks    device uint32 [num_tokens, mask_words], row-major, 4-byte aligned; bit
+ *                 j % 32 of word j / 32 is new token j of the row's sequence.  Bits from
+ *                 n_b on are not used.  A row that sees nothing is zero.
+ *   mask_words    1 .. 32.  A sequence of more than 32 * mask_words new tokens sets
+ *                 PA_STATUS_BAD_LENGTH and its output rows are zero.
+ * The other arguments, the products' rounding, bad entries and the choice of the kernel
+ * (pa_pool_set_prefill_kernel) as there; the workspace is pa_tree_workspace_size().  What
+ * lies in the cache at positions that a row does not see, be it NaN, does not reach it.
+ * Cites: as pa_prefill_attention.
+ */
+PA_API int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int layer,
+                             const int* block_tables, int max_blocks_per_seq,
+                             const int* context_lens, const int* query_starts,
+                             const uint32_t* tree_masks, int mask_words, int batch, int num_tokens,
+                             int num_heads, float scale, void* workspace, size_t workspace_bytes,
+                             pa_stream_t stream);
+
+/* Workspace bytes of pa_tree_attention for these sizes on the current device (0 when
+ * nothing is split).
+ * Cites: no counterpart on the pages (the scratch of split contexts). */
+PA_API int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens, int num_heads,
+                                  int max_blocks_per_seq, size_t* bytes);
 
 /* Which kernel a pool's prefill attention uses.  PA_PREFILL_AUTO (default): fp32
  * pools mma.sync (TF32 products of split operands); bf16 pools mma.sync for calls
@@ -702,6 +750,96 @@ PA_API int pa_device_compact_blocks(pa_pool* pool, const void* dev_stack, const 
 /* Workspace bytes of pa_device_compact_blocks.
  * Cites: no counterpart on the pages (as pa_device_compact_blocks). */
 PA_API int pa_compact_workspace_size(const pa_pool* pool, size_t* bytes);
+
+/* ----------------------------------------------------------------------------
+ * New tokens planned, drafted trees decided, pages given back: with
+ * pa_norm_rope_write_kv_slots and pa_tree_attention a step of tree speculation (or, without
+ * trees, the admission of prompts) that never waits for the host.
+ *
+ * A tree of drafted tokens is the sequence's n_b new tokens in any order that puts a
+ * parent before its children: token 0 is the root, the last token that is certain, whose K
+ * and V are not yet cached.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Gives n_b = new_counts[b] new tokens to every sequence of cached_lens[b] tokens: the pages
+ * of the blocks that it starts, popped from the stack in increasing order of sequence and block
+ * into its table row, and, in rows query_starts[b] .. of the batch, where each token goes.
+ *   parents       device int32 [num_tokens], each row's parent as an index within its
+ *                 sequence's new tokens, -1 for a root; NULL: each token follows the one
+ *                 before it.  A parent that is not below its child sets
+ *                 PA_STATUS_BAD_LENGTH and counts as -1.
+ *   num_tokens    rows of the batch, at least the sum of the counts.
+ *   context_lens  [batch]: cached_lens[b] + n_b.
+ *   query_starts  [batch + 1]: the prefix sums of n_b.
+ *   slots         int64 [num_tokens], 8-byte aligned: page * block_size + row, -1 behind
+ *                 the last sequence and where a page is missing.
+ *   positions     int32 [num_tokens]: cached_lens[b] and the token's depth below its root
+ *                 (parents NULL: its index); 0 behind the last sequence.
+ *   tree_masks    uint32 [num_tokens, mask_words], as pa_tree_attention reads them: the token
+ *                 and its ancestors; NULL: none are written.
+ * All device arrays, 4-byte aligned if not said otherwise; no output (the stack and the
+ * tables among them) overlaps an input or another output.  A length or count below 0,
+ * past the table or above 32 * mask_words (where masks are written) sets
+ * PA_STATUS_BAD_LENGTH, and the sequence gets no tokens; so do the sequences from the first
+ * whose tokens do not fit into num_tokens.  When the stack runs dry the entries of the pages
+ * that were not to be had are -1 (PA_STATUS_NO_FREE_BLOCKS); so are stack ids outside
+ * the pool, and the slots in a cached last page whose entry is no page
+ * (PA_STATUS_BAD_BLOCK_ID).  The last cached page must not be shared: the new tokens go into
+ * it (pa_device_fork_sequences gives each child its own).
+ * Cites: mini-infer, "Python Implementation: Physical Block Pool" (allocate_block, once per
+ * block that is needed); "vllmini", "PagedAttention Metaphor" (token t in block t / B of the
+ * table, at offset t % B).
+ */
+PA_API int pa_device_plan_tokens(pa_pool* pool, void* dev_stack, int* block_tables,
+                                 int max_blocks_per_seq, const int* cached_lens,
+                                 const int* new_counts, const int* parents, int batch,
+                                 int num_tokens, int* context_lens, int* query_starts,
+                                 int64_t* slots, int* positions, uint32_t* tree_masks,
+                                 int mask_words, pa_stream_t stream);
+
+/*
+ * Sequences shortened from context_lens[b] to new_lens[b] tokens: the pages of blocks past
+ * ceil(new_lens[b] / B) go back on the stack and their entries become -1.  The last block
+ * of the last sequence goes first, so a plan that is trimmed back leaves the stack as it was.
+ * The pages must have one owner each.  new_lens[b] outside [0, context_lens[b]] or a length
+ * past the table sets PA_STATUS_BAD_LENGTH and the row stays; ids outside the pool are
+ * skipped (PA_STATUS_BAD_BLOCK_ID).
+ * Cites: mini-infer, "Python Implementation: Physical Block Pool" (free_block, once per block
+ * that is no longer needed).
+ */
+PA_API int pa_device_trim_sequences(pa_pool* pool, void* dev_stack, int* block_tables,
+                                    int max_blocks_per_seq, const int* context_lens,
+                                    const int* new_lens, int batch, pa_stream_t stream);
+
+/*
+ * Decides every sequence's tree.  The root is accepted; a node is when its parent is and
+ * tokens[node] == targets[parent], the lowest node where there are several; of the path
+ * at most max_path nodes are kept.  The K and V of its k-th node move, in every layer, from
+ * slots[node] to slots[query_starts[b] + k], so that the accepted tokens follow the cached
+ * ones.
+ *   slots, parents  as pa_device_plan_tokens wrote and read them; the slots are distinct.
+ *   tokens, targets device int32 [num_tokens]: the drafted token of each row, and the
+ *                   model's choice (greedy or sampled) of the token after it.
+ *   context_lens, query_starts  the batch's, the new tokens included.
+ *   max_path        1 .. 1024.
+ *   accepted_counts [batch]; accepted_nodes [batch, max_path], the path, -1 past it;
+ *   next_tokens     [batch]: targets of the last accepted node (the next root; -1 where
+ *                   the sequence had no new tokens);
+ *   next_lens       [batch]: context_lens[b] - n_b + accepted_counts[b], for
+ *                   pa_device_trim_sequences and the next plan.
+ * Device int32, no output overlaps an input or another.  Starts that are no starts, more
+ * than 1024 new tokens or more than context_lens[b] set PA_STATUS_BAD_LENGTH: nothing is
+ * accepted and the length stays; a parent that is not below its child sets it too, and the
+ * node is not accepted.  A slot that is no page's (a dry stack's -1 among them) sets
+ * PA_STATUS_BAD_BLOCK_ID and that row does not move.
+ * Cites: no counterpart on the pages (they draft no tokens).
+ */
+PA_API int pa_device_accept_tree(pa_pool* pool, const int64_t* slots, const int* parents,
+                                 const int* tokens, const int* targets, const int* context_lens,
+                                 const int* query_starts, int batch, int num_tokens, int max_path,
+                                 int* accepted_counts, int* accepted_nodes, int* next_tokens,
+                                 int* next_lens, pa_stream_t stream);
 
 /* ----------------------------------------------------------------------------
  * Device status.

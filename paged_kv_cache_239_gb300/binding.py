@@ -126,6 +126,13 @@ _SIGNATURES = {
     "pa_device_free_shared": ([_P, _P, _P, _P, _I, _P, _P, _I, _P], _I),
     "pa_device_compact_blocks": ([_P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P], _I),
     "pa_compact_workspace_size": ([_P, _PSZ], _I),
+    "pa_norm_rope_write_kv_slots": ([_P, _I, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P, _F, _P, _P, _I,
+                                     _I, _P], _I),
+    "pa_tree_attention": ([_P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _F, _P, _SZ, _P], _I),
+    "pa_tree_workspace_size": ([_P, _I, _I, _I, _I, _PSZ], _I),
+    "pa_device_plan_tokens": ([_P, _P, _P, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P], _I),
+    "pa_device_trim_sequences": ([_P, _P, _P, _I, _P, _P, _I, _P], _I),
+    "pa_device_accept_tree": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P], _I),
     "pa_get_status": ([_PU, _P], _I),
     "pa_selftest_wait_timeout": ([_P], _I),
 }
@@ -462,6 +469,33 @@ def pa_prefill_attention(out, q, pool: int, layer: int, block_tables, max_blocks
         _ptr(workspace), workspace_bytes, _stream(stream)), "pa_prefill_attention")
 
 
+def pa_norm_rope_write_kv_slots(pool: int, layer: int, q_out, q, q_stride: int, k, k_stride: int, v,
+                                v_stride: int, rope, q_weight, k_weight, eps: float, positions,
+                                slots, num_tokens: int, num_heads: int, stream=None) -> None:
+    _check(lib().pa_norm_rope_write_kv_slots(
+        pool, layer, _ptr(q_out), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, rope,
+        _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(slots), num_tokens, num_heads,
+        _stream(stream)), "pa_norm_rope_write_kv_slots")
+
+
+def pa_tree_attention(out, q, pool: int, layer: int, block_tables, max_blocks_per_seq: int,
+                      context_lens, query_starts, tree_masks, mask_words: int, batch: int,
+                      num_tokens: int, num_heads: int, scale: float, workspace=None,
+                      workspace_bytes: int = 0, stream=None) -> None:
+    _check(lib().pa_tree_attention(
+        _ptr(out), _ptr(q), pool, layer, _ptr(block_tables), max_blocks_per_seq,
+        _ptr(context_lens), _ptr(query_starts), _ptr(tree_masks), mask_words, batch, num_tokens,
+        num_heads, scale, _ptr(workspace), workspace_bytes, _stream(stream)), "pa_tree_attention")
+
+
+def pa_tree_workspace_size(pool: int, batch: int, num_tokens: int, num_heads: int,
+                           max_blocks_per_seq: int) -> int:
+    v = _SZ()
+    _check(lib().pa_tree_workspace_size(pool, batch, num_tokens, num_heads, max_blocks_per_seq,
+                                        ctypes.byref(v)), "pa_tree_workspace_size")
+    return v.value
+
+
 def pa_pool_set_prefill_kernel(pool: int, kind: int) -> None:
     _check(lib().pa_pool_set_prefill_kernel(pool, kind), "pa_pool_set_prefill_kernel")
 
@@ -512,6 +546,37 @@ def pa_compact_workspace_size(pool: int) -> int:
     v = _SZ()
     _check(lib().pa_compact_workspace_size(pool, ctypes.byref(v)), "pa_compact_workspace_size")
     return v.value
+
+
+# ------------------------------------- new tokens planned, trees decided
+
+
+def pa_device_plan_tokens(pool: int, dev_stack, block_tables, max_blocks_per_seq: int, cached_lens,
+                          new_counts, parents, batch: int, num_tokens: int, context_lens,
+                          query_starts, slots, positions, tree_masks, mask_words: int,
+                          stream=None) -> None:
+    _check(lib().pa_device_plan_tokens(
+        pool, _ptr(dev_stack), _ptr(block_tables), max_blocks_per_seq, _ptr(cached_lens),
+        _ptr(new_counts), _ptr(parents), batch, num_tokens, _ptr(context_lens),
+        _ptr(query_starts), _ptr(slots), _ptr(positions), _ptr(tree_masks), mask_words,
+        _stream(stream)), "pa_device_plan_tokens")
+
+
+def pa_device_trim_sequences(pool: int, dev_stack, block_tables, max_blocks_per_seq: int,
+                             context_lens, new_lens, batch: int, stream=None) -> None:
+    _check(lib().pa_device_trim_sequences(
+        pool, _ptr(dev_stack), _ptr(block_tables), max_blocks_per_seq, _ptr(context_lens),
+        _ptr(new_lens), batch, _stream(stream)), "pa_device_trim_sequences")
+
+
+def pa_device_accept_tree(pool: int, slots, parents, tokens, targets, context_lens, query_starts,
+                          batch: int, num_tokens: int, max_path: int, accepted_counts,
+                          accepted_nodes, next_tokens, next_lens, stream=None) -> None:
+    _check(lib().pa_device_accept_tree(
+        pool, _ptr(slots), _ptr(parents), _ptr(tokens), _ptr(targets), _ptr(context_lens),
+        _ptr(query_starts), batch, num_tokens, max_path, _ptr(accepted_counts),
+        _ptr(accepted_nodes), _ptr(next_tokens), _ptr(next_lens), _stream(stream)),
+        "pa_device_accept_tree")
 
 
 def pa_get_status(stream=None) -> int:

@@ -974,6 +974,152 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
     return PA_OK;
 }
 
+// What both forms of the norm + rotation + append check and fill in; the caller has set
+// p->num_tokens and where the tokens go.  *done: there is nothing to launch.
+int norm_rope_params(pa_pool* pool, int layer, void* q_out, const void* q, int64_t q_stride,
+                     const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     const pa_rope* rope, const void* q_weight, const void* k_weight, float eps,
+                     int num_heads, bool empty, pa::NormRopeParams* out, bool* done) {
+    const pa::PoolGeom& g = pool->g;
+    pa::NormRopeParams& p = *out;
+    const int num_tokens = p.num_tokens;
+    *done = false;
+    if (num_heads <= 0 || num_heads % g.Hkv != 0)
+        return fail(PA_ERR_INVALID_ARG, "num_heads %d is not a positive multiple of num_kv_heads %d",
+                    num_heads, g.Hkv);
+    if (g.D != 64 && g.D != 128)
+        return fail(PA_ERR_UNSUPPORTED, "norm and rotation are built for head_dim 64 and 128, not %d",
+                    g.D);
+    if (rope && rope->rotary_dim > g.D)
+        return fail(PA_ERR_INVALID_ARG, "rotary_dim %d is above head_dim %d", rope->rotary_dim, g.D);
+    if (!q_weight != !k_weight)
+        return fail(PA_ERR_INVALID_ARG, "q_weight and k_weight: both or neither");
+    if (q_weight && !(eps >= 0.f && std::isfinite(eps)))
+        return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (empty) {
+        *done = true;
+        return PA_OK;
+    }
+    if (!q_out || !q || !k || !v || !aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) ||
+        !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+        return fail(PA_ERR_INVALID_ARG,
+                    "q_out, q, k, v must be non-NULL and, as the weights, 16-byte aligned");
+    const struct {
+        int64_t stride;
+        int heads;
+        const void* at;
+        const char* name;
+    } in[3] = {{q_stride, num_heads, q, "q"}, {k_stride, g.Hkv, k, "k"}, {v_stride, g.Hkv, v, "v"}};
+    const size_t out_bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
+    for (const auto& x : in) {
+        const int64_t row = (int64_t)x.heads * g.D;
+        if (x.stride < row || x.stride * g.elt % 16 != 0 || x.stride > (int64_t)1 << 40)
+            return fail(PA_ERR_INVALID_ARG,
+                        "%s_stride %lld: at least the row (%lld elements), a multiple of 16 bytes",
+                        x.name, (long long)x.stride, (long long)row);
+        if (x.at == q_out && x.at == q && q_stride == row) continue;  // in place
+        const size_t bytes = ((size_t)(num_tokens - 1) * x.stride + row) * g.elt;
+        if (overlap(q_out, out_bytes, x.at, bytes))
+            return fail(PA_ERR_INVALID_ARG, "q_out overlaps %s", x.name);
+    }
+    cudaError_t e = pa::status_word(&p.status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    p.q_out = q_out;
+    p.q = q, p.k = k, p.v = v;
+    p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
+    p.q_weight = q_weight, p.k_weight = k_weight;
+    p.eps = eps;
+    p.k_base = g.k_base, p.v_base = g.v_base;
+    p.s_blk = g.s_blk, p.tile_off = layer * g.s_layer, p.s_head = g.s_head;
+    p.num_blocks = g.num_blocks;
+    p.H = num_heads, p.Hkv = g.Hkv, p.B = g.B;
+    p.amplitude = 1.f;
+    if (rope) {
+        p.rotary = rope->rotary_dim;
+        p.interleaved = rope->interleaved;
+        p.amplitude = rope->amplitude;
+        std::copy(rope->freq, rope->freq + rope->rotary_dim / 2, p.freq);
+    }
+    return PA_OK;
+}
+
+int norm_rope_launch(const pa_pool* pool, const pa::NormRopeParams& p, const char* what,
+                     pa_stream_t stream) {
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    const cudaError_t e = pa::launch_norm_rope(p, pool->g.dtype, pool->g.D, sms,
+                                               reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, what);
+}
+
+// Attention of new tokens: causal, or (tree_masks) of drafted trees.
+int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const int* block_tables,
+               int max_blocks_per_seq, const int* context_lens, const int* query_starts,
+               const uint32_t* tree_masks, int mask_words, int batch, int num_tokens, int num_heads,
+               float scale, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_layer(pool, layer)) return rc;
+    const pa::PoolGeom& g = pool->g;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
+    if (!std::isfinite(scale * 1.4426950408889634f))
+        return fail(PA_ERR_INVALID_ARG, "scale is not finite (times log2 e)");
+    PrefillShape sh;
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
+        return rc;
+    if (batch == 0 || num_tokens == 0) return PA_OK;
+    if (!out || !q || !aligned(out, 16) || !aligned(q, 16))
+        return fail(PA_ERR_INVALID_ARG, "out and q must be non-NULL and 16-byte aligned");
+    if (!query_starts || !aligned(query_starts, 4))
+        return fail(PA_ERR_INVALID_ARG, "query_starts must be non-NULL and 4-byte aligned");
+    const size_t bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
+    if (overlap(out, bytes, q, bytes)) return fail(PA_ERR_INVALID_ARG, "out overlaps q");
+    if (sh.ws_bytes &&
+        (!workspace || workspace_bytes < sh.ws_bytes || !aligned(workspace, 256)))
+        return fail(PA_ERR_WORKSPACE,
+                    "workspace must be 256-byte aligned and hold %zu bytes (got %p, %zu)",
+                    sh.ws_bytes, workspace, workspace_bytes);
+    pa::PrefillParams p{};
+    cudaError_t e = pa::status_word(&p.status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    p.out = out;
+    p.q = q;
+    p.k_base = g.k_base, p.v_base = g.v_base;
+    p.s_blk = g.s_blk, p.tile_off = layer * g.s_layer, p.s_head = g.s_head;
+    p.num_blocks = g.num_blocks;
+    p.H = num_heads, p.Hkv = g.Hkv, p.G = num_heads / g.Hkv, p.layer = layer;
+    p.bt = block_tables, p.maxb = max_blocks_per_seq;
+    p.lens = context_lens, p.starts = query_starts;
+    p.batch = batch, p.num_tokens = num_tokens;
+    p.masks = tree_masks, p.words = mask_words;
+    p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax evaluated with exp2
+    p.splits = sh.splits, p.cluster = sh.cluster;
+    p.grid = sh.grid;
+    if (sh.ws_bytes) {
+        char* ws = static_cast<char*>(workspace);
+        p.part_o = reinterpret_cast<float*>(ws);
+        p.part_ml = reinterpret_cast<float*>(ws + sh.ml_off);
+        if (sh.grid) p.cut = reinterpret_cast<int4*>(ws + sh.cut_off);
+    }
+    // division by G: with s = ceil(log2 G) and m = ceil(2^(31 + s) / G), x m
+    // >> (31 + s) is exact for x < 2^31 (m G - 2^(31 + s) < G <= 2^s)
+    p.div_shift = 31;
+    while ((1LL << (p.div_shift - 31)) < p.G) ++p.div_shift;
+    p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (sh.grid) {
+        if (int rc = pool_tmaps(pool)) return rc;
+        p.slot_blk = pool->tma_slots[0];
+        p.slot_layer = pool->tma_slots[1];
+        e = tree_masks ? pa::launch_tree_umma(p, pool->tmaps, g.D, g.B, s)
+                       : pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
+    } else {
+        e = tree_masks ? pa::launch_tree_mma(p, g.dtype, g.D, g.B, s)
+                       : pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
+    return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1049,76 +1195,46 @@ int pa_norm_rope_write_kv(pa_pool* pool, int layer, void* q_out, const void* q, 
                           int num_tokens, int num_heads, pa_stream_t stream) {
     if (int rc = check_pool(pool)) return rc;
     if (int rc = check_layer(pool, layer)) return rc;
-    const pa::PoolGeom& g = pool->g;
-    if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
+        return rc;
     if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
     if (!query_starts && num_tokens != batch)
         return fail(PA_ERR_INVALID_ARG, "without query_starts num_tokens (%d) must be batch (%d)",
                     num_tokens, batch);
-    if (num_heads <= 0 || num_heads % g.Hkv != 0)
-        return fail(PA_ERR_INVALID_ARG, "num_heads %d is not a positive multiple of num_kv_heads %d",
-                    num_heads, g.Hkv);
-    if (g.D != 64 && g.D != 128)
-        return fail(PA_ERR_UNSUPPORTED, "norm and rotation are built for head_dim 64 and 128, not %d",
-                    g.D);
-    if (rope && rope->rotary_dim > g.D)
-        return fail(PA_ERR_INVALID_ARG, "rotary_dim %d is above head_dim %d", rope->rotary_dim, g.D);
-    if (!q_weight != !k_weight)
-        return fail(PA_ERR_INVALID_ARG, "q_weight and k_weight: both or neither");
-    if (q_weight && !(eps >= 0.f && std::isfinite(eps)))
-        return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0");
-    if (batch == 0 || num_tokens == 0) return PA_OK;
-    if (!q_out || !q || !k || !v || !aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) ||
-        !aligned(v, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
-        return fail(PA_ERR_INVALID_ARG,
-                    "q_out, q, k, v must be non-NULL and, as the weights, 16-byte aligned");
-    if (query_starts && !aligned(query_starts, 4))
+    if (batch > 0 && num_tokens > 0 && query_starts && !aligned(query_starts, 4))
         return fail(PA_ERR_INVALID_ARG, "query_starts must be 4-byte aligned");
-    const struct {
-        int64_t stride;
-        int heads;
-        const void* at;
-        const char* name;
-    } in[3] = {{q_stride, num_heads, q, "q"}, {k_stride, g.Hkv, k, "k"}, {v_stride, g.Hkv, v, "v"}};
-    const size_t out_bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
-    for (const auto& x : in) {
-        const int64_t row = (int64_t)x.heads * g.D;
-        if (x.stride < row || x.stride * g.elt % 16 != 0 || x.stride > (int64_t)1 << 40)
-            return fail(PA_ERR_INVALID_ARG,
-                        "%s_stride %lld: at least the row (%lld elements), a multiple of 16 bytes",
-                        x.name, (long long)x.stride, (long long)row);
-        if (x.at == q_out && x.at == q && q_stride == row) continue;  // in place
-        const size_t bytes = ((size_t)(num_tokens - 1) * x.stride + row) * g.elt;
-        if (overlap(q_out, out_bytes, x.at, bytes))
-            return fail(PA_ERR_INVALID_ARG, "q_out overlaps %s", x.name);
-    }
-    int sms = 0;
-    if (int rc = num_sms_current(&sms)) return rc;
     pa::NormRopeParams p{};
-    cudaError_t e = pa::status_word(&p.status);
-    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
-    p.q_out = q_out;
-    p.q = q, p.k = k, p.v = v;
-    p.q_stride = q_stride, p.k_stride = k_stride, p.v_stride = v_stride;
-    p.q_weight = q_weight, p.k_weight = k_weight;
-    p.eps = eps;
-    p.k_base = g.k_base, p.v_base = g.v_base;
-    p.s_blk = g.s_blk, p.tile_off = layer * g.s_layer, p.s_head = g.s_head;
-    p.num_blocks = g.num_blocks;
-    p.H = num_heads, p.Hkv = g.Hkv, p.B = g.B;
     p.bt = block_tables, p.maxb = max_blocks_per_seq;
     p.lens = context_lens, p.starts = query_starts;
     p.batch = batch, p.num_tokens = num_tokens;
-    p.amplitude = 1.f;
-    if (rope) {
-        p.rotary = rope->rotary_dim;
-        p.interleaved = rope->interleaved;
-        p.amplitude = rope->amplitude;
-        std::copy(rope->freq, rope->freq + rope->rotary_dim / 2, p.freq);
-    }
-    e = pa::launch_norm_rope(p, g.dtype, g.D, sms, reinterpret_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "pa_norm_rope_write_kv launch");
-    return PA_OK;
+    bool done;
+    if (int rc = norm_rope_params(pool, layer, q_out, q, q_stride, k, k_stride, v, v_stride, rope,
+                                  q_weight, k_weight, eps, num_heads, batch == 0 || num_tokens == 0,
+                                  &p, &done))
+        return rc;
+    return done ? PA_OK : norm_rope_launch(pool, p, "pa_norm_rope_write_kv launch", stream);
+}
+
+int pa_norm_rope_write_kv_slots(pa_pool* pool, int layer, void* q_out, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const pa_rope* rope, const void* q_weight,
+                                const void* k_weight, float eps, const int* positions,
+                                const int64_t* slots, int num_tokens, int num_heads,
+                                pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_layer(pool, layer)) return rc;
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+    if (num_tokens > 0 && (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 8)))
+        return fail(PA_ERR_INVALID_ARG,
+                    "positions (4-byte aligned) and slots (8-byte aligned) must be non-NULL");
+    pa::NormRopeParams p{};
+    p.num_tokens = num_tokens;
+    p.positions = positions, p.slots = reinterpret_cast<const long long*>(slots);
+    bool done;
+    if (int rc = norm_rope_params(pool, layer, q_out, q, q_stride, k, k_stride, v, v_stride, rope,
+                                  q_weight, k_weight, eps, num_heads, num_tokens == 0, &p, &done))
+        return rc;
+    return done ? PA_OK : norm_rope_launch(pool, p, "pa_norm_rope_write_kv_slots launch", stream);
 }
 
 int pa_pool_set_prefill_kernel(pa_pool* pool, int kind) {
@@ -1146,64 +1262,30 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
                          const int* query_starts, int batch, int num_tokens, int num_heads,
                          float scale, void* workspace, size_t workspace_bytes,
                          pa_stream_t stream) {
-    if (int rc = check_pool(pool)) return rc;
-    if (int rc = check_layer(pool, layer)) return rc;
-    const pa::PoolGeom& g = pool->g;
-    if (int rc = check_tables(block_tables, max_blocks_per_seq, g.B, context_lens, batch)) return rc;
-    if (!std::isfinite(scale * 1.4426950408889634f))
-        return fail(PA_ERR_INVALID_ARG, "scale is not finite (times log2 e)");
-    PrefillShape sh;
-    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
-        return rc;
-    if (batch == 0 || num_tokens == 0) return PA_OK;
-    if (!out || !q || !aligned(out, 16) || !aligned(q, 16))
-        return fail(PA_ERR_INVALID_ARG, "out and q must be non-NULL and 16-byte aligned");
-    if (!query_starts || !aligned(query_starts, 4))
-        return fail(PA_ERR_INVALID_ARG, "query_starts must be non-NULL and 4-byte aligned");
-    const size_t bytes = (size_t)num_tokens * num_heads * g.D * g.elt;
-    if (overlap(out, bytes, q, bytes)) return fail(PA_ERR_INVALID_ARG, "out overlaps q");
-    if (sh.ws_bytes &&
-        (!workspace || workspace_bytes < sh.ws_bytes || !aligned(workspace, 256)))
-        return fail(PA_ERR_WORKSPACE,
-                    "workspace must be 256-byte aligned and hold %zu bytes (got %p, %zu)",
-                    sh.ws_bytes, workspace, workspace_bytes);
-    pa::PrefillParams p{};
-    cudaError_t e = pa::status_word(&p.status);
-    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
-    p.out = out;
-    p.q = q;
-    p.k_base = g.k_base, p.v_base = g.v_base;
-    p.s_blk = g.s_blk, p.tile_off = layer * g.s_layer, p.s_head = g.s_head;
-    p.num_blocks = g.num_blocks;
-    p.H = num_heads, p.Hkv = g.Hkv, p.G = num_heads / g.Hkv, p.layer = layer;
-    p.bt = block_tables, p.maxb = max_blocks_per_seq;
-    p.lens = context_lens, p.starts = query_starts;
-    p.batch = batch, p.num_tokens = num_tokens;
-    p.qscale = scale * 1.4426950408889634f;  // log2(e): softmax evaluated with exp2
-    p.splits = sh.splits, p.cluster = sh.cluster;
-    p.grid = sh.grid;
-    if (sh.ws_bytes) {
-        char* ws = static_cast<char*>(workspace);
-        p.part_o = reinterpret_cast<float*>(ws);
-        p.part_ml = reinterpret_cast<float*>(ws + sh.ml_off);
-        if (sh.grid) p.cut = reinterpret_cast<int4*>(ws + sh.cut_off);
+    return attend_new(out, q, pool, layer, block_tables, max_blocks_per_seq, context_lens,
+                      query_starts, nullptr, 0, batch, num_tokens, num_heads, scale, workspace,
+                      workspace_bytes, stream);
+}
+
+int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens, int num_heads,
+                           int max_blocks_per_seq, size_t* bytes) {
+    return pa_prefill_workspace_size(pool, batch, num_tokens, num_heads, max_blocks_per_seq, bytes);
+}
+
+int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int layer,
+                      const int* block_tables, int max_blocks_per_seq, const int* context_lens,
+                      const int* query_starts, const uint32_t* tree_masks, int mask_words, int batch,
+                      int num_tokens, int num_heads, float scale, void* workspace,
+                      size_t workspace_bytes, pa_stream_t stream) {
+    if (mask_words < 1 || mask_words > pa::kMaxTreeWords)
+        return fail(PA_ERR_INVALID_ARG, "mask_words %d outside [1, %d]", mask_words, pa::kMaxTreeWords);
+    if (!tree_masks || !aligned(tree_masks, 4)) {
+        if (batch > 0 && num_tokens > 0)
+            return fail(PA_ERR_INVALID_ARG, "tree_masks must be non-NULL and 4-byte aligned");
     }
-    // division by G: with s = ceil(log2 G) and m = ceil(2^(31 + s) / G), x m
-    // >> (31 + s) is exact for x < 2^31 (m G - 2^(31 + s) < G <= 2^s)
-    p.div_shift = 31;
-    while ((1LL << (p.div_shift - 31)) < p.G) ++p.div_shift;
-    p.div_mul = (unsigned)(((1ULL << p.div_shift) + p.G - 1) / p.G);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (sh.grid) {
-        if (int rc = pool_tmaps(pool)) return rc;
-        p.slot_blk = pool->tma_slots[0];
-        p.slot_layer = pool->tma_slots[1];
-        e = pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
-    } else {
-        e = pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s);
-    }
-    if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
-    return PA_OK;
+    return attend_new(out, q, pool, layer, block_tables, max_blocks_per_seq, context_lens,
+                      query_starts, tree_masks, mask_words, batch, num_tokens, num_heads, scale,
+                      workspace, workspace_bytes, stream);
 }
 
 // --------------------------------------------------------------------- pages
@@ -1272,6 +1354,138 @@ int pa_device_free_shared(pa_pool* pool, void* dev_stack, int* shares, int* bloc
                                  finished, max_blocks_per_seq, batch, g.B, g.num_blocks, g.status};
     cudaError_t e = pa::launch_free_shared(p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "pa_device_free_shared launch");
+    return PA_OK;
+}
+
+int pa_device_plan_tokens(pa_pool* pool, void* dev_stack, int* block_tables,
+                          int max_blocks_per_seq, const int* cached_lens, const int* new_counts,
+                          const int* parents, int batch, int num_tokens, int* context_lens,
+                          int* query_starts, int64_t* slots, int* positions, uint32_t* tree_masks,
+                          int mask_words, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, cached_lens, batch))
+        return rc;
+    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+    if (tree_masks && (mask_words < 1 || mask_words > pa::kMaxTreeWords))
+        return fail(PA_ERR_INVALID_ARG, "mask_words %d outside [1, %d]", mask_words, pa::kMaxTreeWords);
+    if (!query_starts || !aligned(query_starts, 4) || !aligned(tree_masks, 4) || !aligned(parents, 4))
+        return fail(PA_ERR_INVALID_ARG,
+                    "query_starts must be non-NULL; query_starts, tree_masks, parents 4-byte aligned");
+    if (num_tokens > 0 && (!slots || !positions || !aligned(slots, 8) || !aligned(positions, 4)))
+        return fail(PA_ERR_INVALID_ARG,
+                    "slots (8-byte aligned) and positions (4-byte aligned) must be non-NULL");
+    if (batch > 0 && (!new_counts || !context_lens || !aligned(new_counts, 4) || !aligned(context_lens, 4)))
+        return fail(PA_ERR_INVALID_ARG,
+                    "new_counts and context_lens must be non-NULL and 4-byte aligned");
+    if (int rc = check_stack(dev_stack)) return rc;
+    const size_t seqs = (size_t)batch * 4, tokens = (size_t)num_tokens * 4;
+    const struct {
+        const void* at;
+        size_t bytes;
+    } in[3] = {{cached_lens, seqs}, {new_counts, seqs}, {parents, parents ? tokens : 0}},
+      out[7] = {{context_lens, seqs},
+                {query_starts, seqs + 4},
+                {slots, 2 * tokens},
+                {positions, tokens},
+                {tree_masks, tree_masks ? tokens * mask_words : 0},
+                {dev_stack, ((size_t)pool->g.num_blocks + 1) * 4},
+                {block_tables, seqs * max_blocks_per_seq}};
+    for (int o = 0; o < 7; ++o) {
+        for (const auto& x : in)
+            if (overlap(out[o].at, out[o].bytes, x.at, x.bytes))
+                return fail(PA_ERR_INVALID_ARG, "an output overlaps an input");
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o].at, out[o].bytes, out[i].at, out[i].bytes))
+                return fail(PA_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    pa::PlanParams p{};
+    cudaError_t e = pa::status_word(&p.status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    p.stack = static_cast<int*>(dev_stack), p.bt = block_tables;
+    p.maxb = max_blocks_per_seq, p.batch = batch, p.num_tokens = num_tokens;
+    p.B = pool->g.B, p.num_blocks = pool->g.num_blocks;
+    p.cached = cached_lens, p.counts = new_counts, p.parents = parents;
+    p.lens = context_lens, p.starts = query_starts, p.positions = positions;
+    p.slots = reinterpret_cast<long long*>(slots);
+    p.masks = tree_masks, p.words = mask_words;
+    e = pa::launch_plan(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_device_plan_tokens launch");
+    return PA_OK;
+}
+
+int pa_device_trim_sequences(pa_pool* pool, void* dev_stack, int* block_tables,
+                             int max_blocks_per_seq, const int* context_lens, const int* new_lens,
+                             int batch, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
+        return rc;
+    if (batch == 0) return PA_OK;
+    if (int rc = check_stack(dev_stack)) return rc;
+    if (!new_lens || !aligned(new_lens, 4))
+        return fail(PA_ERR_INVALID_ARG, "new_lens must be non-NULL and 4-byte aligned");
+    pa::TrimParams p{};
+    cudaError_t e = pa::status_word(&p.status);
+    if (e != cudaSuccess) return cuda_fail(e, "status word lookup");
+    p.stack = static_cast<int*>(dev_stack), p.bt = block_tables;
+    p.maxb = max_blocks_per_seq, p.batch = batch;
+    p.B = pool->g.B, p.num_blocks = pool->g.num_blocks;
+    p.lens = context_lens, p.new_lens = new_lens;
+    e = pa::launch_trim(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_device_trim_sequences launch");
+    return PA_OK;
+}
+
+int pa_device_accept_tree(pa_pool* pool, const int64_t* slots, const int* parents,
+                          const int* tokens, const int* targets, const int* context_lens,
+                          const int* query_starts, int batch, int num_tokens, int max_path,
+                          int* accepted_counts, int* accepted_nodes, int* next_tokens,
+                          int* next_lens, pa_stream_t stream) {
+    if (int rc = check_pool(pool)) return rc;
+    if (batch < 0 || num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "batch (%d) and num_tokens (%d) must be >= 0", batch,
+                    num_tokens);
+    if (max_path < 1 || max_path > pa::kMaxTreeNodes)
+        return fail(PA_ERR_INVALID_ARG, "max_path %d outside [1, %d]", max_path, pa::kMaxTreeNodes);
+    if (batch == 0) return PA_OK;
+    if (num_tokens > 0 && (!slots || !parents || !tokens || !targets || !aligned(slots, 8) ||
+                           !aligned(parents, 4) || !aligned(tokens, 4) || !aligned(targets, 4)))
+        return fail(PA_ERR_INVALID_ARG,
+                    "slots (8-byte aligned), parents, tokens and targets (4-byte aligned) must be non-NULL");
+    if (!context_lens || !query_starts || !aligned(context_lens, 4) || !aligned(query_starts, 4))
+        return fail(PA_ERR_INVALID_ARG,
+                    "context_lens and query_starts must be non-NULL and 4-byte aligned");
+    if (!accepted_counts || !accepted_nodes || !next_tokens || !next_lens ||
+        !aligned(accepted_counts, 4) || !aligned(accepted_nodes, 4) || !aligned(next_tokens, 4) ||
+        !aligned(next_lens, 4))
+        return fail(PA_ERR_INVALID_ARG, "the outputs must be non-NULL and 4-byte aligned");
+    const size_t seqs = (size_t)batch * 4, rows = (size_t)num_tokens * 4;
+    const struct {
+        const void* at;
+        size_t bytes;
+    } in[6] = {{slots, 2 * rows}, {parents, rows}, {tokens, rows}, {targets, rows},
+               {context_lens, seqs}, {query_starts, seqs + 4}},
+      out[4] = {{accepted_counts, seqs}, {accepted_nodes, seqs * max_path}, {next_tokens, seqs},
+                {next_lens, seqs}};
+    for (int o = 0; o < 4; ++o) {
+        for (const auto& x : in)
+            if (overlap(out[o].at, out[o].bytes, x.at, x.bytes))
+                return fail(PA_ERR_INVALID_ARG, "an output overlaps an input");
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o].at, out[o].bytes, out[i].at, out[i].bytes))
+                return fail(PA_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    int sms = 0;
+    if (int rc = num_sms_current(&sms)) return rc;
+    pa::AcceptParams p{};
+    if (int rc = page_geom(pool, &p.g)) return rc;
+    p.slots = reinterpret_cast<const long long*>(slots);
+    p.parents = parents, p.tokens = tokens, p.targets = targets;
+    p.lens = context_lens, p.starts = query_starts;
+    p.batch = batch, p.num_tokens = num_tokens, p.max_path = max_path;
+    p.counts = accepted_counts, p.nodes = accepted_nodes;
+    p.next_tokens = next_tokens, p.next_lens = next_lens;
+    const cudaError_t e = pa::launch_accept(p, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_device_accept_tree launch");
     return PA_OK;
 }
 

@@ -121,13 +121,15 @@ struct NormRopeParams {
     const int* lens;
     const int* starts;       // [batch + 1], or null: token t is sequence t
     int batch, num_tokens, splits;
+    const int* positions;    // with slots, in place of the tables, lengths and starts
+    const long long* slots;  // [num_tokens] page * B + row, negative: no token
     int rotary, interleaved;
     unsigned* status;
     unsigned long long freq[kMaxRotaryPairs];  // turns per position, as fractions of 2^64
 };
 
 // Attention of several new tokens per sequence (see pa_prefill_umma.cuh for long
-// calls on bf16 pools, pa_prefill_mma.cu for short ones and for fp32).
+// calls on bf16 pools, pa_prefill_mma.cuh for short ones and for fp32).
 struct PrefillParams {
     void* out;               // [num_tokens, H, D], pool dtype
     const void* q;           // [num_tokens, H, D], pool dtype
@@ -149,6 +151,29 @@ struct PrefillParams {
     int slot_blk, slot_layer;  // tensor-map dimensions of the pool's axes
     unsigned div_mul;        // x / G = x * div_mul >> div_shift for x < 2^31
     int div_shift;
+    const unsigned* masks;   // trees: [num_tokens, words], see pa_tree_mask.cuh
+    int words;
+};
+
+// New tokens: pages, slots, positions and masks; and pages given back (see pa_plan.cu).
+struct PlanParams {
+    int *stack, *bt;
+    int maxb, batch, num_tokens, B;
+    long long num_blocks;
+    const int *cached, *counts;
+    const int* parents;      // [num_tokens] or null
+    int *lens, *starts, *positions;
+    long long* slots;
+    unsigned* masks;         // [num_tokens, words] or null
+    int words;
+    unsigned* status;
+};
+struct TrimParams {
+    int *stack, *bt;
+    int maxb, batch, B;
+    long long num_blocks;
+    const int *lens, *new_lens;
+    unsigned* status;
 };
 
 // The pages of a pool (see pa_pages.cu).
@@ -174,6 +199,15 @@ struct FreeSharedParams {
     long long num_blocks;
     unsigned* status;
 };
+// Drafted trees decided, their rows moved (see pa_accept.cu).
+constexpr int kMaxTreeWords = 32, kMaxTreeNodes = 32 * kMaxTreeWords;
+struct AcceptParams {
+    PageGeom g;
+    const long long* slots;
+    const int *parents, *tokens, *targets, *lens, *starts;
+    int batch, num_tokens, max_path, parts;
+    int *counts, *nodes, *next_tokens, *next_lens;
+};
 struct CompactParams {
     PageGeom g;
     const int *stack, *shares, *bt, *lens;
@@ -196,6 +230,14 @@ cudaError_t launch_prefill_mma(const PrefillParams& p, int dtype, int D, int B, 
 int prefill_umma_grid(int G, int Hkv, int batch, int num_tokens, int maxb, int B, int num_sms);
 cudaError_t launch_prefill_umma(const PrefillParams& p, const void* tmaps, int D, int B,
                                 cudaStream_t s);
+
+// The same kernels with a mask for each token.
+cudaError_t launch_tree_mma(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s);
+cudaError_t launch_tree_umma(const PrefillParams& p, const void* tmaps, int D, int B, cudaStream_t s);
+
+cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);
+cudaError_t launch_trim(const TrimParams& p, cudaStream_t s);
+cudaError_t launch_accept(const AcceptParams& p, int num_sms, cudaStream_t s);
 
 cudaError_t launch_copy_blocks(const PageGeom& g, const int* src, const int* dst, int n,
                                int num_sms, cudaStream_t s);

@@ -18,6 +18,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_stack.cuh"
 
 namespace pa {
 
@@ -50,43 +51,6 @@ __device__ __forceinline__ void warp_copy_tile(const PageGeom& g, int i, int src
         b[c] = v0, b[c + 32] = v1, b[c + 64] = v2, b[c + 96] = v3;
     }
     for (; c < chunks; c += 32) b[c] = ld_dep(a + c);
-}
-
-// The stack's height, held to what the array can hold (flagged if it was not).
-__device__ __forceinline__ int stack_height(const int* stack, long long num_blocks,
-                                            unsigned* status) {
-    const int h = ld_dep(stack);
-    if (h >= 0 && h <= num_blocks) return h;
-    if (threadIdx.x == 0) atomicOr(status, kStatusBadLength);
-    return h < 0 ? 0 : (int)num_blocks;
-}
-
-// Exclusive prefix sum of `v` over the CTA; `total` receives the sum.
-__device__ __forceinline__ int cta_exclusive_scan(int v, int* s_warp, int& total) {
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(kFullMask, incl, o);
-        if (lane >= o) incl += t;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-        int w = lane < (blockDim.x >> 5) ? s_warp[lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(kFullMask, w, o);
-            if (lane >= o) w += t;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    const int before = warp > 0 ? s_warp[warp - 1] : 0;
-    total = s_warp[(blockDim.x >> 5) - 1];
-    __syncthreads();
-    return before + incl - v;
 }
 
 // ------------------------------------------------------------------- copies

@@ -2,7 +2,9 @@
 // bf16 paged cache on the 5th-generation tensor cores: the calls that are not short.
 //
 //   out_t = sum_{s <= p_t} softmax_s(scale q_t . k_s) v_s,
-//   p_t = context_lens[b] - n_b + i for the i-th of sequence b's n_b new tokens.
+//   p_t = context_lens[b] - n_b + i for the i-th of sequence b's n_b new tokens;
+// TREE: over the s < context_lens[b] - n_b and the new tokens whose bits are set in the
+// token's mask.
 //
 // The query heads of a KV head's group share its keys, so the rows of a tile
 // are (token, head of the group) in that order, flattened: row r is token r / G,
@@ -55,7 +57,7 @@
 // Many keys, few rows: bytes; 3 - 5 tokens over 4 contexts of 32,768 to 131,000: 150
 // us, 6.3 TB/s (94 % of a plain copy's rate; 167 us without turns), in shares cut to
 // the tile.  Short calls:
-// latency (pa_prefill_mma.cu takes the shortest); one token over 100 keys takes 8.7 us,
+// latency (pa_prefill_mma.cuh takes the shortest); one token over 100 keys takes 8.7 us,
 // of which 2.5 go to the schedule (its code is fetched by every SM), 2.5 to the first
 // K tile and its scores, and 2.5 to the join's launch; 8 chunks of up to 513 tokens
 // with 16 heads on 2 of 64: 25 us, of which 9 are five to seven tiles.
@@ -76,6 +78,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
+#include "pa_tree_mask.cuh"
 
 namespace pa {
 
@@ -119,7 +122,7 @@ struct PfSeq {
     int start, n_new, n, first_pos, rows, tiles;
 };
 
-template <int B>
+template <int B, bool TREE>
 __device__ __forceinline__ PfSeq pf_sequence(const PrefillParams& p, int b, bool* bad) {
     PfSeq s{0, 0, 0, 0, 0, 0};
     *bad = false;
@@ -131,7 +134,7 @@ __device__ __forceinline__ PfSeq pf_sequence(const PrefillParams& p, int b, bool
         return s;
     }
     s.start = s0, s.n_new = s1 - s0, s.n = n;
-    if (n < s.n_new || n > p.maxb * B || n < 0) {
+    if (n < s.n_new || n > p.maxb * B || n < 0 || (TREE && s.n_new > 32 * p.words)) {
         *bad = true;
         s.n = 0;  // no key is seen: zero rows
     }
@@ -159,14 +162,15 @@ __device__ __forceinline__ int pf_div(const PrefillParams& p, int x) {
 }
 
 // Key tiles of pair i of a sequence (at least one: the pair owes its output).
+template <bool TREE>
 __device__ __forceinline__ int pf_key_tiles(const PrefillParams& p, const PfSeq& s, int i) {
     const int last = min(s.rows, 256 * (i + 1)) - 1;
-    const int see = s.first_pos + pf_div(p, last) + 1;
+    const int see = TREE ? s.n : s.first_pos + pf_div(p, last) + 1;
     return see > 128 ? (see + 127) >> 7 : 1;
 }
 
 // a / b, in 32 bits where both fit; out of line (see pf_wait_call).
-__device__ __noinline__ long long pf_div64(long long a, long long b) {
+static __device__ __noinline__ long long pf_div64(long long a, long long b) {
     if ((unsigned long long)(a | b) >> 32) return a / b;
     return (unsigned)a / (unsigned)b;
 }
@@ -191,11 +195,11 @@ struct PfWalk {
 };
 
 // Units of sequence b0 + lane (all lanes of the warp take part).
-template <int B>
+template <int B, bool TREE>
 __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b, int lane,
                                                   bool report, PfSeq& s) {
     bool bad;
-    s = pf_sequence<B>(p, b, &bad);
+    s = pf_sequence<B, TREE>(p, b, &bad);
     if (bad && report) atomicOr(p.status, kStatusBadLength);
     long long u = 0;
     // (a sequence taken by the whole warp costs what about 32 pairs cost one lane)
@@ -203,7 +207,7 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
     if (s.tiles <= lim) {
         int v = s.tiles * kPairUnits;
 #pragma unroll 1
-        for (int i = 0; i < s.tiles; ++i) v += pf_key_tiles(p, s, i);
+        for (int i = 0; i < s.tiles; ++i) v += pf_key_tiles<TREE>(p, s, i);
         u = v;
     }
     unsigned big = __ballot_sync(kFullMask, s.tiles > lim);
@@ -211,12 +215,13 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
         const int f = __ffs(big) - 1;
         big &= big - 1;
         PfSeq o;
+        o.n = __shfl_sync(kFullMask, s.n, f);
         o.first_pos = __shfl_sync(kFullMask, s.first_pos, f);
         o.rows = __shfl_sync(kFullMask, s.rows, f);
         o.tiles = __shfl_sync(kFullMask, s.tiles, f);
         long long v = 0;
 #pragma unroll 1
-        for (int i = lane; i < o.tiles; i += 32) v += kPairUnits + pf_key_tiles(p, o, i);
+        for (int i = lane; i < o.tiles; i += 32) v += kPairUnits + pf_key_tiles<TREE>(p, o, i);
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(kFullMask, v, x);
         if (lane == f) u = v;
@@ -228,7 +233,7 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
 // units, [24] offset within the pair, [32] b, [36] KV head, [40] pair, [48] the
 // sequence, all for warp 0.  Up to 32 sequences are that warp's, without barriers in
 // between.
-template <typename C>
+template <typename C, bool TREE>
 __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned char* ctrl) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nw = p.batch <= 32 ? 1 : C::THREADS / 32;  // warps that take part
@@ -240,7 +245,7 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
     PfSeq s{0, 0, 0, 0, 0, 0};
 #pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += nw * 32) {
-        u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, blockIdx.x == 0, s);
+        u = pf_seq_units<C::B, TREE>(p, b0 + threadIdx.x, lane, blockIdx.x == 0, s);
         mine += u;
     }
 #pragma unroll
@@ -266,7 +271,7 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
     long long before = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < p.batch; b0 += nw * 32) {
-        if (p.batch > nw * 32) u = pf_seq_units<C::B>(p, b0 + threadIdx.x, lane, false, s);
+        if (p.batch > nw * 32) u = pf_seq_units<C::B, TREE>(p, b0 + threadIdx.x, lane, false, s);
         long long incl = u * p.Hkv;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -304,7 +309,7 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
         int i = 0;
 #pragma unroll 1
         for (int i0 = 0; i0 < s.tiles; i0 += 32) {
-            const int c = i0 + lane < s.tiles ? kPairUnits + pf_key_tiles(p, s, i0 + lane) : 0;
+            const int c = i0 + lane < s.tiles ? kPairUnits + pf_key_tiles<TREE>(p, s, i0 + lane) : 0;
             long long incl = c;
 #pragma unroll
             for (int x = 1; x < 32; x <<= 1) {
@@ -341,11 +346,11 @@ __device__ __forceinline__ void pf_walk_begin(const PrefillParams& p, const unsi
 
 // The next piece with work; kvt: the pair's key tiles, gpos: the global unit of
 // its first one.
-template <typename C>
+template <typename C, bool TREE>
 __device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, PfPiece& pc,
                                              int& kvt, long long& gpos) {
     while (w.left > 0) {
-        kvt = pf_key_tiles(p, w.s, w.i);
+        kvt = pf_key_tiles<TREE>(p, w.s, w.i);
         const long long c = kPairUnits + kvt;
         const long long take = min(c - w.off, w.left);
         const int u0 = (int)max(w.off - kPairUnits, 0LL), u1 = (int)(w.off + take - kPairUnits);
@@ -354,7 +359,8 @@ __device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, 
         pc.row0 = 256 * w.i, pc.rows = w.s.rows, pc.start = w.s.start;
         pc.nj = pc.rows - pc.row0 > 128 ? 2 : 1;
         pc.first_pos = w.s.first_pos, pc.n = w.s.n, pc.b = w.b;
-        pc.pair_pos = pc.first_pos + pf_div(p, pc.row0);
+        // (TREE: the last position that all rows see)
+        pc.pair_pos = TREE ? pc.first_pos - 1 : pc.first_pos + pf_div(p, pc.row0);
         pc.flags = (u0 == 0 && u1 == kvt ? 1 : 0) | (w.count == 0 ? 2 : 0);
         w.left -= take;
         if (w.off + take == c) {  // on to the next pair
@@ -365,7 +371,7 @@ __device__ __forceinline__ bool pf_walk_next(const PrefillParams& p, PfWalk& w, 
                     w.kvh = 0;
                     while (w.left > 0 && ++w.b < p.batch) {
                         bool bad;
-                        w.s = pf_sequence<C::B>(p, w.b, &bad);
+                        w.s = pf_sequence<C::B, TREE>(p, w.b, &bad);
                         if (w.s.tiles > 0) break;
                     }
                     if (w.b >= p.batch) w.left = 0;
@@ -451,7 +457,7 @@ __device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, volatile 
     atomicOr(status, kStatusTimeout);
     return false;
 }
-__device__ __noinline__ bool pf_wait_call(uint32_t bar, uint32_t parity, volatile int* abort_all,
+static __device__ __noinline__ bool pf_wait_call(uint32_t bar, uint32_t parity, volatile int* abort_all,
                                           unsigned* status) {
     return pf_wait(bar, parity, abort_all, status);
 }
@@ -559,7 +565,7 @@ __device__ __forceinline__ float poison(const int* marks, int D, int d, int pos)
     return n || (a && b) ? NAN : a ? INFINITY : b ? -INFINITY : 0.f;
 }
 
-template <int D, int B, bool TURNS>
+template <int D, int B, bool TURNS, bool TREE>
 __global__ void __launch_bounds__(384, 1)
     pa_prefill_umma_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv,
@@ -607,7 +613,7 @@ __global__ void __launch_bounds__(384, 1)
     pdl_wait();
     // (the K producer alone needs the schedule: with few sequences the other warps are
     // at their first wait, their code fetched, when it hands out the first piece)
-    pf_schedule<C>(p, ctrl);
+    pf_schedule<C, TREE>(p, ctrl);
     auto wait = [&](int bar, uint32_t parity) {
         return pf_wait(bar0 + 8 * bar, parity, abort_all, p.status);
     };
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (kv == 0) {
                     int kvt;
                     long long gpos;
-                    const bool more = pf_walk_next<C>(p, w, pc, kvt, gpos);
+                    const bool more = pf_walk_next<C, TREE>(p, w, pc, kvt, gpos);
                     const int slot = np % C::NP;
                     if (np >= C::NP &&
                         !__all_sync(kFullMask, wait(C::PC_EMPTY + slot, (np / C::NP - 1) & 1)))
@@ -918,7 +924,8 @@ __global__ void __launch_bounds__(384, 1)
                 // for two tiles ahead: it takes 2000 cycles and more beside the softmax, and
                 // asked for one ahead the last product waited 2000 - 4400 for it.)
                 ++piece;
-                const int last = pc.first_pos + pf_div(p, min(pc.rows, pc.row0 + 256) - 1);
+                const int last =
+                    TREE ? pc.n - 1 : pc.first_pos + pf_div(p, min(pc.rows, pc.row0 + 256) - 1);
 #pragma unroll 1
                 for (int kt = pc.kt0; kt < pc.kt1 && ok; ++kt, vseq += 2) {
                     if (!pf_unclean(pc, kt)) continue;
@@ -970,7 +977,7 @@ __global__ void __launch_bounds__(384, 1)
                                             n < (1 << 24); ++n)
                                 __nanosleep(100);
 #pragma unroll 1
-                            for (int k = lane; k < 3 * D; k += 32) marks[k] = INT_MAX;
+                            for (int k = lane; k < 3 * D && !TREE; k += 32) marks[k] = INT_MAX;
                             mark_at = piece;
                             if (lane == 0) *mark_piece = piece;
                             __syncwarp();
@@ -986,7 +993,8 @@ __global__ void __launch_bounds__(384, 1)
                                 const float v = __bfloat162float(*at);
                                 if (isfinite(v)) continue;
                                 const int d = (x & ~63) + ((((x >> 3) & 7) ^ (r & 7)) << 3) + (x & 7);
-                                atomicMin(marks + (v != v ? 0 : v > 0.f ? D : 2 * D) + d, t0 + r);
+                                // (TREE: which rows see it is looked up at the output)
+                                if (!TREE) atomicMin(marks + (v != v ? 0 : v > 0.f ? D : 2 * D) + d, t0 + r);
                                 *at = __float2bfloat16(0.f);
                             }
                         }
@@ -1035,7 +1043,9 @@ __global__ void __launch_bounds__(384, 1)
             const int i0 = turns ? j : 0, step = turns ? 2 : 1;
             const bool live = f < pc.rows;
             const int tok = pf_div(p, f);
-            const int pos = live ? pc.first_pos + tok : -1;
+            // the last of the keys that the row sees all of, and TREE: its token's mask
+            const int pos = live ? (TREE ? pc.first_pos - 1 : pc.first_pos + tok) : -1;
+            const unsigned* mask = TREE ? p.masks + (live ? (long long)(pc.start + tok) * p.words : 0) : nullptr;
             float m = -FLT_MAX;   // reference point of the exponentials (scaled, base 2)
             float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -1082,7 +1092,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int e = lim - 32 * c;  // the last of the word's keys the row sees
-                    vis[c] = (e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u) &
+                    const uint32_t seen =
+                        TREE && live && e < 31 ? tree_bits(mask, p.words, 32 * c + t0 - pc.first_pos, pc.n - pc.first_pos)
+                                               : e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u;
+                    vis[c] = seen &
                              (((bits >> (2 * c)) & 1u ? 0xffffu : 0u) |
                               ((bits >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
                 }
@@ -1187,7 +1200,21 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
             }
-            if (live && *mark_piece == piece) {
+            if (TREE && live && *mark_piece == piece) {
+                // values that are not finite, into the rows that see them
+                const __nv_bfloat16* vb =
+                    static_cast<const __nv_bfloat16*>(p.v_base) + p.tile_off + (long long)pc.kvh * p.s_head;
+                tree_odd_values<__nv_bfloat16, D>(
+                    p, vb, pc.b, mask, pc.first_pos, pc.n - pc.first_pos, B, pc.kt0 * C::TT, pc.kt1 * C::TT, col0, 1,
+                    turns ? col0 + D / 2 : D, [&](int d, float v) {
+                        if (pc.whole()) {
+                            __nv_bfloat16& x = static_cast<__nv_bfloat16*>(p.out)[orow * D + d];
+                            x = __float2bfloat16(__bfloat162float(x) + v);
+                        } else {
+                            p.part_o[pf_part_at(part, D, d)] += v;
+                        }
+                    });
+            } else if (live && *mark_piece == piece) {
                 // values that are not finite, into the rows that see them
 #pragma unroll 1
                 for (int d = col0; d < (turns ? col0 + D / 2 : D); ++d) {
@@ -1230,7 +1257,7 @@ struct PfJoin {
         for (int k = 0; k < 8; ++k) o[k] = fmaf(o[k], keep, w * x[k]);
     }
 };
-template <int D>
+template <int D, bool TREE>  // (TREE: a name of its own in either unit)
 __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();

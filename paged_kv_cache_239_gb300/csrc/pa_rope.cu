@@ -3,7 +3,8 @@
 // one pass over the projections' output.
 //
 // Token t of sequence b (n_b new ones, this the i-th) stands at position
-// p = context_lens[b] - n_b + i.  For a query or key head x of D elements
+// p = context_lens[b] - n_b + i, in the slot of that position; SLOTS: at p = positions[t], in
+// slots[t] (a drafted tree's tokens: their depth tells the position).  For a query or key head x of D elements
 //   y_d = x_d * rsqrt(mean(x^2) + eps) * w_d                  (w given; else y = x)
 //   (y_a, y_b) -> A (y_a cos(p f_j) - y_b sin(p f_j), y_a sin(p f_j) + y_b cos(p f_j))
 // for the pairs j < r/2 of the first r elements: (a, b) = (2j, 2j + 1) when
@@ -94,7 +95,7 @@ __device__ __forceinline__ int find_sequence(const int* starts, int batch, int t
     return n;
 }
 
-template <typename T, int D, bool INTERLEAVED>
+template <typename T, int D, bool INTERLEAVED, bool SLOTS>
 __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
     pdl_trigger();
     pdl_wait();
@@ -137,24 +138,40 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
     for (int u = 0; u < U; ++u) load(split * RPW + sub + u * step, raw[u]);
 
     // ---- where the token stands ----
-    int b = t, s0 = t, n_new = 1;
-    if (p.starts != nullptr) {
-        b = find_sequence(p.starts, p.batch, t, lane);
-        if (b >= p.batch) return;    // behind the last sequence: left as it is
-        s0 = ld_dep(p.starts + b);
-        n_new = ld_dep(p.starts + b + 1) - s0;
+    bool good;
+    int pos, blk;
+    long long slot;
+    if constexpr (SLOTS) {
+        const long long at = ld_dep(p.slots + t);
+        pos = ld_dep(p.positions + t);
+        if (at < 0) return;          // no token: left as it is
+        good = pos >= 0;
+        if (!good && split == 0 && lane == 0) atomicOr(p.status, kStatusBadLength);
+        const long long page = at / p.B;
+        const bool there = page < p.num_blocks;
+        if (!there && split == 0 && lane == 0) atomicOr(p.status, kStatusBadBlock);
+        blk = good && there ? (int)page : -1;
+        slot = (long long)blk * p.s_blk + p.tile_off + (at - page * p.B) * D;
+    } else {
+        int b = t, s0 = t, n_new = 1;
+        if (p.starts != nullptr) {
+            b = find_sequence(p.starts, p.batch, t, lane);
+            if (b >= p.batch) return;    // behind the last sequence: left as it is
+            s0 = ld_dep(p.starts + b);
+            n_new = ld_dep(p.starts + b + 1) - s0;
+        }
+        const int n = ld_dep(p.lens + b);
+        const int i = t - s0;
+        good = n >= 0 && n <= p.maxb * p.B && i >= 0 && i < n_new && n_new <= n;
+        if (!good && split == 0 && lane == 0) atomicOr(p.status, kStatusBadLength);
+        pos = good ? n - n_new + i : 0;
+        blk = good ? ld_dep(p.bt + (long long)b * p.maxb + pos / p.B) : -1;
+        if (good && (blk < 0 || blk >= p.num_blocks)) {
+            if (split == 0 && lane == 0) atomicOr(p.status, kStatusBadBlock);
+            blk = -1;
+        }
+        slot = (long long)blk * p.s_blk + p.tile_off + (long long)(pos % p.B) * D;
     }
-    const int n = ld_dep(p.lens + b);
-    const int i = t - s0;
-    const bool good = n >= 0 && n <= p.maxb * p.B && i >= 0 && i < n_new && n_new <= n;
-    if (!good && split == 0 && lane == 0) atomicOr(p.status, kStatusBadLength);
-    const int pos = good ? n - n_new + i : 0;
-    int blk = good ? ld_dep(p.bt + (long long)b * p.maxb + pos / p.B) : -1;
-    if (good && (blk < 0 || blk >= p.num_blocks)) {
-        if (split == 0 && lane == 0) atomicOr(p.status, kStatusBadBlock);
-        blk = -1;
-    }
-    const long long slot = (long long)blk * p.s_blk + p.tile_off + (long long)(pos % p.B) * D;
     const bool norm = p.q_weight != nullptr;
     uint4 wq[2], wk[2];
     wq[0] = wq[1] = wk[0] = wk[1] = make_uint4(0, 0, 0, 0);
@@ -254,9 +271,11 @@ __global__ void __launch_bounds__(kRopeThreads) pa_norm_rope_kernel(const __grid
 
 template <typename T, int D>
 cudaError_t launch_d(const NormRopeParams& p, int grid, cudaStream_t s) {
-    return p.interleaved
-               ? launch_pdl(pa_norm_rope_kernel<T, D, true>, dim3(grid), dim3(kRopeThreads), 0, s, p)
-               : launch_pdl(pa_norm_rope_kernel<T, D, false>, dim3(grid), dim3(kRopeThreads), 0, s, p);
+    auto kern = p.slots != nullptr ? (p.interleaved ? pa_norm_rope_kernel<T, D, true, true>
+                                                    : pa_norm_rope_kernel<T, D, false, true>)
+                                   : (p.interleaved ? pa_norm_rope_kernel<T, D, true, false>
+                                                    : pa_norm_rope_kernel<T, D, false, false>);
+    return launch_pdl(kern, dim3(grid), dim3(kRopeThreads), 0, s, p);
 }
 
 }  // namespace

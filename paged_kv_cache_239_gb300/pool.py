@@ -166,25 +166,39 @@ class BlockPool:
         tokens; query_starts [batch + 1] says which rows are whose (None: one
         token per sequence).  ``out`` may be q itself when q is contiguous."""
         tokens, num_heads = q.shape[0], q.shape[1]
-        q_stride = self._check_rows(q, tokens, num_heads, "q")
-        k_stride = self._check_rows(k, tokens, self.num_kv_heads, "k")
-        v_stride = self._check_rows(v, tokens, self.num_kv_heads, "v")
-        if q_weight is not None:
-            self._check_dense(q_weight, (self.head_dim,), self.dtype, "q_weight")
-        if k_weight is not None:
-            self._check_dense(k_weight, (self.head_dim,), self.dtype, "k_weight")
+        strides = self._check_new_rows(q, k, v, q_weight, k_weight, rope)
         batch, maxb = self._check_batch(block_tables, context_lens, query_starts)
         if out is None:
             out = self._empty(q.shape, self.dtype, stream)
         else:
             self._check_dense(out, (tokens, num_heads, self.head_dim), self.dtype, "out")
-        if rope is not None and rope.handle is None:  # (NULL would mean no rotation)
-            raise ValueError("the Rope is closed")
         self._check_current()
-        B.pa_norm_rope_write_kv(self.handle, layer, out, q, q_stride, k, k_stride, v, v_stride,
+        B.pa_norm_rope_write_kv(self.handle, layer, out, q, strides[0], k, strides[1], v, strides[2],
                                 None if rope is None else rope.handle, q_weight, k_weight, eps,
                                 block_tables, maxb, context_lens, query_starts, batch, tokens,
                                 num_heads, stream)
+        return out
+
+    def norm_rope_write_kv_slots(self, layer: int, q: torch.Tensor, k: torch.Tensor,
+                                 v: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                                 rope=None, q_weight: Optional[torch.Tensor] = None,
+                                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """norm_rope_write_kv with a position (int32) and a slot (int64, page *
+        block_size + row) for each token, as ``device_plan_tokens`` writes them.  Rows
+        with a negative slot are no tokens: neither ``out`` nor the cache is written."""
+        tokens, num_heads = q.shape[0], q.shape[1]
+        strides = self._check_new_rows(q, k, v, q_weight, k_weight, rope)
+        self._check_dense(positions, (tokens,), torch.int32, "positions")
+        self._check_dense(slots, (tokens,), torch.int64, "slots")
+        if out is None:
+            out = self._empty(q.shape, self.dtype, stream)
+        else:
+            self._check_dense(out, (tokens, num_heads, self.head_dim), self.dtype, "out")
+        self._check_current()
+        B.pa_norm_rope_write_kv_slots(self.handle, layer, out, q, strides[0], k, strides[1], v,
+                                      strides[2], None if rope is None else rope.handle, q_weight,
+                                      k_weight, eps, positions, slots, tokens, num_heads, stream)
         return out
 
     def set_prefill_kernel(self, kind: str) -> None:
@@ -222,6 +236,120 @@ class BlockPool:
                                query_starts, batch, tokens, num_heads, scale, workspace, wbytes,
                                stream)
         return out
+
+    def tree_workspace_size(self, batch: int, num_tokens: int, num_heads: int,
+                            max_blocks_per_seq: int) -> int:
+        return B.pa_tree_workspace_size(self.handle, batch, num_tokens, num_heads,
+                                        max_blocks_per_seq)
+
+    def tree_attention(self, q: torch.Tensor, layer: int, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, query_starts: torch.Tensor,
+                       tree_masks: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """prefill_attention of drafted trees: a new token sees what is cached before its
+        sequence's new tokens and those of them whose bits are set in its row of
+        tree_masks (int32 [tokens, words], as ``device_plan_tokens`` writes them)."""
+        tokens, num_heads = q.shape[0], q.shape[1]
+        shape = (tokens, num_heads, self.head_dim)
+        self._check_dense(q, shape, self.dtype, "q")
+        batch, maxb = self._check_batch(block_tables, context_lens, query_starts)
+        words = tree_masks.shape[-1]
+        self._check_dense(tree_masks, (tokens, words), torch.int32, "tree_masks")
+        if out is None:
+            out = self._empty(shape, self.dtype, stream)
+        else:
+            self._check_dense(out, shape, self.dtype, "out")
+        self._check_current()
+        if workspace is None:  # (the call checks one that is given)
+            need = self.tree_workspace_size(batch, tokens, num_heads, maxb)
+            if need:
+                workspace = self._empty((need,), torch.uint8, stream)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        B.pa_tree_attention(out, q, self.handle, layer, block_tables, maxb, context_lens,
+                            query_starts, tree_masks, words, batch, tokens, num_heads, scale,
+                            workspace, wbytes, stream)
+        return out
+
+    # -- new tokens planned, drafted trees decided --------------------------
+    def device_plan_tokens(self, stack: torch.Tensor, block_tables: torch.Tensor,
+                           cached_lens: torch.Tensor, new_counts: torch.Tensor, num_tokens: int,
+                           parents: Optional[torch.Tensor] = None, mask_words: int = 0,
+                           context_lens: Optional[torch.Tensor] = None,
+                           query_starts: Optional[torch.Tensor] = None,
+                           slots: Optional[torch.Tensor] = None,
+                           positions: Optional[torch.Tensor] = None,
+                           tree_masks: Optional[torch.Tensor] = None, stream=None):
+        """Gives new_counts[b] tokens to every sequence of cached_lens[b]: pages from
+        the device stack into its table row, and for each of the batch's num_tokens
+        rows its slot and position (-1 and 0 behind the last sequence).  ``parents``
+        (int32 [num_tokens], an index within the sequence's new tokens, -1: a
+        root) makes them trees; with ``mask_words`` (or ``tree_masks``) each row's
+        ancestors are written as bits.  Returns (context_lens, query_starts, slots,
+        positions, tree_masks); those that are given are written in place."""
+        batch, maxb = self._check_batch(block_tables, cached_lens)
+        self._check_pages(stack, None)
+        self._check_dense(new_counts, (batch,), torch.int32, "new_counts")
+        if parents is not None:
+            self._check_dense(parents, (num_tokens,), torch.int32, "parents")
+        if tree_masks is not None:
+            mask_words = mask_words or tree_masks.shape[-1]
+        new = lambda t, shape, dtype, name: (  # noqa: E731
+            self._empty(shape, dtype, stream) if t is None
+            else (self._check_dense(t, shape, dtype, name), t)[1])
+        context_lens = new(context_lens, (batch,), torch.int32, "context_lens")
+        query_starts = new(query_starts, (batch + 1,), torch.int32, "query_starts")
+        slots = new(slots, (num_tokens,), torch.int64, "slots")
+        positions = new(positions, (num_tokens,), torch.int32, "positions")
+        if mask_words:
+            tree_masks = new(tree_masks, (num_tokens, mask_words), torch.int32, "tree_masks")
+        self._check_current()
+        B.pa_device_plan_tokens(self.handle, stack, block_tables, maxb, cached_lens, new_counts,
+                                parents, batch, num_tokens, context_lens, query_starts, slots,
+                                positions, tree_masks, mask_words, stream)
+        return context_lens, query_starts, slots, positions, tree_masks
+
+    def device_trim_sequences(self, stack: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, new_lens: torch.Tensor,
+                              stream=None) -> None:
+        """Sequences shortened to new_lens: the pages past them go back on the stack, in
+        the reverse of the order ``device_plan_tokens`` takes them in."""
+        batch, maxb = self._check_batch(block_tables, context_lens)
+        self._check_pages(stack, None)
+        self._check_dense(new_lens, (batch,), torch.int32, "new_lens")
+        self._check_current()
+        B.pa_device_trim_sequences(self.handle, stack, block_tables, maxb, context_lens, new_lens,
+                                   batch, stream)
+
+    def device_accept_tree(self, slots: torch.Tensor, parents: torch.Tensor, tokens: torch.Tensor,
+                           targets: torch.Tensor, context_lens: torch.Tensor,
+                           query_starts: torch.Tensor, max_path: int,
+                           counts: Optional[torch.Tensor] = None,
+                           nodes: Optional[torch.Tensor] = None,
+                           next_tokens: Optional[torch.Tensor] = None,
+                           next_lens: Optional[torch.Tensor] = None, stream=None):
+        """Follows every tree from its root along the tokens that the model chose itself
+        (targets[parent] == tokens[child]) and moves the K and V of that path, in all
+        layers, up behind the cached tokens.  Returns (counts, nodes [batch, max_path],
+        next_tokens, next_lens); those that are given are written in place."""
+        batch, rows = context_lens.shape[0], tokens.shape[0]
+        self._check_dense(context_lens, (batch,), torch.int32, "context_lens")
+        self._check_dense(query_starts, (batch + 1,), torch.int32, "query_starts")
+        self._check_dense(slots, (rows,), torch.int64, "slots")
+        for t, name in ((parents, "parents"), (tokens, "tokens"), (targets, "targets")):
+            self._check_dense(t, (rows,), torch.int32, name)
+        out = []
+        for t, shape, name in ((counts, (batch,), "counts"), (nodes, (batch, max_path), "nodes"),
+                               (next_tokens, (batch,), "next_tokens"),
+                               (next_lens, (batch,), "next_lens")):
+            if t is None:
+                t = self._empty(shape, torch.int32, stream)
+            else:
+                self._check_dense(t, shape, torch.int32, name)
+            out.append(t)
+        self._check_current()
+        B.pa_device_accept_tree(self.handle, slots, parents, tokens, targets, context_lens,
+                                query_starts, batch, rows, max_path, *out, stream)
+        return tuple(out)
 
     # -- pages --------------------------------------------------------------
     def copy_blocks(self, src_ids: torch.Tensor, dst_ids: torch.Tensor, stream=None) -> None:
@@ -333,6 +461,20 @@ class BlockPool:
         if tokens and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         return stride[0] if tokens > 1 else heads * d
+
+    def _check_new_rows(self, q, k, v, q_weight, k_weight, rope):
+        """The token strides of what norm + rotation + append read."""
+        tokens = q.shape[0]
+        strides = (self._check_rows(q, tokens, q.shape[1], "q"),
+                   self._check_rows(k, tokens, self.num_kv_heads, "k"),
+                   self._check_rows(v, tokens, self.num_kv_heads, "v"))
+        if q_weight is not None:
+            self._check_dense(q_weight, (self.head_dim,), self.dtype, "q_weight")
+        if k_weight is not None:
+            self._check_dense(k_weight, (self.head_dim,), self.dtype, "k_weight")
+        if rope is not None and rope.handle is None:  # (NULL would mean no rotation)
+            raise ValueError("the Rope is closed")
+        return strides
 
     def _check_batch(self, block_tables, context_lens, query_starts=None):
         batch, maxb = block_tables.shape  # (two dimensions, or a ValueError)
