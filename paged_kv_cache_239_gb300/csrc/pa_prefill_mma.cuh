@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
         if constexpr (TREE) {
             pos[h] = r < rows ? first_pos - 1 : -1;
             mask[h] = p.masks + (r < rows ? (long long)(start + token(row0 + r)) * p.words : 0);
+            if (r < rows) tree_prefetch(mask[h]);
         } else {
             pos[h] = r < rows ? first_pos + token(row0 + r) : -1;
         }
@@ -613,8 +614,9 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
         if (TREE && s_odd) {
             __syncwarp();  // (column t of all, by the four threads of the row)
             if (r < rows)
-                tree_odd_values<T, D>(p, vb - E * cc, b, mask[h], first_pos, n_new, B, kt0 * BN, kt1 * BN, t, 4,
-                                      D, [&](int col, float v) { part[r * L::LO + col] += v; });
+                tree_odd_values<T, D>(vb - E * cc, p.s_blk, p.num_blocks, p.bt + (long long)b * p.maxb, mask[h],
+                                      first_pos, n_new, B, kt0 * BN, kt1 * BN, t, 4, D,
+                                      [row = part + r * L::LO](int col, float v) { row[col] += v; });
         }
         if (t == 0) part_ml[r] = make_float2(m[h], l[h]);
     }

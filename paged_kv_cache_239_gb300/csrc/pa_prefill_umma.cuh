@@ -1046,6 +1046,7 @@ __global__ void __launch_bounds__(384, 1)
             // the last of the keys that the row sees all of, and TREE: its token's mask
             const int pos = live ? (TREE ? pc.first_pos - 1 : pc.first_pos + tok) : -1;
             const unsigned* mask = TREE ? p.masks + (live ? (long long)(pc.start + tok) * p.words : 0) : nullptr;
+            if (TREE && live) tree_prefetch(mask);
             float m = -FLT_MAX;   // reference point of the exponentials (scaled, base 2)
             float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -1059,7 +1060,9 @@ __global__ void __launch_bounds__(384, 1)
                 const unsigned bits = (unsigned)box_bits[((seq >> 1) + i) & 7] & 0xffu;
                 // keys 0 .. lim of the tile are the row's, in pages that are there
                 const int lim = pos - t0;
-                const bool masked = __any_sync(kFullMask, lim < 127) || bits != 0xffu;
+                // (TREE: rows that are not there may see what they like, no one reads them)
+                const bool tail = TREE && t0 + C::TT > pc.first_pos;
+                const bool masked = (TREE ? tail : __any_sync(kFullMask, lim < 127)) || bits != 0xffu;
                 // settles the row's reference point: 0, it stays; 1, raised, the
                 // sum and O scaled down; -1, stop
                 auto raise = [&](float mt) {
@@ -1089,13 +1092,15 @@ __global__ void __launch_bounds__(384, 1)
                     return 1;
                 };
                 uint32_t vis[4];
+                if constexpr (TREE) {
+                    uint4 seen = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+                    if (tail && live) seen = tree_bits128(mask, p.words, t0 - pc.first_pos, pc.n - pc.first_pos);
+                    vis[0] = seen.x, vis[1] = seen.y, vis[2] = seen.z, vis[3] = seen.w;
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const int e = lim - 32 * c;  // the last of the word's keys the row sees
-                    const uint32_t seen =
-                        TREE && live && e < 31 ? tree_bits(mask, p.words, 32 * c + t0 - pc.first_pos, pc.n - pc.first_pos)
-                                               : e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u;
-                    vis[c] = seen &
+                    vis[c] = (TREE ? vis[c] : e >= 31 ? 0xffffffffu : e < 0 ? 0u : (2u << e) - 1u) &
                              (((bits >> (2 * c)) & 1u ? 0xffffu : 0u) |
                               ((bits >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
                 }
@@ -1204,15 +1209,15 @@ __global__ void __launch_bounds__(384, 1)
                 // values that are not finite, into the rows that see them
                 const __nv_bfloat16* vb =
                     static_cast<const __nv_bfloat16*>(p.v_base) + p.tile_off + (long long)pc.kvh * p.s_head;
+                __nv_bfloat16* to = pc.whole() ? static_cast<__nv_bfloat16*>(p.out) + orow * D : nullptr;
                 tree_odd_values<__nv_bfloat16, D>(
-                    p, vb, pc.b, mask, pc.first_pos, pc.n - pc.first_pos, B, pc.kt0 * C::TT, pc.kt1 * C::TT, col0, 1,
-                    turns ? col0 + D / 2 : D, [&](int d, float v) {
-                        if (pc.whole()) {
-                            __nv_bfloat16& x = static_cast<__nv_bfloat16*>(p.out)[orow * D + d];
-                            x = __float2bfloat16(__bfloat162float(x) + v);
-                        } else {
-                            p.part_o[pf_part_at(part, D, d)] += v;
-                        }
+                    vb, p.s_blk, p.num_blocks, p.bt + (long long)pc.b * p.maxb, mask, pc.first_pos,
+                    pc.n - pc.first_pos, B, pc.kt0 * C::TT, pc.kt1 * C::TT, col0, 1, turns ? col0 + D / 2 : D,
+                    [to, part, part_o = p.part_o](int d, float v) {
+                        if (to != nullptr)
+                            to[d] = __float2bfloat16(__bfloat162float(to[d]) + v);
+                        else
+                            part_o[pf_part_at(part, D, d)] += v;
                     });
             } else if (live && *mark_piece == piece) {
                 // values that are not finite, into the rows that see them
