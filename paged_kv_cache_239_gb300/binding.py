@@ -172,11 +172,14 @@ def last_error() -> str:
 
 
 def _check(rc: int, func: str) -> None:
-    if rc != PA_OK:
+    if rc:
         msg = last_error()
         if rc == PA_ERR_NO_FREE_BLOCKS:
             raise OutOfBlocksError(rc, func, msg)
         raise PagedAttnError(rc, func, msg)
+
+
+check = _check  # (for callers of lib()'s functions themselves)
 
 
 def _ptr(x) -> Optional[int]:
@@ -190,10 +193,10 @@ def _ptr(x) -> Optional[int]:
         raise TypeError(f"cannot pass {type(x).__name__} as a pointer") from None
 
 
-_raw_stream = None  # the raw handle of torch's current stream on the current device
+_current = None  # the current device, and the raw handle of torch's current stream on it
 
 
-def _find_raw_stream():
+def _find_current():
     """torch.cuda.current_stream() builds a Stream object (about 3 us, as long as a
     small launch takes); the raw getter behind it does not."""
     import torch
@@ -201,19 +204,25 @@ def _find_raw_stream():
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     device = getattr(torch._C, "_cuda_getDevice", None)
     if not torch.cuda.is_available():
-        return lambda: None
+        return lambda: -1, lambda device: None
     torch.cuda.init()
     if raw is None or device is None:
-        return lambda: torch.cuda.current_stream().cuda_stream
-    return lambda: raw(device())
+        return torch.cuda.current_device, lambda device: torch.cuda.current_stream().cuda_stream
+    return device, raw
+
+
+def current_stream():
+    """(raw handle of torch's current stream, current device); (None, -1) without CUDA."""
+    global _current
+    if _current is None:
+        _current = _find_current()
+    device = _current[0]()
+    return _current[1](device), device
 
 
 def _stream(stream) -> Optional[int]:
-    global _raw_stream
     if stream is None:
-        if _raw_stream is None:
-            _raw_stream = _find_raw_stream()
-        return _raw_stream()
+        return current_stream()[0]
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

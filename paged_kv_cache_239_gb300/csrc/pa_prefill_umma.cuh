@@ -99,7 +99,9 @@ struct PrefillCfg {
     static constexpr int NP = 4;
     static constexpr int TMEM_SLOT = 384, ABORT = 388, MARK_PIECE = 392, DONE = 396, BITS = 404,
                          SCHED = 448, BLOCKS = 528, PIECES = 592, MARKS = 832, SCAN = MARKS;
-    static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 3 * 128 * 4;
+    // (TREE has no marks: there the groups that serve a row tile in turns exchange their sums)
+    static constexpr int SMEM_BYTES = OFF_CTRL + MARKS + 2 * 128 * 8;
+    static_assert(3 * 128 * 4 <= 2 * 128 * 8, "marks");
     static constexpr int THREADS = 384;
     // TMEM: S_0, S_1 (P in their first 64 columns), O_0, O_1
     static constexpr int O_COL = 256;
@@ -202,6 +204,8 @@ __device__ __forceinline__ long long pf_seq_units(const PrefillParams& p, int b,
     s = pf_sequence<B, TREE>(p, b, &bad);
     if (bad && report) atomicOr(p.status, kStatusBadLength);
     long long u = 0;
+    if constexpr (TREE)  // (all pairs of a sequence see the same keys)
+        return s.tiles ? (long long)s.tiles * (kPairUnits + pf_key_tiles<TREE>(p, s, 0)) : 0;
     // (a sequence taken by the whole warp costs what about 32 pairs cost one lane)
     const int lim = 32 * max(1, __popc(__ballot_sync(kFullMask, s.tiles > 16)));
     if (s.tiles <= lim) {
@@ -307,8 +311,13 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
         s = pf_kept(ctrl + C::SCHED + 48);
         long long off = out[3];
         int i = 0;
+        if constexpr (TREE) {
+            const int c = kPairUnits + pf_key_tiles<TREE>(p, s, 0);
+            i = (int)pf_div64(off, c);
+            off -= (long long)i * c;
+        }
 #pragma unroll 1
-        for (int i0 = 0; i0 < s.tiles; i0 += 32) {
+        for (int i0 = 0; i0 < s.tiles && !TREE; i0 += 32) {
             const int c = i0 + lane < s.tiles ? kPairUnits + pf_key_tiles<TREE>(p, s, i0 + lane) : 0;
             long long incl = c;
 #pragma unroll
@@ -673,6 +682,18 @@ __global__ void __launch_bounds__(384, 1)
                     }
                     __syncwarp();
                     if (!more) break;
+                    if constexpr (TREE) {
+                        // Q on its way to L2 while the tiles before it are worked on (from
+                        // DRAM it held up a piece's first scores for 1.6 - 3.6 us)
+                        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+#pragma unroll 1
+                        for (int x = lane; x < min(256, pc.rows - pc.row0) * C::NH; x += 32) {
+                            const int f = pc.row0 + x / C::NH, tok = pf_div(p, f);
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                                q + ((long long)(pc.start + tok) * p.H + pc.kvh * p.G + f - tok * p.G) * D +
+                                64 * (x % C::NH)));
+                        }
+                    }
                 } else if (!next_piece()) {
                     break;
                 }
@@ -1126,18 +1147,22 @@ __global__ void __launch_bounds__(384, 1)
                                    (turns ? 0 : 128 * j) + r;
             // In turns, each group has the sums of its own tiles: both learn the other's
             // maxima and sums, through the rows that a second row tile would have in the
-            // workspace, and each joins and writes half of the columns.
+            // workspace (TREE: in shared memory), and each joins and writes half of the columns.
             float w0 = 1.f, w1 = 0.f;
             const int col0 = turns ? j * (D / 2) : 0;
             if (turns) {
                 float2* ml = reinterpret_cast<float2*>(p.part_ml) + part;
-                __stcg(ml + 128 * j, make_float2(m, l));
+                float2* sums = reinterpret_cast<float2*>(ctrl + C::MARKS) + r;
+                if (TREE)
+                    sums[128 * j] = make_float2(m, l);
+                else
+                    __stcg(ml + 128 * j, make_float2(m, l));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar0 + 8 * C::X_SUMS);
                 if (!(ok = __all_sync(kFullMask, wait(C::X_SUMS, nturns & 1)))) break;
                 tc_fence_after();
-                const float2 other = __ldcg(ml + 128 * (1 - j));
+                const float2 other = TREE ? sums[128 * (1 - j)] : __ldcg(ml + 128 * (1 - j));
                 const float top = fmaxf(m, other.x);
                 const float mine = ex2_approx(m - top), theirs = ex2_approx(other.x - top);
                 w0 = j == 0 ? mine : theirs, w1 = j == 0 ? theirs : mine;
