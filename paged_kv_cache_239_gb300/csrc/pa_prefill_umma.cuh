@@ -341,6 +341,40 @@ __device__ __forceinline__ void pf_schedule(const PrefillParams& p, unsigned cha
     __syncwarp();
 }
 
+// The same for up to 32 sequences of trees, by one warp: all pairs of a sequence cost the
+// same, so that its lane knows where they stand.
+template <typename C>
+__device__ __forceinline__ void tree_schedule(const PrefillParams& p, unsigned char* ctrl) {
+    const int lane = threadIdx.x & 31;
+    bool bad;
+    const PfSeq s = pf_sequence<C::B, true>(p, lane, &bad);
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadLength);
+    const int c = kPairUnits + pf_key_tiles<true>(p, s, 0);
+    const long long u = (long long)s.tiles * p.Hkv * c;
+    long long incl = u;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const long long v = __shfl_up_sync(kFullMask, incl, x);
+        if (lane >= x) incl += v;
+    }
+    const long long T = __shfl_sync(kFullMask, incl, 31);
+    const long long grid = min((long long)gridDim.x, T), j = blockIdx.x;
+    long long* out = reinterpret_cast<long long*>(ctrl + C::SCHED);
+    int* outi = reinterpret_cast<int*>(ctrl + C::SCHED + 32);
+    long long x = 0;
+    if (j < grid) x = pf_div64((j + (lane & 1)) * T + grid - 1, grid);
+    const long long lo = __shfl_sync(kFullMask, x, 0), hi = __shfl_sync(kFullMask, x, 1);
+    if (lane == 0) out[0] = T, out[1] = lo, out[2] = hi - lo;
+    const long long at = lo - (incl - u);  // within the lane's sequence, if it is this one's
+    if (at >= 0 && at < u && hi > lo) {
+        const int pair = (int)pf_div64(at, c), h = pair / s.tiles;
+        outi[0] = lane, outi[1] = h, outi[2] = pair - h * s.tiles;
+        out[3] = at - (long long)pair * c;
+        pf_keep(s, ctrl + C::SCHED + 48);
+    }
+    __syncwarp();
+}
+
 template <typename C>
 __device__ __forceinline__ void pf_walk_begin(const PrefillParams& p, const unsigned char* ctrl,
                                               PfWalk& w) {
@@ -599,17 +633,22 @@ __global__ void __launch_bounds__(384, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < C::NBAR; ++i) {
-            const bool p_full = i >= C::P_FULL && i < C::P_FULL + 6;
-            const bool pc_empty = i >= C::PC_EMPTY && i < C::PC_EMPTY + C::NP;
-            mbar_init(bar0 + 8 * i, p_full ? 4 : pc_empty ? 11 : i >= C::X_SUMS ? 8 : 1);
-        }
-        *abort_all = 0, *mark_piece = -1, done[0] = 0, done[1] = 0;
+    static_assert(C::NBAR <= 64, "barriers");
+    if (warp == 2 || warp == 3) {  // (a barrier to a lane)
+        const int i = threadIdx.x - 64;
+        const bool p_full = i >= C::P_FULL && i < C::P_FULL + 6;
+        const bool pc_empty = i >= C::PC_EMPTY && i < C::PC_EMPTY + C::NP;
+        if (i < C::NBAR) mbar_init(bar0 + 8 * i, p_full ? 4 : pc_empty ? 11 : i >= C::X_SUMS ? 8 : 1);
+        if (i == 0) *abort_all = 0, *mark_piece = -1, done[0] = 0, done[1] = 0;
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
+    // (the schedule of up to 32 trees is warp 0's alone, and runs beside all this)
+    const bool early = TREE && p.batch <= 32;
+    if (early && warp == 0) {
+        pdl_wait();
+        tree_schedule<C>(p, ctrl);
+    }
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
@@ -622,7 +661,7 @@ __global__ void __launch_bounds__(384, 1)
     pdl_wait();
     // (the K producer alone needs the schedule: with few sequences the other warps are
     // at their first wait, their code fetched, when it hands out the first piece)
-    pf_schedule<C, TREE>(p, ctrl);
+    if (!early) pf_schedule<C, TREE>(p, ctrl);
     auto wait = [&](int bar, uint32_t parity) {
         return pf_wait(bar0 + 8 * bar, parity, abort_all, p.status);
     };
