@@ -2,13 +2,16 @@
 
 Each translation unit is compiled in parallel, then linked into one shared
 library under ``paged_kv_cache_239_gb300/_build/``.  Only one ``-gencode``
-(sm_103a) is emitted.
+(sm_103a) is emitted.  Beside it, for the installed Python and torch, the module
+``pagedcalls`` (``pa_calls.cpp``), which calls the library.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,9 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 OUT_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libpagedattn.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
+
+CALLS_NAME = "pagedcalls.so"
+CALLS_PATH = os.path.join(OUT_DIR, CALLS_NAME)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["pa_api.cpp", "pa_aux.cu", "pa_decode_bf16.cu", "pa_decode_f32.cu",
@@ -41,10 +47,39 @@ def _inputs():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _compile_calls() -> str:
+    """The object of the Python module (found without importing torch, which takes
+    longer than the rest of the build on a cold machine)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = os.path.join(torch_dir, "include")
+    obj = os.path.join(OUT_DIR, "pa_calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include"),
+           "-c", os.path.join(CSRC, "pa_calls.cpp"), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for pa_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    torch_lib = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lpagedattn", "-Wl,-rpath,$ORIGIN",
+           "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           f"-Wl,-rpath,{torch_lib}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -70,14 +105,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(res.stdout + res.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls_obj = calls.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl", "-lpthread"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_calls(calls_obj)
     return LIB_PATH
 
 

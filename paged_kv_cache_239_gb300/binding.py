@@ -13,7 +13,7 @@ import os
 import re
 from typing import Optional
 
-from ._build_lib import LIB_PATH, INCLUDE
+from ._build_lib import CALLS_PATH, INCLUDE, LIB_PATH
 
 PA_OK = 0
 PA_ERR_INVALID_ARG = 1
@@ -160,6 +160,32 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_calls = None
+
+
+def calls():
+    """The module that makes a speculation step's calls (``csrc/pa_calls.cpp``): it checks
+    the tensors and calls the library without ctypes.  Raises if it has not been built,
+    or for another torch."""
+    global _calls
+    if _calls is None:
+        import importlib.util
+
+        import torch
+
+        lib()  # (says how to build it)
+        spec = importlib.util.spec_from_file_location("pagedcalls", CALLS_PATH)
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"{CALLS_PATH} is missing: build it as {LIB_PATH}")
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if module.torch_version != torch.__version__.split("+")[0]:
+            raise RuntimeError(f"{CALLS_PATH} was built for torch {module.torch_version}, not "
+                               f"{torch.__version__}: build it again")
+        _calls = module
+    return _calls
+
+
 def header_symbols() -> list:
     """Names of the functions declared in include/pagedattn.h."""
     text = open(os.path.join(INCLUDE, "pagedattn.h")).read()
@@ -172,7 +198,7 @@ def last_error() -> str:
 
 
 def _check(rc: int, func: str) -> None:
-    if rc:
+    if rc != PA_OK:
         msg = last_error()
         if rc == PA_ERR_NO_FREE_BLOCKS:
             raise OutOfBlocksError(rc, func, msg)
@@ -193,10 +219,10 @@ def _ptr(x) -> Optional[int]:
         raise TypeError(f"cannot pass {type(x).__name__} as a pointer") from None
 
 
-_current = None  # the current device, and the raw handle of torch's current stream on it
+_raw_stream = None  # the raw handle of torch's current stream on the current device
 
 
-def _find_current():
+def _find_raw_stream():
     """torch.cuda.current_stream() builds a Stream object (about 3 us, as long as a
     small launch takes); the raw getter behind it does not."""
     import torch
@@ -204,25 +230,19 @@ def _find_current():
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     device = getattr(torch._C, "_cuda_getDevice", None)
     if not torch.cuda.is_available():
-        return lambda: -1, lambda device: None
+        return lambda: None
     torch.cuda.init()
     if raw is None or device is None:
-        return torch.cuda.current_device, lambda device: torch.cuda.current_stream().cuda_stream
-    return device, raw
-
-
-def current_stream():
-    """(raw handle of torch's current stream, current device); (None, -1) without CUDA."""
-    global _current
-    if _current is None:
-        _current = _find_current()
-    device = _current[0]()
-    return _current[1](device), device
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _stream(stream) -> Optional[int]:
+    global _raw_stream
     if stream is None:
-        return current_stream()[0]
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

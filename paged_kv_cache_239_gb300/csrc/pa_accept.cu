@@ -13,7 +13,7 @@
 // among themselves, several CTAs to a sequence, each of which walks by itself.
 //
 // What bounds it: bytes, two times the rows that move, and for small batches the chain of
-// dependent loads before them (starts, parents, targets, slots).
+// dependent loads (starts, the tree, rows).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,9 +29,12 @@ constexpr int kAcceptThreads = 256;
 __global__ void __launch_bounds__(kAcceptThreads) pa_accept_kernel(const AcceptParams p) {
     pdl_trigger();
     pdl_wait();
-    __shared__ int s_child[kMaxTreeNodes], s_path[kMaxTreeNodes];
-    __shared__ long long s_src[kMaxTreeNodes], s_dst[kMaxTreeNodes];
+    extern __shared__ long long s_moves[];  // [max_path] sources, destinations; then the path
+    __shared__ int s_child[kMaxTreeNodes], s_target[kMaxTreeNodes];
+    __shared__ long long s_slot[kMaxTreeNodes];
     __shared__ int s_count;
+    long long *s_src = s_moves, *s_dst = s_moves + p.max_path;
+    int* s_path = reinterpret_cast<int*>(s_moves + 2 * p.max_path);
     const int tid = threadIdx.x;
     const int b = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
     const int start = ld_dep(p.starts + b), end = ld_dep(p.starts + b + 1), len = ld_dep(p.lens + b);
@@ -39,14 +42,23 @@ __global__ void __launch_bounds__(kAcceptThreads) pa_accept_kernel(const AcceptP
     const bool good = start >= 0 && end >= start && end <= p.num_tokens && n <= kMaxTreeNodes && n <= len;
     const int nodes = good ? n : 0;
     if (!good && part == 0 && tid == 0) atomicOr(p.g.status, kStatusBadLength);
-    for (int i = tid; i < nodes; i += kAcceptThreads) s_child[i] = kMaxTreeNodes;
-    __syncthreads();
-    for (int i = 1 + tid; i < nodes; i += kAcceptThreads) {
-        const int up = ld_dep(p.parents + start + i);
-        if (up < -1 || up >= i) {
-            if (part == 0) atomicOr(p.g.status, kStatusBadLength);
-        } else if (up >= 0 && ld_dep(p.tokens + start + i) == ld_dep(p.targets + start + up)) {
-            atomicMin(s_child + up, i);
+    // (all of the tree in one round of loads)
+    for (int i0 = 0; i0 < nodes; i0 += kAcceptThreads) {
+        const int i = i0 + tid;
+        int up = -1, token = 0;
+        if (i < nodes) {
+            up = ld_dep(p.parents + start + i), token = ld_dep(p.tokens + start + i);
+            s_target[i] = ld_dep(p.targets + start + i);
+            s_slot[i] = ld_dep(p.slots + start + i);
+            s_child[i] = kMaxTreeNodes;
+        }
+        __syncthreads();
+        if (i > 0 && i < nodes) {
+            if (up < -1 || up >= i) {
+                if (part == 0) atomicOr(p.g.status, kStatusBadLength);
+            } else if (up >= 0 && token == s_target[up]) {
+                atomicMin(s_child + up, i);
+            }
         }
     }
     __syncthreads();
@@ -62,7 +74,7 @@ __global__ void __launch_bounds__(kAcceptThreads) pa_accept_kernel(const AcceptP
             p.nodes[(long long)b * p.max_path + k] = k < count ? s_path[k] : -1;
         if (tid == 0) {
             p.counts[b] = count;
-            p.next_tokens[b] = count > 0 ? ld_dep(p.targets + start + s_path[count - 1]) : -1;
+            p.next_tokens[b] = count > 0 ? s_target[s_path[count - 1]] : -1;
             p.next_lens[b] = good ? len - n + count : len;
         }
     }
@@ -70,7 +82,7 @@ __global__ void __launch_bounds__(kAcceptThreads) pa_accept_kernel(const AcceptP
     for (int k = tid; k < count; k += kAcceptThreads) {
         long long from = -1, to = -1;
         if (s_path[k] != k) {
-            const long long a = ld_dep(p.slots + start + s_path[k]), z = ld_dep(p.slots + start + k);
+            const long long a = s_slot[s_path[k]], z = s_slot[k];
             const long long most = p.g.num_blocks * p.g.B;
             if (a >= 0 && a < most && z >= 0 && z < most) {
                 const int row = p.g.tile_bytes / p.g.B;
@@ -123,7 +135,8 @@ cudaError_t launch_accept(const AcceptParams& p_in, int num_sms, cudaStream_t s)
     p.parts = (int)parts;
     const long long grid = parts * p.batch;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_pdl(pa_accept_kernel, dim3((unsigned)grid), dim3(kAcceptThreads), 0, s, p);
+    return launch_pdl(pa_accept_kernel, dim3((unsigned)grid), dim3(kAcceptThreads),
+                      (size_t)p.max_path * 20, s, p);
 }
 
 }  // namespace pa

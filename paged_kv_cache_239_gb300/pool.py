@@ -23,16 +23,6 @@ _PREFILL_KERNELS = {"auto": B.PA_PREFILL_AUTO, "mma": B.PA_PREFILL_MMA, "tcgen05
 _I32, _I64 = torch.int32, torch.int64
 
 
-def _dense(t: torch.Tensor, shape, dtype, device: int) -> bool:
-    """What ``BlockPool._check_dense`` demands.  The calls of a speculation step take a
-    dozen small tensors each and run for a few microseconds: they look at all of them in one
-    expression, hand their addresses to the library as they are, and leave it to the slow
-    checks to say what is wrong (through these and the binding's functions a call took
-    10.5 us of the host, of which the launch is 2.9)."""
-    return (t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == device)
-
-
 class BlockPool:
     def __init__(self, num_blocks: int, block_size: int = 16, num_layers: int = 24,
                  num_kv_heads: int = 2, head_dim: int = 64, dtype=torch.bfloat16,
@@ -47,7 +37,7 @@ class BlockPool:
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
         self.dtype = tensor.dtype
         self._device_index = tensor.get_device()
-        self._lib = B.lib()
+        self._calls, self._type = B.calls(), B._dtype_code(tensor.dtype)
         self.handle = B.pa_pool_create(tensor, num_blocks, num_layers, num_kv_heads, block_size,
                                        head_dim, tensor.dtype)
 
@@ -201,23 +191,21 @@ class BlockPool:
         """norm_rope_write_kv with a position (int32) and a slot (int64, page *
         block_size + row) for each token, as ``device_plan_tokens`` writes them.  Rows
         with a negative slot are no tokens: neither ``out`` nor the cache is written."""
-        tokens, num_heads = q.shape[0], q.shape[1]
-        strides = self._check_new_rows(q, k, v, q_weight, k_weight, rope)
-        dev, rows = self._device_index, (tokens,)
-        if not (_dense(positions, rows, _I32, dev) and _dense(slots, rows, _I64, dev)):
-            self._check_dense(positions, rows, _I32, "positions")
-            self._check_dense(slots, rows, _I64, "slots")
         if out is None:
             out = self._empty(q.shape, self.dtype, stream)
-        else:
-            self._check_dense(out, (tokens, num_heads, self.head_dim), self.dtype, "out")
-        stream = self._call_stream(stream)
-        B.check(self._lib.pa_norm_rope_write_kv_slots(
-            self.handle, layer, out.data_ptr(), q.data_ptr(), strides[0], k.data_ptr(), strides[1],
-            v.data_ptr(), strides[2], None if rope is None else rope.handle,
-            None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps, positions.data_ptr(),
-            slots.data_ptr(), tokens, num_heads, stream), "pa_norm_rope_write_kv_slots")
+        if rope is not None and rope.handle is None:  # (NULL would mean no rotation)
+            raise ValueError("the Rope is closed")
+        rc = self._calls.append(
+            self.handle, self._device_index, self._type, self.num_kv_heads, self.head_dim, layer, out,
+            q, k, v, None if rope is None else rope.handle, q_weight, k_weight, eps, positions, slots,
+            None if stream is None else B._stream(stream))
+        if rc:
+            rows = (q.shape[0],)
+            self._refused(rc, "pa_norm_rope_write_kv_slots", lambda: (
+                self._check_new_rows(q, k, v, q_weight, k_weight, rope),
+                self._check_dense(positions, rows, _I32, "positions"),
+                self._check_dense(slots, rows, _I64, "slots"),
+                self._check_dense(out, rows + (q.shape[1], self.head_dim), self.dtype, "out")))
         return out
 
     def set_prefill_kernel(self, kind: str) -> None:
@@ -268,31 +256,27 @@ class BlockPool:
         """prefill_attention of drafted trees: a new token sees what is cached before its
         sequence's new tokens and those of them whose bits are set in its row of
         tree_masks (int32 [tokens, words], as ``device_plan_tokens`` writes them)."""
-        tokens, num_heads = q.shape[0], q.shape[1]
-        batch, maxb = block_tables.shape  # (two dimensions, or a ValueError)
-        words = tree_masks.shape[-1]
-        dev, dtype, shape = self._device_index, self.dtype, (tokens, num_heads, self.head_dim)
         if out is None:
-            out = self._empty(shape, dtype, stream)
-        if not (_dense(q, shape, dtype, dev) and _dense(out, shape, dtype, dev)
-                and _dense(block_tables, (batch, maxb), _I32, dev)
-                and _dense(context_lens, (batch,), _I32, dev)
-                and _dense(query_starts, (batch + 1,), _I32, dev)
-                and _dense(tree_masks, (tokens, words), _I32, dev)):
-            self._check_dense(q, shape, dtype, "q")
-            self._check_dense(out, shape, dtype, "out")
-            self._check_batch(block_tables, context_lens, query_starts)
-            self._check_dense(tree_masks, (tokens, words), _I32, "tree_masks")
-        raw = self._call_stream(stream)
+            out = self._empty(q.shape, self.dtype, stream)
         if workspace is None:  # (the call checks one that is given)
-            need = self.tree_workspace_size(batch, tokens, num_heads, maxb)
+            batch, maxb = block_tables.shape  # (two dimensions, or a ValueError)
+            self._check_current()
+            need = self.tree_workspace_size(batch, q.shape[0], q.shape[1], maxb)
             if need:
                 workspace = self._empty((need,), torch.uint8, stream)
-        B.check(self._lib.pa_tree_attention(
-            out.data_ptr(), q.data_ptr(), self.handle, layer, block_tables.data_ptr(), maxb,
-            context_lens.data_ptr(), query_starts.data_ptr(), tree_masks.data_ptr(), words, batch,
-            tokens, num_heads, scale, None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.nbytes, raw), "pa_tree_attention")
+        rc = self._calls.tree(
+            self.handle, self._device_index, self._type, self.head_dim, layer, out, q, block_tables,
+            context_lens, query_starts, tree_masks, scale, workspace,
+            None if stream is None else B._stream(stream))
+        if rc:
+            shape = (q.shape[0], q.shape[1], self.head_dim)
+            self._refused(rc, "pa_tree_attention", lambda: (
+                self._check_dense(q, shape, self.dtype, "q"),
+                self._check_dense(out, shape, self.dtype, "out"),
+                self._check_batch(block_tables, context_lens, query_starts),
+                self._check_dense(tree_masks, (q.shape[0], tree_masks.shape[-1]), _I32, "tree_masks"),
+                workspace is None or self._check_dense(workspace, workspace.shape, workspace.dtype,
+                                                       "workspace")))
         return out
 
     # -- new tokens planned, drafted trees decided --------------------------
@@ -311,8 +295,8 @@ class BlockPool:
         root) makes them trees; with ``mask_words`` (or ``tree_masks``) each row's
         ancestors are written as bits.  Returns (context_lens, query_starts, slots,
         positions, tree_masks); those that are given are written in place."""
-        batch, maxb = block_tables.shape  # (two dimensions, or a ValueError)
-        dev, seqs, rows = self._device_index, (batch,), (num_tokens,)
+        batch = cached_lens.shape[0]
+        seqs, rows = (batch,), (num_tokens,)
         if tree_masks is not None:
             mask_words = mask_words or tree_masks.shape[-1]
         elif mask_words:
@@ -325,29 +309,21 @@ class BlockPool:
             slots = self._empty(rows, _I64, stream)
         if positions is None:
             positions = self._empty(rows, _I32, stream)
-        if not (_dense(block_tables, (batch, maxb), _I32, dev) and _dense(cached_lens, seqs, _I32, dev)
-                and _dense(stack, (self.num_blocks + 1,), _I32, dev)
-                and _dense(new_counts, seqs, _I32, dev)
-                and (parents is None or _dense(parents, rows, _I32, dev))
-                and _dense(context_lens, seqs, _I32, dev)
-                and _dense(query_starts, (batch + 1,), _I32, dev) and _dense(slots, rows, _I64, dev)
-                and _dense(positions, rows, _I32, dev)
-                and (tree_masks is None or _dense(tree_masks, (num_tokens, mask_words), _I32, dev))):
-            self._check_batch(block_tables, cached_lens, query_starts)
-            self._check_pages(stack, None)
-            for t, name in ((new_counts, "new_counts"), (context_lens, "context_lens")):
-                self._check_dense(t, seqs, _I32, name)
-            if parents is not None:
-                self._check_dense(parents, rows, _I32, "parents")
-            self._check_dense(slots, rows, _I64, "slots")
-            self._check_dense(positions, rows, _I32, "positions")
-            self._check_dense(tree_masks, (num_tokens, mask_words), _I32, "tree_masks")
-        B.check(self._lib.pa_device_plan_tokens(
-            self.handle, stack.data_ptr(), block_tables.data_ptr(), maxb, cached_lens.data_ptr(),
-            new_counts.data_ptr(), None if parents is None else parents.data_ptr(), batch,
-            num_tokens, context_lens.data_ptr(), query_starts.data_ptr(), slots.data_ptr(),
-            positions.data_ptr(), None if tree_masks is None else tree_masks.data_ptr(), mask_words,
-            self._call_stream(stream)), "pa_device_plan_tokens")
+        rc = self._calls.plan(
+            self.handle, self._device_index, self.num_blocks, stack, block_tables, cached_lens,
+            new_counts, num_tokens, parents, context_lens, query_starts, slots, positions, tree_masks,
+            mask_words, None if stream is None else B._stream(stream))
+        if rc:
+            self._refused(rc, "pa_device_plan_tokens", lambda: (
+                self._check_batch(block_tables, cached_lens, query_starts),
+                self._check_pages(stack, None),
+                self._check_dense(new_counts, seqs, _I32, "new_counts"),
+                self._check_dense(context_lens, seqs, _I32, "context_lens"),
+                parents is None or self._check_dense(parents, rows, _I32, "parents"),
+                self._check_dense(slots, rows, _I64, "slots"),
+                self._check_dense(positions, rows, _I32, "positions"),
+                tree_masks is None or self._check_dense(tree_masks, (num_tokens, mask_words), _I32,
+                                                        "tree_masks")))
         return context_lens, query_starts, slots, positions, tree_masks
 
     def device_trim_sequences(self, stack: torch.Tensor, block_tables: torch.Tensor,
@@ -355,17 +331,13 @@ class BlockPool:
                               stream=None) -> None:
         """Sequences shortened to new_lens: the pages past them go back on the stack, in
         the reverse of the order ``device_plan_tokens`` takes them in."""
-        batch, maxb = block_tables.shape  # (two dimensions, or a ValueError)
-        dev, seqs = self._device_index, (batch,)
-        if not (_dense(block_tables, (batch, maxb), _I32, dev) and _dense(context_lens, seqs, _I32, dev)
-                and _dense(stack, (self.num_blocks + 1,), _I32, dev)
-                and _dense(new_lens, seqs, _I32, dev)):
-            self._check_batch(block_tables, context_lens)
-            self._check_pages(stack, None)
-            self._check_dense(new_lens, seqs, _I32, "new_lens")
-        B.check(self._lib.pa_device_trim_sequences(
-            self.handle, stack.data_ptr(), block_tables.data_ptr(), maxb, context_lens.data_ptr(),
-            new_lens.data_ptr(), batch, self._call_stream(stream)), "pa_device_trim_sequences")
+        rc = self._calls.trim(self.handle, self._device_index, self.num_blocks, stack, block_tables,
+                              context_lens, new_lens, None if stream is None else B._stream(stream))
+        if rc:
+            self._refused(rc, "pa_device_trim_sequences", lambda: (
+                self._check_batch(block_tables, context_lens),
+                self._check_pages(stack, None),
+                self._check_dense(new_lens, (block_tables.shape[0],), _I32, "new_lens")))
 
     def device_accept_tree(self, slots: torch.Tensor, parents: torch.Tensor, tokens: torch.Tensor,
                            targets: torch.Tensor, context_lens: torch.Tensor,
@@ -378,8 +350,8 @@ class BlockPool:
         (targets[parent] == tokens[child]) and moves the K and V of that path, in all
         layers, up behind the cached tokens.  Returns (counts, nodes [batch, max_path],
         next_tokens, next_lens); those that are given are written in place."""
-        batch, total = context_lens.shape[0], tokens.shape[0]
-        dev, seqs, rows = self._device_index, (batch,), (total,)
+        batch = context_lens.shape[0]
+        seqs, rows = (batch,), (tokens.shape[0],)
         if counts is None:
             counts = self._empty(seqs, _I32, stream)
         if nodes is None:
@@ -388,25 +360,20 @@ class BlockPool:
             next_tokens = self._empty(seqs, _I32, stream)
         if next_lens is None:
             next_lens = self._empty(seqs, _I32, stream)
-        if not (_dense(slots, rows, _I64, dev) and _dense(parents, rows, _I32, dev)
-                and _dense(tokens, rows, _I32, dev) and _dense(targets, rows, _I32, dev)
-                and _dense(context_lens, seqs, _I32, dev)
-                and _dense(query_starts, (batch + 1,), _I32, dev) and _dense(counts, seqs, _I32, dev)
-                and _dense(nodes, (batch, max_path), _I32, dev)
-                and _dense(next_tokens, seqs, _I32, dev) and _dense(next_lens, seqs, _I32, dev)):
-            self._check_dense(slots, rows, _I64, "slots")
-            for t, name in ((parents, "parents"), (tokens, "tokens"), (targets, "targets")):
-                self._check_dense(t, rows, _I32, name)
-            self._check_dense(query_starts, (batch + 1,), _I32, "query_starts")
-            self._check_dense(nodes, (batch, max_path), _I32, "nodes")
-            for t, name in ((context_lens, "context_lens"), (counts, "counts"),
-                            (next_tokens, "next_tokens"), (next_lens, "next_lens")):
-                self._check_dense(t, seqs, _I32, name)
-        B.check(self._lib.pa_device_accept_tree(
-            self.handle, slots.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
-            targets.data_ptr(), context_lens.data_ptr(), query_starts.data_ptr(), batch, total,
-            max_path, counts.data_ptr(), nodes.data_ptr(), next_tokens.data_ptr(),
-            next_lens.data_ptr(), self._call_stream(stream)), "pa_device_accept_tree")
+        rc = self._calls.accept(
+            self.handle, self._device_index, slots, parents, tokens, targets, context_lens,
+            query_starts, max_path, counts, nodes, next_tokens, next_lens,
+            None if stream is None else B._stream(stream))
+        if rc:
+            self._refused(rc, "pa_device_accept_tree", lambda: (
+                self._check_dense(slots, rows, _I64, "slots"),
+                [self._check_dense(t, rows, _I32, name) for t, name in (
+                    (parents, "parents"), (tokens, "tokens"), (targets, "targets"))],
+                self._check_dense(query_starts, (batch + 1,), _I32, "query_starts"),
+                self._check_dense(nodes, (batch, max_path), _I32, "nodes"),
+                [self._check_dense(t, seqs, _I32, name) for t, name in (
+                    (context_lens, "context_lens"), (counts, "counts"), (next_tokens, "next_tokens"),
+                    (next_lens, "next_lens"))]))
         return counts, nodes, next_tokens, next_lens
 
     # -- pages --------------------------------------------------------------
@@ -496,15 +463,15 @@ class BlockPool:
         if self._device_index < 0 or torch.cuda.current_device() != self._device_index:
             raise ValueError(f"the pool is on {self.pool.device}, which is not the current CUDA device")
 
-    def _call_stream(self, stream) -> Optional[int]:
-        """The raw stream of a call, which launches on torch's current device."""
-        if stream is not None:
+    def _refused(self, rc: int, name: str, checks) -> None:
+        """A call that did not go through: the library's error, or what is wrong with
+        the tensors (which the call only looked over)."""
+        if rc > 0:
+            B.check(rc, name)
+        if rc == self._calls.WRONG_DEVICE:
             self._check_current()
-            return B._stream(stream)
-        raw, device = B.current_stream()
-        if device != self._device_index or device < 0:
-            raise ValueError(f"the pool is on {self.pool.device}, which is not the current CUDA device")
-        return raw
+        checks()
+        raise TypeError(f"{name}: an argument is not of the type that the call takes")
 
     def _check_dense(self, t: torch.Tensor, shape, dtype, name: str) -> None:
         if (t.shape == shape and t.dtype is dtype and t.get_device() == self._device_index
