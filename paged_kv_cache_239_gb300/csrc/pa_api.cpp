@@ -919,10 +919,10 @@ int check_stack(const void* dev_stack) {
 // What both prefill calls need of the sizes: how the work is split, and where
 // the workspace holds what.
 struct PrefillShape {
-    int splits = 1, cluster = 1, grid = 0;
+    int splits = 1, cluster = 1, grid = 0, row_tile = 0;
     size_t ml_off = 0, cut_off = 0, ws_bytes = 0;
 };
-int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads, int maxb,
+int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads, int maxb, bool tree,
                   PrefillShape* sh) {
     const pa::PoolGeom& g = pool->g;
     if (batch < 0 || num_tokens < 0)
@@ -954,16 +954,24 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
     if (int rc = num_sms_current(&sms)) return rc;
     const int G = num_heads / g.Hkv;
     size_t rows = 0;  // rows of partials
-    const bool mma = kind == PA_PREFILL_AUTO
-                         ? g.dtype == 0 || pa::prefill_mma_preferred(G, g.Hkv, batch, num_tokens, maxb,
-                                                                     g.D, g.B, sms)
-                         : kind == PA_PREFILL_MMA;
+    double here = 0, there = 0;  // (trees: both kernels' times by estimate)
+    if (tree) {
+        here = pa::tree_mma_plan(g.dtype, G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms, &sh->row_tile,
+                                 &sh->splits, &sh->cluster);
+        there = pa::tree_umma_time(G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms);
+    }
+    const bool mma = kind != PA_PREFILL_AUTO ? kind == PA_PREFILL_MMA
+                     : g.dtype == 0         ? true
+                     : tree                 ? here < there
+                                            : pa::prefill_mma_preferred(G, g.Hkv, batch, num_tokens, maxb, g.D,
+                                                                        g.B, sms);
     if (!mma) {
         sh->grid = pa::prefill_umma_grid(G, g.Hkv, batch, num_tokens, maxb, g.B, sms);
         if (sh->grid > 1) rows = (size_t)sh->grid * 2 * 256;
     } else {
-        sh->splits = pa::prefill_mma_splits(g.dtype, G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms,
-                                            &sh->cluster);
+        if (!tree)
+            sh->splits = pa::prefill_mma_splits(g.dtype, G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms,
+                                                &sh->cluster);
         const int groups = sh->splits / sh->cluster;
         if (groups > 1) rows = (size_t)groups * num_tokens * num_heads;
     }
@@ -1064,7 +1072,8 @@ int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const i
     if (!std::isfinite(scale * 1.4426950408889634f))
         return fail(PA_ERR_INVALID_ARG, "scale is not finite (times log2 e)");
     PrefillShape sh;
-    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq,
+                               tree_masks != nullptr, &sh))
         return rc;
     if (batch == 0 || num_tokens == 0) return PA_OK;
     if (!out || !q || !aligned(out, 16) || !aligned(q, 16))
@@ -1113,8 +1122,10 @@ int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const i
         e = tree_masks ? pa::launch_tree_umma(p, pool->tmaps, g.D, g.B, s)
                        : pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
     } else {
-        e = tree_masks ? pa::launch_tree_mma(p, g.dtype, g.D, g.B, s)
-                       : pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s);
+        p.row_tile = sh.row_tile;
+        e = !tree_masks      ? pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s)
+            : g.dtype == 1 ? pa::launch_tree_mma_bf16(p, g.D, g.B, s)
+                           : pa::launch_tree_mma_f32(p, g.D, g.B, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
     return PA_OK;
@@ -1251,7 +1262,7 @@ int pa_prefill_workspace_size(const pa_pool* pool, int batch, int num_tokens, in
     if (int rc = check_pool(pool)) return rc;
     if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes is NULL");
     PrefillShape sh;
-    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, &sh))
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, false, &sh))
         return rc;
     *bytes = sh.ws_bytes;
     return PA_OK;
@@ -1269,7 +1280,13 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
 
 int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens, int num_heads,
                            int max_blocks_per_seq, size_t* bytes) {
-    return pa_prefill_workspace_size(pool, batch, num_tokens, num_heads, max_blocks_per_seq, bytes);
+    if (int rc = check_pool(pool)) return rc;
+    if (!bytes) return fail(PA_ERR_INVALID_ARG, "bytes is NULL");
+    PrefillShape sh;
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, true, &sh))
+        return rc;
+    *bytes = sh.ws_bytes;
+    return PA_OK;
 }
 
 int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int layer,

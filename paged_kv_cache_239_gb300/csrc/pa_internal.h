@@ -153,6 +153,7 @@ struct PrefillParams {
     int div_shift;
     const unsigned* masks;   // trees: [num_tokens, words], see pa_tree_mask.cuh
     int words;
+    int row_tile;            // trees on mma.sync, fp32: rows of a tile
 };
 
 // New tokens: pages, slots, positions and masks; and pages given back (see pa_plan.cu).
@@ -232,7 +233,13 @@ cudaError_t launch_prefill_umma(const PrefillParams& p, const void* tmaps, int D
                                 cudaStream_t s);
 
 // The same kernels with a mask for each token.
-cudaError_t launch_tree_mma(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s);
+cudaError_t launch_tree_mma_bf16(const PrefillParams& p, int D, int B, cudaStream_t s);
+cudaError_t launch_tree_mma_f32(const PrefillParams& p, int D, int B, cudaStream_t s);
+// mma.sync: the rows of its tiles (fp32: 16, 32 or 64), the parts of each context and those
+// of a cluster, and the call's time by estimate, in us; and tcgen05's.
+double tree_mma_plan(int dtype, int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
+                     int num_sms, int* row_tile, int* splits, int* cluster);
+double tree_umma_time(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B, int num_sms);
 cudaError_t launch_tree_umma(const PrefillParams& p, const void* tmaps, int D, int B, cudaStream_t s);
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);

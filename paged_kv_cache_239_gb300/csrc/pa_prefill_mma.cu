@@ -48,7 +48,7 @@ int prefill_mma_splits(int dtype, int G, int Hkv, int batch, int num_tokens, int
                        int num_sms, int* cluster) {
     const int BN = dtype == 1 ? (D == 64 ? CoreBf16<64>::BN : CoreBf16<128>::BN)
                               : (D == 64 ? CoreF32<64>::BN : CoreF32<128>::BN);
-    const long long tiles = ((long long)num_tokens * G / BM + batch) * Hkv;
+    const long long tiles = ((long long)num_tokens * G / CoreF32<64>::BM + batch) * Hkv;
     const long long keys = ((long long)maxb * B + BN - 1) / BN;  // tiles
     if (tiles <= 0) return *cluster = 1;
     const long long wide = std::min({2 * num_sms / tiles, keys, 256LL});
@@ -66,7 +66,18 @@ int prefill_mma_splits(int dtype, int G, int Hkv, int batch, int num_tokens, int
 }
 
 cudaError_t launch_prefill_mma(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s) {
-    return launch_mma<false>(p, dtype, D, B, s);
+    if (dtype == 1) {
+        if (D == 64 && B == 16) return launch_mma_inst<CoreBf16<64>, 64, 16, false>(p, s);
+        if (D == 64 && B == 32) return launch_mma_inst<CoreBf16<64>, 64, 32, false>(p, s);
+        if (D == 128 && B == 16) return launch_mma_inst<CoreBf16<128>, 128, 16, false>(p, s);
+        if (D == 128 && B == 32) return launch_mma_inst<CoreBf16<128>, 128, 32, false>(p, s);
+    } else {
+        if (D == 64 && B == 16) return launch_mma_inst<CoreF32<64>, 64, 16, false>(p, s);
+        if (D == 64 && B == 32) return launch_mma_inst<CoreF32<64>, 64, 32, false>(p, s);
+        if (D == 128 && B == 16) return launch_mma_inst<CoreF32<128>, 128, 16, false>(p, s);
+        if (D == 128 && B == 32) return launch_mma_inst<CoreF32<128>, 128, 32, false>(p, s);
+    }
+    return cudaErrorNotSupported;
 }
 
 }  // namespace pa

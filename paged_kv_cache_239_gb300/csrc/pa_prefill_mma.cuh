@@ -50,6 +50,13 @@
 // clusters, whose parts a second launch joins (4 tokens over 30,000 keys 30 us; 49 with
 // 64 parts).
 //
+// Trees are often smaller than 64 rows (8 nodes of 4 heads: 32), and the products of two TF32
+// parts take long (fp32).  Row tiles of 16 RG rows leave 4 / RG key groups of warps, each of which takes its
+// own keys of every tile (of twice as many) and is joined to the others at the end, so that all
+// four warps work: 4 trees of 8 nodes with 32 heads on 8 of 128 over 500 - 2,000 keys 31 us for 48,
+// one over 20,000 76 for 134.  (bf16, whose calls wait for their keys, gained 2 % on average from
+// it and does without.)
+//
 // inf * 0 and inf - inf would make NaN of what a row sees as an infinite value, or
 // does not see at all.  Values that are not finite (bf16: in tiles that some row does
 // not see whole) are zeroed in shared memory and remembered by column and position,
@@ -77,7 +84,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int BM = 64, kThreads = 128;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -132,11 +139,13 @@ struct Joined {
 };
 
 // fp32 operands: where the chunks of a row stand, and the two products.
-template <int D>
+template <int D, int RG_ = 4>
 struct CoreF32 {
     using T = float;
-    static constexpr int BN = D == 128 ? 16 : 32;         // keys per tile
-    static constexpr int CTAS = 3;                        // per SM
+    static constexpr int RG = RG_, KG = 4 / RG, BM = 16 * RG;   // row groups, key groups, rows
+    static constexpr int BN = (D == 128 ? 16 : 32) * (KG > 1 ? 2 : 1);  // keys per tile,
+    static constexpr int W = BN / KG;                     // and of them a warp's
+    static constexpr int CTAS = KG > 1 ? 2 : 3;           // per SM
     static constexpr int LQ = D + 16, LV = D + 4;         // row strides (floats) of q and k; v
     static constexpr int QS = 4 * LQ, VS = 4 * LV;        // (bytes)
     static constexpr bool LOOK_ALL = true;                // every tile's V is looked over
@@ -153,12 +162,12 @@ struct CoreF32 {
 
     // S = Q K^T: s[i] the 8 keys from 8 i, this warp's 16 rows.  The small products have a
     // sum of their own: cut off at its last bit they lose 2^-12 of what they lose at s's.
-    static __device__ __forceinline__ void scores(float (&s)[BN / 8][4], const unsigned char* sq,
-                                                  const unsigned char* k, int warp, int lane) {
+    static __device__ __forceinline__ void scores(float (&s)[W / 8][4], const unsigned char* sq,
+                                                  const unsigned char* k, int rg, int lane) {
         const int g = lane >> 2, t = lane & 3;
-        const float* qw = reinterpret_cast<const float*>(sq) + (16 * warp + g) * LQ + 4 * t;
+        const float* qw = reinterpret_cast<const float*>(sq) + (16 * rg + g) * LQ + 4 * t;
         const float* sk = reinterpret_cast<const float*>(k);
-        float small[BN / 8][4] = {};
+        float small[W / 8][4] = {};
 #pragma unroll 4
         for (int d = 0; d < D; d += 16) {
             uint32_t ah[2][4], al[2][4];
@@ -168,9 +177,9 @@ struct CoreF32 {
                 split(x.x, ah[0][h], al[0][h]), split(x.y, ah[0][2 + h], al[0][2 + h]);
                 split(x.z, ah[1][h], al[1][h]), split(x.w, ah[1][2 + h], al[1][2 + h]);
             }
-            uint32_t bh[BN / 8][4], bl[BN / 8][4];
+            uint32_t bh[W / 8][4], bl[W / 8][4];
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i) {
+            for (int i = 0; i < W / 8; ++i) {
                 const float4 x = lds4(sk + (8 * i + g) * LQ + 4 * t + d);
                 split(x.x, bh[i][0], bl[i][0]), split(x.y, bh[i][1], bl[i][1]);
                 split(x.z, bh[i][2], bl[i][2]), split(x.w, bh[i][3], bl[i][3]);
@@ -179,32 +188,32 @@ struct CoreF32 {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int i = 0; i < BN / 8; ++i) mma8(small[i], al[u], bh[i][2 * u], bh[i][2 * u + 1]);
+                for (int i = 0; i < W / 8; ++i) mma8(small[i], al[u], bh[i][2 * u], bh[i][2 * u + 1]);
 #pragma unroll
-                for (int i = 0; i < BN / 8; ++i) mma8(small[i], ah[u], bl[i][2 * u], bl[i][2 * u + 1]);
+                for (int i = 0; i < W / 8; ++i) mma8(small[i], ah[u], bl[i][2 * u], bl[i][2 * u + 1]);
 #pragma unroll
-                for (int i = 0; i < BN / 8; ++i) mma8(s[i], ah[u], bh[i][2 * u], bh[i][2 * u + 1]);
+                for (int i = 0; i < W / 8; ++i) mma8(s[i], ah[u], bh[i][2 * u], bh[i][2 * u + 1]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < BN / 8; ++i)
+        for (int i = 0; i < W / 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[i][k] += small[i][k];
         // x - hi is NaN for an infinite x: scores that are not finite are summed plainly
         float z = 0.f;
 #pragma unroll
-        for (int i = 0; i < BN / 8; ++i)
+        for (int i = 0; i < W / 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) z = fmaf(s[i][k], 0.f, z);
         if (__any_sync(kFullMask, z != 0.f)) {
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i)
+            for (int i = 0; i < W / 8; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
             for (int d = 0; d < D; ++d) {
                 const float q0 = qw[d - 4 * t], q1 = qw[8 * LQ + d - 4 * t];
 #pragma unroll
-                for (int i = 0; i < BN / 8; ++i)
+                for (int i = 0; i < W / 8; ++i)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float x = sk[(8 * i + 2 * t + c) * LQ + d];
@@ -215,13 +224,13 @@ struct CoreF32 {
     }
 
     // O += P V: step i sums over keys 8 i + (2 t, 2 t + 1); the tile's sum starts from zero
-    static __device__ __forceinline__ void values(float (&o)[D / 8][4], const float (&s)[BN / 8][4],
+    static __device__ __forceinline__ void values(float (&o)[D / 8][4], const float (&s)[W / 8][4],
                                                   const unsigned char* v, int lane) {
         const int g = lane >> 2, t = lane & 3;
         const float* sv = reinterpret_cast<const float*>(v);
-        uint32_t ah[BN / 8][4], al[BN / 8][4];
+        uint32_t ah[W / 8][4], al[W / 8][4];
 #pragma unroll
-        for (int i = 0; i < BN / 8; ++i) {
+        for (int i = 0; i < W / 8; ++i) {
             split(s[i][0], ah[i][0], al[i][0]), split(s[i][2], ah[i][1], al[i][1]);
             split(s[i][1], ah[i][2], al[i][2]), split(s[i][3], ah[i][3], al[i][3]);
         }
@@ -229,7 +238,7 @@ struct CoreF32 {
         for (int d = 0; d < D; d += 32) {
             float part[4][4] = {};
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i) {
+            for (int i = 0; i < W / 8; ++i) {
                 const float* v0 = sv + (8 * i + 2 * t) * LV + 4 * g;
                 const float4 x = lds4(v0 + d), y = lds4(v0 + LV + d);
                 const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -255,7 +264,8 @@ struct CoreF32 {
 template <int D>
 struct CoreBf16 {
     using T = __nv_bfloat16;
-    static constexpr int BN = D == 128 ? 32 : 64;
+    static constexpr int RG = 4, KG = 1, BM = 64;
+    static constexpr int BN = D == 128 ? 32 : 64, W = BN;
     static constexpr int CTAS = 3;
     static constexpr int QS = 2 * D, VS = 2 * D;
     static constexpr bool LOOK_ALL = false;
@@ -277,31 +287,31 @@ struct CoreBf16 {
     }
     static __device__ __forceinline__ void clamp(__nv_bfloat16&) {}
 
-    static __device__ __forceinline__ void scores(float (&s)[BN / 8][4], const unsigned char* sq,
-                                                  const unsigned char* k, int warp, int lane) {
+    static __device__ __forceinline__ void scores(float (&s)[W / 8][4], const unsigned char* sq,
+                                                  const unsigned char* k, int rg, int lane) {
         const uint32_t qa = smem_addr(sq), ka = smem_addr(k);
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
             uint32_t a[4];
-            ldmatrix_x4(qa + q_at(16 * warp + (lane & 15), 2 * d + (lane >> 4)), a[0], a[1], a[2], a[3]);
-            uint32_t b[BN / 16][4];  // (all on their way before the first product waits)
+            ldmatrix_x4(qa + q_at(16 * rg + (lane & 15), 2 * d + (lane >> 4)), a[0], a[1], a[2], a[3]);
+            uint32_t b[W / 16][4];  // (all on their way before the first product waits)
 #pragma unroll
-            for (int i = 0; i < BN / 16; ++i)
+            for (int i = 0; i < W / 16; ++i)
                 ldmatrix_x4(ka + q_at(8 * (2 * i + (lane >> 4)) + (lane & 7), 2 * d + ((lane >> 3) & 1)), b[i][0],
                             b[i][1], b[i][2], b[i][3]);
 #pragma unroll
-            for (int i = 0; i < BN / 16; ++i) {
+            for (int i = 0; i < W / 16; ++i) {
                 mma_bf16_16816(s[2 * i], a[0], a[1], a[2], a[3], b[i][0], b[i][1]);
                 mma_bf16_16816(s[2 * i + 1], a[0], a[1], a[2], a[3], b[i][2], b[i][3]);
             }
         }
     }
 
-    static __device__ __forceinline__ void values(float (&o)[D / 8][4], const float (&s)[BN / 8][4],
+    static __device__ __forceinline__ void values(float (&o)[D / 8][4], const float (&s)[W / 8][4],
                                                   const unsigned char* v, int lane) {
         const uint32_t va = smem_addr(v);
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k) {
+        for (int k = 0; k < W / 16; ++k) {
             const uint32_t a[4] = {pack(s[2 * k][0], s[2 * k][1]), pack(s[2 * k][2], s[2 * k][3]),
                                    pack(s[2 * k + 1][0], s[2 * k + 1][1]), pack(s[2 * k + 1][2], s[2 * k + 1][3])};
 #pragma unroll
@@ -329,7 +339,7 @@ template <class C, int D>
 struct Cfg {
     static constexpr int STAGE = C::BN * (C::QS + C::VS);  // k, then v
     static constexpr int LO = D + 4;                       // row stride (floats) of a part of O
-    static constexpr int WORK = BM * C::QS + 2 * STAGE, PART = BM * LO * 4 + BM * 8;
+    static constexpr int WORK = C::BM * C::QS + 2 * STAGE, PART = C::KG * C::BM * (LO * 4 + 8);
     static constexpr int MARKS = WORK > PART ? WORK : PART;  // (the part replaces q and the stages)
     static constexpr int SMEM = MARKS + 3 * D * 4;
 };
@@ -341,13 +351,49 @@ __device__ __forceinline__ void store4(__nv_bfloat16* at, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// The CTA's row tile, by one warp: at[0] its sequence (-1: none), [1] first row, [2] the
+// sequence's first token, [3] new tokens, [4] context.  The last tiles come first, of all KV heads
+// (a prompt's last rows see most: what starts late is short).
+template <int ROWS, int B>
+__device__ __forceinline__ void find_tile(const PrefillParams& p, int lane, int* at) {
+    int left = gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv, found = -1, row0 = 0;
+    for (int b0 = 0; b0 < p.batch && found < 0; b0 += 32) {
+        const int b = b0 + lane;
+        int tiles = 0, s0 = 0, s1 = 0, n = 0;
+        if (b < p.batch) {
+            s0 = ld_dep(p.starts + b), s1 = ld_dep(p.starts + b + 1);
+            n = ld_dep(p.lens + b);
+            const bool good = s0 >= 0 && s1 >= s0 && s1 <= p.num_tokens;
+            if ((!good || n < 0 || n > p.maxb * B) && blockIdx.x == 0 && blockIdx.y == 0)
+                atomicOr(p.status, kStatusBadLength);
+            if (good) tiles = (int)(((long long)(s1 - s0) * p.G + ROWS - 1) / ROWS);
+        }
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned hit = __ballot_sync(kFullMask, left >= incl - tiles && left < incl);
+        if (hit) {
+            const int f = __ffs(hit) - 1;
+            found = b0 + f;
+            row0 = (left - (__shfl_sync(kFullMask, incl, f) - __shfl_sync(kFullMask, tiles, f))) * ROWS;
+            if (lane == f) at[2] = s0, at[3] = s1 - s0, at[4] = n;
+        }
+        left -= __shfl_sync(kFullMask, incl, 31);
+    }
+    if (lane == 0) at[0] = found, at[1] = row0;
+}
+
 template <class C, int D, int B, bool TREE>
 __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
     using T = typename C::T;
     using L = Cfg<C, D>;
-    constexpr int BN = C::BN;
+    constexpr int BN = C::BN, BM = C::BM, KG = C::KG, W = C::W;
+    static_assert(KG == 1 || TREE, "key groups: trees");
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* sq = smem;
     unsigned char* ring = sq + BM * C::QS;
@@ -355,44 +401,16 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
     __shared__ int s_at[5];  // sequence, first row, first token, new tokens, context
     __shared__ int s_odd;    // TREE: a new token's value is not finite
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rg = KG == 1 ? warp : warp % C::RG, kg = KG == 1 ? 0 : warp / C::RG;
     const int g = lane >> 2, t = lane & 3;
     auto token = [&](int row) {  // row / G (the host's multiplier, for rows below 2^31)
         return (int)(((unsigned long long)(unsigned)row * p.div_mul) >> p.div_shift);
     };
 
-    // ---- the tile: sequence and first row; the last tiles first, of all KV heads (a
-    // prompt's last rows see most: what starts late is short) ----
+    // ---- the tile: sequence and first row ----
     const int kvh = blockIdx.x % p.Hkv;
-    if (warp == 0) {
-        int left = gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv, found = -1, row0 = 0;
-        for (int b0 = 0; b0 < p.batch && found < 0; b0 += 32) {
-            const int b = b0 + lane;
-            int tiles = 0, s0 = 0, s1 = 0, n = 0;
-            if (b < p.batch) {
-                s0 = ld_dep(p.starts + b), s1 = ld_dep(p.starts + b + 1);
-                n = ld_dep(p.lens + b);
-                const bool good = s0 >= 0 && s1 >= s0 && s1 <= p.num_tokens;
-                if ((!good || n < 0 || n > p.maxb * B) && blockIdx.x == 0 && blockIdx.y == 0)
-                    atomicOr(p.status, kStatusBadLength);
-                if (good) tiles = (int)(((long long)(s1 - s0) * p.G + BM - 1) / BM);
-            }
-            int incl = tiles;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kFullMask, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const unsigned hit = __ballot_sync(kFullMask, left >= incl - tiles && left < incl);
-            if (hit) {
-                const int f = __ffs(hit) - 1;
-                found = b0 + f;
-                row0 = (left - (__shfl_sync(kFullMask, incl, f) - __shfl_sync(kFullMask, tiles, f))) * BM;
-                if (lane == f) s_at[2] = s0, s_at[3] = s1 - s0, s_at[4] = n;
-            }
-            left -= __shfl_sync(kFullMask, incl, 31);
-        }
-        if (lane == 0) s_at[0] = found, s_at[1] = row0, s_odd = 0;
-    }
+    if (warp == 0) find_tile<BM, B>(p, lane, s_at);
+    if (tid == 0) s_odd = 0;
     for (int x = tid; x < 3 * D; x += kThreads) marks[x] = INT_MAX;
     __syncthreads();
     const int b = s_at[0], row0 = s_at[1];
@@ -467,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int r = 16 * warp + g + 8 * h;
+        const int r = 16 * rg + g + 8 * h;
         if constexpr (TREE) {
             pos[h] = r < rows ? first_pos - 1 : -1;
             mask[h] = p.masks + (r < rows ? (long long)(start + token(row0 + r)) * p.words : 0);
@@ -502,9 +520,11 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
             __syncthreads();
         }
         // (tile kt is in for all, and the other stage has been read)
-        bool there[PAGES], all_there = true;
+        unsigned pages = 0;  // those that are there
 #pragma unroll
-        for (int u = 0; u < PAGES; ++u) there[u] = page[u] >= 0, all_there = all_there && there[u];
+        for (int u = 0; u < PAGES; ++u) pages |= page[u] >= 0 ? 1u << u : 0u;
+        const bool all_there = pages == (1u << PAGES) - 1u;
+        auto there = [&](int key) { return pages >> (BN > B ? (kg * W + key) / B : 0) & 1u; };  // (of the warp's)
         copy(kt + 1);
         if (any_odd) {
             marked = true;
@@ -525,49 +545,50 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
                     }
             __syncthreads();
         }
-        if (16 * warp >= rows) continue;  // (none of the warp's rows are there)
+        if (16 * rg >= rows) continue;  // (none of the warp's rows are there)
 
-        float s[BN / 8][4];
+        float s[W / 8][4];
 #pragma unroll
-        for (int i = 0; i < BN / 8; ++i)
+        for (int i = 0; i < W / 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
-        C::scores(s, sq, sk, warp, lane);
-        // weights: the keys of s[i][2 h + c] are t0 + 8 i + 2 t + c, its row pos[h]
+        C::scores(s, sq, sk + kg * W * C::QS, rg, lane);
+        // weights: the keys of s[i][2 h + c] are k0 + 8 i + 2 t + c, its row pos[h]
+        const int k0 = t0 + kg * W;
 #pragma unroll
-        for (int i = 0; i < BN / 8; ++i)
+        for (int i = 0; i < W / 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[i][k] *= p.qscale;
         if (TREE && partly) {
-            constexpr int W = (BN + 31) / 32;
-            uint32_t vis[2][W];
+            constexpr int WORDS = (W + 31) / 32;
+            uint32_t vis[2][WORDS];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int w = 0; w < W; ++w)
-                    vis[h][w] = 16 * warp + g + 8 * h < rows
-                                    ? tree_bits(mask[h], p.words, t0 + 32 * w - first_pos, n_new)
+                for (int w = 0; w < WORDS; ++w)
+                    vis[h][w] = 16 * rg + g + 8 * h < rows
+                                    ? tree_bits(mask[h], p.words, k0 + 32 * w - first_pos, n_new)
                                     : 0u;
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i)
+            for (int i = 0; i < W / 8; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (!(vis[k >> 1][8 * i / 32] >> ((8 * i + 2 * t + (k & 1)) & 31) & 1u) ||
-                        !there[BN > B ? 8 * i / B : 0])
+                        !there(8 * i))
                         s[i][k] = -INFINITY;
         } else if (partly || !all_there) {
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i)
+            for (int i = 0; i < W / 8; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (t0 + 8 * i + 2 * t + (k & 1) > pos[k >> 1] || !there[BN > B ? 8 * i / B : 0])
+                    if (k0 + 8 * i + 2 * t + (k & 1) > pos[k >> 1] || !there(8 * i))
                         s[i][k] = -INFINITY;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float mt = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i) mt = fmaxf(mt, fmaxf(s[i][2 * h], s[i][2 * h + 1]));
+            for (int i = 0; i < W / 8; ++i) mt = fmaxf(mt, fmaxf(s[i][2 * h], s[i][2 * h + 1]));
             mt = fmaxf(mt, __shfl_xor_sync(kFullMask, mt, 1));
             mt = fmaxf(mt, __shfl_xor_sync(kFullMask, mt, 2));
             const float mn = fmaxf(fmaxf(m[h], mt), -3.0e38f);  // finite: a row may see no key
@@ -575,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
             m[h] = mn;
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < BN / 8; ++i)
+            for (int i = 0; i < W / 8; ++i)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float& x = s[i][2 * h + c];
@@ -587,38 +608,71 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) o[i][2 * h] *= alpha, o[i][2 * h + 1] *= alpha;
         }
-        C::values(o, s, sv, lane);
+        C::values(o, s, sv + kg * W * C::VS, lane);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the marks; and q and the stages are free
     float* part = reinterpret_cast<float*>(smem);  // this CTA's part of O
-    float2* part_ml = reinterpret_cast<float2*>(part + BM * L::LO);
+    float2* part_ml = reinterpret_cast<float2*>(part + KG * BM * L::LO);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         l[h] += __shfl_xor_sync(kFullMask, l[h], 1);
         l[h] += __shfl_xor_sync(kFullMask, l[h], 2);
-        const int r = 16 * warp + g + 8 * h;  // (rows that are not there: into their own places)
+        const int r = 16 * rg + g + 8 * h;  // (rows that are not there: into their own places)
+        float* row = part + (kg * BM + r) * L::LO;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) part[r * L::LO + C::column(i, c, t)] = o[i][2 * h + c];
-        if (marked) {
+            for (int c = 0; c < 2; ++c) row[C::column(i, c, t)] = o[i][2 * h + c];
+        if (KG == 1 && marked) {
             __syncwarp();  // (column t of all, by the four threads of the row)
             for (int col = t; col < D; col += 4) {
                 const bool nan = marks[col] <= pos[h], up = marks[D + col] <= pos[h],
                            down = marks[2 * D + col] <= pos[h];
                 if (nan || up || down)
-                    part[r * L::LO + col] = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+                    row[col] = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
             }
         }
-        if (TREE && s_odd) {
+        if (TREE && KG == 1 && s_odd) {
             __syncwarp();  // (column t of all, by the four threads of the row)
             if (r < rows)
                 tree_odd_values<T, D>(vb - E * cc, p.s_blk, p.num_blocks, p.bt + (long long)b * p.maxb, mask[h],
                                       first_pos, n_new, B, kt0 * BN, kt1 * BN, t, 4, D,
-                                      [row = part + r * L::LO](int col, float v) { row[col] += v; });
+                                      [row](int col, float v) { row[col] += v; });
         }
-        if (t == 0) part_ml[r] = make_float2(m[h], l[h]);
+        if (t == 0) part_ml[kg * BM + r] = make_float2(m[h], l[h]);
+    }
+    constexpr int LPR = D / 4, ROWS = kThreads / LPR;  // lanes per row, rows per pass
+    const int c4 = tid % LPR;
+    if constexpr (KG > 1) {
+        // the key groups' parts, and what is not finite
+        __syncthreads();
+        for (int x0 = 0; x0 < rows; x0 += ROWS) {
+            const int x = x0 + tid / LPR;
+            const bool live = x < rows;
+            Joined j;
+            if (live) {
+#pragma unroll
+                for (int k = 0; k < KG; ++k)
+                    j.add(part_ml[k * BM + x], lds4(part + (k * BM + x) * L::LO + 4 * c4));
+                float v[4] = {j.o.x, j.o.y, j.o.z, j.o.w};
+                if (marked)
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = 4 * c4 + c;
+                        const bool nan = marks[col] < first_pos, up = marks[D + col] < first_pos,
+                                   down = marks[2 * D + col] < first_pos;
+                        if (nan || up || down) v[c] = nan || (up && down) ? NAN : up ? INFINITY : -INFINITY;
+                    }
+                if (s_odd)
+                    tree_odd_values<T, D>(vb - E * cc + 4 * c4, p.s_blk, p.num_blocks, p.bt + (long long)b * p.maxb,
+                                          p.masks + (long long)(start + token(row0 + x)) * p.words, first_pos, n_new, B,
+                                          kt0 * BN, kt1 * BN, 0, 1, 4, [&v](int c, float y) { v[c] += y; });
+                j.o = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            __syncwarp();  // (all of the row's lanes have read its sums)
+            if (live) store4(part + x * L::LO + 4 * c4, j.o);
+            if (live && c4 == 0) part_ml[x] = make_float2(j.m, j.l);
+        }
     }
 
     // ---- the cluster's parts: each CTA joins its share of the rows ----
@@ -629,8 +683,6 @@ __global__ void __launch_bounds__(kThreads, C::CTAS) pa_prefill_mma_kernel(const
         __syncthreads();
     const int rank = p.cluster > 1 ? (int)cluster.block_rank() : 0;
     const int groups = p.splits / p.cluster;
-    constexpr int LPR = D / 4, ROWS = kThreads / LPR;  // lanes per row, rows per pass
-    const int c4 = tid % LPR;
     for (int x = rank * ROWS + tid / LPR; x < rows; x += p.cluster * ROWS) {
         const int f = row0 + x, tok = token(f);
         const long long orow = (long long)(start + tok) * p.H + kvh * p.G + f - tok * p.G;
@@ -696,7 +748,7 @@ cudaError_t launch_mma_inst(const PrefillParams& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Cfg<C, D>::SMEM);
     if (e != cudaSuccess) return e;
-    const long long ctas = ((long long)p.num_tokens * p.G / BM + p.batch) * p.Hkv;
+    const long long ctas = ((long long)p.num_tokens * p.G / C::BM + p.batch) * p.Hkv;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, p.splits);
@@ -717,22 +769,6 @@ cudaError_t launch_mma_inst(const PrefillParams& p, cudaStream_t s) {
     constexpr int RPC = kJoinThreads / (D / 4);
     return launch_pdl(pa_prefill_mma_join_kernel<typename C::T, D, TREE>, dim3((unsigned)((rows + RPC - 1) / RPC)),
                       dim3(kJoinThreads), 0, s, p);
-}
-
-template <bool TREE>
-cudaError_t launch_mma(const PrefillParams& p, int dtype, int D, int B, cudaStream_t s) {
-    if (dtype == 1) {
-        if (D == 64 && B == 16) return launch_mma_inst<CoreBf16<64>, 64, 16, TREE>(p, s);
-        if (D == 64 && B == 32) return launch_mma_inst<CoreBf16<64>, 64, 32, TREE>(p, s);
-        if (D == 128 && B == 16) return launch_mma_inst<CoreBf16<128>, 128, 16, TREE>(p, s);
-        if (D == 128 && B == 32) return launch_mma_inst<CoreBf16<128>, 128, 32, TREE>(p, s);
-    } else {
-        if (D == 64 && B == 16) return launch_mma_inst<CoreF32<64>, 64, 16, TREE>(p, s);
-        if (D == 64 && B == 32) return launch_mma_inst<CoreF32<64>, 64, 32, TREE>(p, s);
-        if (D == 128 && B == 16) return launch_mma_inst<CoreF32<128>, 128, 16, TREE>(p, s);
-        if (D == 128 && B == 32) return launch_mma_inst<CoreF32<128>, 128, 32, TREE>(p, s);
-    }
-    return cudaErrorNotSupported;
 }
 
 }  // namespace

@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(384, 1)
             int* blocks = reinterpret_cast<int*>(ctrl + C::BLOCKS) + 8 * kv;
             int seq = kv;  // the next stage of the ring (K the even, V the odd ones)
             bool aborted = false;
-            const uint64_t pol = l2_policy_evict_normal();
+            const uint64_t pol_normal = l2_policy_evict_normal(), pol_first = l2_policy_evict_first();
             if (kv == 0 && lane == 0 && p.cut != nullptr)
                 p.cut[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);  // (no cut pair yet)
             PfWalk w;
@@ -743,6 +743,9 @@ __global__ void __launch_bounds__(384, 1)
                                : -1;
                 };
                 int blk_next = box_block(pc.kt0);
+                // (a tree's keys are read once, unless it has several pairs; 32 trees of 16 nodes: 63.6
+                // us for 67.0)
+                const uint64_t pol = TREE && pc.rows <= C::ROWS ? pol_first : pol_normal;
 #pragma unroll 1
                 for (int kt = pc.kt0; kt < pc.kt1; ++kt, seq += 2) {
                     const int tok = kt * C::TT + 16 * lane;
