@@ -1329,28 +1329,44 @@ struct PfJoin {
         for (int k = 0; k < 8; ++k) o[k] = fmaf(o[k], keep, w * x[k]);
     }
 };
-template <int D, bool TREE>  // (TREE: a name of its own in either unit)
-__global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const PrefillParams p) {
+template <int D, bool TREE, int W = 8>  // W warps (TREE: a name of its own in either unit)
+__global__ void __launch_bounds__(32 * W) pa_prefill_umma_join_kernel(const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
-    __shared__ float s_part[8][10][32];  // per warp: columns, maximum and sum of 32 rows
+    __shared__ float s_part[W][10][32];  // per warp: columns, maximum and sum of 32 rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int4 a = ld_dep(p.cut + 2 * blockIdx.x);
-    const int4 e = ld_dep(p.cut + 2 * blockIdx.x + 1);
+    int main_cta = blockIdx.x;
+    if (TREE && gridDim.x < p.grid) {  // the blockIdx.x-th of the CTAs that recorded a cut pair
+        constexpr int K = 5;  // 32 CTAs at a time
+        int pieces[K], left = blockIdx.x;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            pieces[k] = 32 * k + lane < p.grid ? ld_dep(&p.cut[2 * (32 * k + lane) + 1].x) : 0;
+        main_cta = -1;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const unsigned cuts = __ballot_sync(kFullMask, pieces[k] > 1);
+            if (left >= 0 && left < __popc(cuts)) main_cta = 32 * k + __fns(cuts, 0, left + 1);
+            left -= __popc(cuts);
+        }
+        if (main_cta < 0) return;
+    }
+    const int4 a = ld_dep(p.cut + 2 * main_cta);
+    const int4 e = ld_dep(p.cut + 2 * main_cta + 1);
     const int pieces = e.x, rows = min(256, e.z - a.z);
     if (pieces <= 1) return;
-    const int units = (rows + 31) / 32 * (D / 8);
+    const int units = (rows + 31) / 32 * (D / 8), warps = W * gridDim.y;
     int ways = 1;  // warps to a unit; above 1 there is a warp for each
     if (pieces > 4)
-        while (ways < 8 && 2 * ways * units <= kJoinParts * 8) ways *= 2;
+        while (ways < 8 && 2 * ways * units <= warps) ways *= 2;
     const int way = warp % ways;
-    for (int u = (blockIdx.y * 8 + warp) / ways; u < units || ways > 1; u += kJoinParts * 8) {
+    for (int u = (blockIdx.y * W + warp) / ways; u < units || ways > 1; u += warps) {
         const int r = u / (D / 8) * 32 + lane, d = u % (D / 8) * 8;
         // (rows of part k: CTA x + k's first slot, but for k = 0)
-        const long long row0 = (long long)blockIdx.x * 512 + 256 * e.y + r;
-        auto row = [&](int k) { return k == 0 ? row0 : (long long)(blockIdx.x + k) * 512 + r; };
+        const long long row0 = (long long)main_cta * 512 + 256 * e.y + r;
+        auto row = [&](int k) { return k == 0 ? row0 : (long long)(main_cta + k) * 512 + r; };
         PfJoin j;
-        for (int k0 = way; k0 < pieces && r < rows; k0 += 4 * ways) {
+        for (int k0 = way; k0 < pieces && r < rows && u < units; k0 += 4 * ways) {
             float2 ml[4];
             float x[4][8];
 #pragma unroll
@@ -1379,7 +1395,7 @@ __global__ void __launch_bounds__(256) pa_prefill_umma_join_kernel(const Prefill
                 j.add(make_float2(s_part[w][8][lane], s_part[w][9][lane]), x);
             }
         }
-        if (r < rows) {
+        if (r < rows && u < units) {
             const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
             const int f = a.z + r, tok = pf_div(p, f);
             const long long orow = (long long)(a.w + tok) * p.H + a.y * p.G + (f - tok * p.G);

@@ -38,6 +38,17 @@ cudaError_t launch_turns(const PrefillParams& p, const CUtensorMap* tm, cudaStre
     }
     e = launch_pdl(kern, dim3((unsigned)p.grid), dim3(C::THREADS), C::SMEM_BYTES, s, p, tm[0], tm[1], tq);
     if (e != cudaSuccess || p.grid == 1) return e;
+    if constexpr (TREE) {
+        // One tree or two: a few pairs, each cut in many parts.  CTAs that look up which pairs those
+        // are, and more of them to each (8 pairs in 16 - 19 parts, trees of 64 / 32 / 8 nodes of
+        // 4 heads: 17.5 / 15.3 / 14.2 us for the call, 22.2 / 17.5 / 14.7 with eight for each
+        // main CTA; from 16 pairs on there is no gain).
+        const long long rows = (long long)p.num_tokens * p.G;
+        const long long pairs = (rows / 256 + p.batch) * p.Hkv;  // (at most)
+        if ((rows > 256LL * p.batch ? rows / 256 : p.batch) * p.Hkv * 16 <= p.grid && p.grid <= 160)
+            return launch_pdl(pa_prefill_umma_join_kernel<D, TREE, 16>,
+                              dim3((unsigned)pairs, rows >= 128LL * p.batch ? 16 : 8), dim3(512), 0, s, p);
+    }
     return launch_pdl(pa_prefill_umma_join_kernel<D, TREE>, dim3((unsigned)p.grid, kJoinParts),
                       dim3(256), 0, s, p);
 }
