@@ -769,7 +769,7 @@ PA_API int pa_compact_workspace_size(const pa_pool* pool, size_t* bytes);
  *                 sequence's new tokens, -1 for a root; NULL: each token follows the one
  *                 before it.  A parent that is not below its child sets
  *                 PA_STATUS_BAD_LENGTH and counts as -1.
- *   num_tokens    rows of the batch, at least the sum of the counts.
+ *   num_tokens    rows of the batch, at least the sum of the counts, at most 2^30.
  *   context_lens  [batch]: cached_lens[b] + n_b.
  *   query_starts  [batch + 1]: the prefix sums of n_b.
  *   slots         int64 [num_tokens], 8-byte aligned: page * block_size + row, -1 behind
@@ -805,6 +805,7 @@ PA_API int pa_device_plan_tokens(pa_pool* pool, void* dev_stack, int* block_tabl
  * The pages must have one owner each.  new_lens[b] outside [0, context_lens[b]] or a length
  * past the table sets PA_STATUS_BAD_LENGTH and the row stays; ids outside the pool are
  * skipped (PA_STATUS_BAD_BLOCK_ID).
+ * batch * max_blocks_per_seq <= 2^30.
  * Cites: mini-infer, "Python Implementation: Physical Block Pool" (free_block, once per block
  * that is no longer needed).
  */

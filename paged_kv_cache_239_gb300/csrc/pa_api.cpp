@@ -1382,7 +1382,8 @@ int pa_device_plan_tokens(pa_pool* pool, void* dev_stack, int* block_tables,
     if (int rc = check_pool(pool)) return rc;
     if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, cached_lens, batch))
         return rc;
-    if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+    if (num_tokens < 0 || num_tokens > 1 << 30)
+        return fail(PA_ERR_INVALID_ARG, "num_tokens %d outside [0, 2^30]", num_tokens);
     if (tree_masks && (mask_words < 1 || mask_words > pa::kMaxTreeWords))
         return fail(PA_ERR_INVALID_ARG, "mask_words %d outside [1, %d]", mask_words, pa::kMaxTreeWords);
     if (!query_starts || !aligned(query_starts, 4) || !aligned(tree_masks, 4) || !aligned(parents, 4))
@@ -1436,6 +1437,8 @@ int pa_device_trim_sequences(pa_pool* pool, void* dev_stack, int* block_tables,
     if (int rc = check_pool(pool)) return rc;
     if (int rc = check_tables(block_tables, max_blocks_per_seq, pool->g.B, context_lens, batch))
         return rc;
+    if ((long long)batch * max_blocks_per_seq > 1 << 30)
+        return fail(PA_ERR_INVALID_ARG, "batch * max_blocks_per_seq is above 2^30");
     if (batch == 0) return PA_OK;
     if (int rc = check_stack(dev_stack)) return rc;
     if (!new_lens || !aligned(new_lens, 4))

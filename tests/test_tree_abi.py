@@ -31,7 +31,7 @@ PLAN = dict(dev_stack=P, block_tables=P + MB, max_blocks_per_seq=4, cached_lens=
 
 @pytest.mark.parametrize("change", [
     dict(batch=-1), dict(num_tokens=-1), dict(max_blocks_per_seq=0), dict(max_blocks_per_seq=1 << 28), dict(mask_words=0),
-    dict(mask_words=33), dict(dev_stack=None), dict(dev_stack=P + 2), dict(block_tables=None), dict(cached_lens=None),
+    dict(num_tokens=(1 << 30) + 1), dict(mask_words=33), dict(dev_stack=None), dict(dev_stack=P + 2), dict(block_tables=None), dict(cached_lens=None),
     dict(new_counts=None), dict(context_lens=None), dict(query_starts=None), dict(slots=None), dict(positions=None),
     dict(slots=P + 7 * MB + 4), dict(positions=P + 8 * MB + 1), dict(tree_masks=P + 9 * MB + 2), dict(parents=P + 2),
     # an output over an input, or over another
@@ -47,7 +47,8 @@ TRIM = dict(dev_stack=P, block_tables=P + MB, max_blocks_per_seq=4, context_lens
 
 
 @pytest.mark.parametrize("change", [dict(batch=-1), dict(max_blocks_per_seq=0), dict(dev_stack=None), dict(block_tables=None),
-                                    dict(context_lens=None), dict(new_lens=None), dict(new_lens=P + 2)])
+                                    dict(context_lens=None), dict(new_lens=None), dict(new_lens=P + 2),
+                                    dict(batch=16, max_blocks_per_seq=(1 << 26) + 1)])
 def test_trim_refusals(pa_lib, pool, change):
     refused(pa_lib, pa_lib.PA_ERR_INVALID_ARG, lambda: pa_lib.pa_device_trim_sequences(pool, **{**TRIM, **change}, stream=0))
     pa_lib.pa_device_trim_sequences(pool, **{**TRIM, "batch": 0}, stream=0)   # (nothing to do)
