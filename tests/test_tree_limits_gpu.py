@@ -297,6 +297,41 @@ def test_calls_need_the_current_device(cuda_device, monkeypatch):
         cache.device_trim_sequences(stack_tensor([], 4, dev), bt, lens, lens)
 
 
+@pytest.mark.parametrize("batch,most,shape,words,pad", [
+    (1, 1024, "chain", 32, 0), (1, 5000, "chain", 0, 3), (2, 6000, "random", 0, 0), (60, 1024, "chain", 32, 11), (130, 700, "random", 32, 0),
+    (1100, 64, "random", 2, 5), (2000, 40, "chain", 2, 30000), (9000, 9, "wide", 1, 0), (3, 0, "chain", 1, 20),
+])
+def test_plan_of_many_tokens(cuda_device, batch, most, shape, words, pad):
+    """Long chains, trees longer than a mask (no masks written), more rows than a round of the
+    launch takes, rows behind the last sequence that take rounds of their own."""
+    dev, block = cuda_device, 16
+    new, cached, trees, tables, ids, nb = plan_case(np.random.default_rng(batch + most), batch, most, block, shape)
+    if batch <= 2:
+        new = [most] * batch
+        trees = [T.random_tree(np.random.default_rng(b), most, shape) for b in range(batch)]
+        cached = [0, 37][:batch]
+        tables = np.full((batch, R.cdiv(most + 37, block)), -1, np.int32)
+        nb = 2 * tables.size + 9
+        ids = [int(x) for x in np.random.default_rng(1).permutation(nb)]
+        if batch == 2:
+            tables[1, :3] = [ids.pop() for _ in range(3)]
+    total = sum(new) + pad
+    want = T.Plan(block, tables, ids, cached, new, trees, total, words)
+    cache = small_pool(nb, block, dev)
+    stack, bt = stack_tensor(ids, nb, dev), ints(tables, dev)
+    lens, starts, slots, positions, masks = cache.device_plan_tokens(
+        stack, bt, ints(cached, dev), ints(new, dev), total, parents=ints([x for t in trees for x in t] + [5] * pad, dev),
+        mask_words=words)
+    status_is(0)
+    assert lens.tolist() == want.lens and starts.tolist() == want.starts
+    assert slots.tolist() == want.slots and positions.tolist() == want.positions
+    assert not words or np.array_equal(masks.cpu().numpy(), want.masks)
+    assert np.array_equal(bt.cpu().numpy(), want.tables) and stack_ids(stack) == want.stack
+    cache.device_trim_sequences(stack, bt, lens, ints(cached, dev))
+    assert np.array_equal(bt.cpu().numpy(), tables) and stack_ids(stack) == ids
+    status_is(0)
+
+
 def test_trim_frees_what_a_prompt_took(cuda_device):
     """Thousands of pages in one call, and rows of bad ids between good ones."""
     dev, block = cuda_device, 16
