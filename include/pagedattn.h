@@ -639,14 +639,16 @@ PA_API int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int 
 PA_API int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens, int num_heads,
                                   int max_blocks_per_seq, size_t* bytes);
 
-/* Which kernel a pool's prefill attention uses.  PA_PREFILL_AUTO (default): fp32
+/* Which kernel a pool's prefill and tree attention use.  PA_PREFILL_AUTO (default): fp32
  * pools mma.sync (TF32 products of split operands); bf16 pools mma.sync for calls
  * that its short start makes faster, by an estimate from the sizes, else tcgen05.
  * The lengths are on the device: the estimate, and how an fp32 or mma.sync call is
  * split, take every context to be as long as the table is wide.  With a table much
  * wider than the contexts of a short call, force PA_PREFILL_MMA (one token over 100
  * keys, 16 heads on 2 of 64: 5.0 us in a table of 7 blocks; in one of 8,192 11.1 by
- * choice, 8.2 by force).
+ * choice, 8.2 by force; a tree of 8 nodes over 500 6.5 and 10.2, 8.8 by force).  On fp32
+ * pools only a tighter table helps: 8 trees of 25 nodes over 2,000 keys, 32 heads on 8 of
+ * 128, 211 us in a table of 126 blocks, 301 in one of 8,192.
  * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at the call.
  * The workspace size follows the choice.
  * Cites: no counterpart on the pages (a choice among this library's kernels). */
