@@ -621,7 +621,8 @@ PA_API int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, i
  *                 n_b on are not used.  A row that sees nothing is zero.
  *   mask_words    1 .. 32.  A sequence of more than 32 * mask_words new tokens sets
  *                 PA_STATUS_BAD_LENGTH and its output rows are zero.
- * The other arguments, the products' rounding, bad entries and the choice of the kernel
+ * The other arguments, the products' rounding (fp32: in two TF32 or three bf16 parts, off by
+ * 2^-22 at most either way), bad entries and the choice of the kernel
  * (pa_pool_set_prefill_kernel) as there; the workspace is pa_tree_workspace_size().  What
  * lies in the cache at positions that a row does not see, be it NaN, does not reach it.
  * Cites: as pa_prefill_attention.
@@ -639,8 +640,9 @@ PA_API int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int 
 PA_API int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens, int num_heads,
                                   int max_blocks_per_seq, size_t* bytes);
 
-/* Which kernel a pool's prefill and tree attention use.  PA_PREFILL_AUTO (default): fp32
- * pools mma.sync (TF32 products of split operands); bf16 pools mma.sync for calls
+/* Which kernel a pool's prefill and tree attention use.  PA_PREFILL_AUTO (default): prefill
+ * on fp32 pools mma.sync (TF32 products of split operands); bf16 pools, and trees on
+ * fp32 ones (bf16 products of operands in three parts), mma.sync for calls
  * that its short start makes faster, by an estimate from the sizes, else tcgen05.
  * The lengths are on the device: the estimate, and how an fp32 or mma.sync call is
  * split, take every context to be as long as the table is wide.  With a table much
@@ -649,7 +651,7 @@ PA_API int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens
  * choice, 8.2 by force; a tree of 8 nodes over 500 6.5 and 10.2, 8.8 by force).  On fp32
  * pools only a tighter table helps: 8 trees of 25 nodes over 2,000 keys, 32 heads on 8 of
  * 128, 211 us in a table of 126 blocks, 301 in one of 8,192.
- * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at the call.
+ * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at a prefill call.
  * The workspace size follows the choice.
  * Cites: no counterpart on the pages (a choice among this library's kernels). */
 enum {

@@ -31,6 +31,7 @@ SOURCES = ["pa_api.cpp", "pa_aux.cu", "pa_decode_bf16.cu", "pa_decode_f32.cu",
            "pa_decode_mma_wide.cu", "pa_decode_umma.cu", "pa_rope.cu",
            "pa_prefill_mma.cu", "pa_prefill_umma.cu", "pa_pages.cu", "pa_plan.cu",
            "pa_tree_mma.cu", "pa_tree_mma_bf16.cu", "pa_tree_mma_f32.cu", "pa_tree_umma.cu",
+           "pa_tree_umma_f32.cu",
            "pa_accept.cu"]
 
 

@@ -946,7 +946,7 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
         std::lock_guard<std::mutex> lock(pool->mu);
         kind = pool->prefill_kernel;
     }
-    if (g.dtype != 1 && kind == PA_PREFILL_TCGEN05)
+    if (g.dtype != 1 && !tree && kind == PA_PREFILL_TCGEN05)
         return fail(PA_ERR_UNSUPPORTED, "the tcgen05 prefill kernel serves bf16 pools");
     *sh = PrefillShape();
     if (batch == 0 || num_tokens == 0) return PA_OK;
@@ -958,10 +958,15 @@ int prefill_shape(const pa_pool* pool, int batch, int num_tokens, int num_heads,
     if (tree) {
         here = pa::tree_mma_plan(g.dtype, G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms, &sh->row_tile,
                                  &sh->splits, &sh->cluster);
-        there = pa::tree_umma_time(G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms);
+        int parts = 1;
+        there = g.dtype == 1 ? pa::tree_umma_time(G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms)
+                             : pa::tree_umma_f32_plan(G, g.Hkv, batch, num_tokens, maxb, g.D, g.B, sms, &parts);
+        if (g.dtype == 0 && (kind == PA_PREFILL_TCGEN05 || (kind == PA_PREFILL_AUTO && there < here)))
+            sh->row_tile = 128, sh->splits = parts, sh->cluster = 1;
     }
-    const bool mma = kind != PA_PREFILL_AUTO ? kind == PA_PREFILL_MMA
-                     : g.dtype == 0         ? true
+    // (fp32 trees on tcgen05 are split and joined as on mma.sync)
+    const bool mma = g.dtype == 0           ? true
+                     : kind != PA_PREFILL_AUTO ? kind == PA_PREFILL_MMA
                      : tree                 ? here < there
                                             : pa::prefill_mma_preferred(G, g.Hkv, batch, num_tokens, maxb, g.D,
                                                                         g.B, sms);
@@ -1125,6 +1130,7 @@ int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const i
         p.row_tile = sh.row_tile;
         e = !tree_masks      ? pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s)
             : g.dtype == 1 ? pa::launch_tree_mma_bf16(p, g.D, g.B, s)
+            : p.row_tile == 128 ? pa::launch_tree_umma_f32(p, g.D, g.B, s)
                            : pa::launch_tree_mma_f32(p, g.D, g.B, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");

@@ -153,7 +153,7 @@ struct PrefillParams {
     int div_shift;
     const unsigned* masks;   // trees: [num_tokens, words], see pa_tree_mask.cuh
     int words;
-    int row_tile;            // trees on mma.sync, fp32: rows of a tile
+    int row_tile;            // trees on fp32 pools: rows of a tile (128: tcgen05)
 };
 
 // New tokens: pages, slots, positions and masks; and pages given back (see pa_plan.cu).
@@ -240,6 +240,8 @@ cudaError_t launch_tree_mma_f32(const PrefillParams& p, int D, int B, cudaStream
 double tree_mma_plan(int dtype, int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B,
                      int num_sms, int* row_tile, int* splits, int* cluster);
 double tree_umma_time(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B, int num_sms);
+double tree_umma_f32_plan(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B, int num_sms, int* splits);
+cudaError_t launch_tree_umma_f32(const PrefillParams& p, int D, int B, cudaStream_t s);
 cudaError_t launch_tree_umma(const PrefillParams& p, const void* tmaps, int D, int B, cudaStream_t s);
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t s);

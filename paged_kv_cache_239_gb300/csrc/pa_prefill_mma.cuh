@@ -54,7 +54,7 @@
 // parts take long (fp32).  Row tiles of 16 RG rows leave 4 / RG key groups of warps, each of which takes its
 // own keys of every tile (of twice as many) and is joined to the others at the end, so that all
 // four warps work: 4 trees of 8 nodes with 32 heads on 8 of 128 over 500 - 2,000 keys 31 us for 48,
-// one over 20,000 76 for 134.  (bf16, whose calls wait for their keys, gained 2 % on average from
+// one over 20,000 76 for 134.  (Calls of many rows take pa_tree_umma_f32.cu.  bf16, whose calls wait for their keys, gained 2 % on average from
 // it and does without.)
 //
 // inf * 0 and inf - inf would make NaN of what a row sees as an infinite value, or

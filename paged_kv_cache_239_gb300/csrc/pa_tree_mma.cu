@@ -1,4 +1,4 @@
-// Attention of drafted trees on mma.sync: when a call takes it, and how it is split.
+// Attention of drafted trees: which kernel a call takes, and how it is split.
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -51,6 +51,29 @@ double tree_umma_time(int G, int Hkv, int batch, int num_tokens, int maxb, int D
     const double parts = std::min(keys / 128 + 1, std::max(1.0, num_sms / pairs));
     return 9.4 + pairs * (5.6 + keys / 128) / num_sms * (D == 64 ? 0.86 : 1.18) +
            parts * std::min(256.0, std::max(32.0, rows)) * D * 2.7e-5;
+}
+
+// The same for the tcgen05 kernel on fp32 pools (one CTA per SM): start, the join of n parts by
+// their bytes, the key tiles of a part and k0 more, times the rounds that the SMs take: beyond one, at
+// least 1.7, for a few CTAs more than there are SMs wait for the others to end.  Least squares over 62
+// calls at 1 to 64 parts; the better of this and mma.sync by estimate takes 2.5 % more than the best
+// (mma.sync for all: 22 %).
+double tree_umma_f32_plan(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B, int num_sms,
+                          int* splits) {
+    struct Time {
+        double start, join, bytes, k0, tile, rest;
+    };
+    const Time t = D == 64 ? Time{2.25, 1.91, 3.39, 2.66, 1.55, 0.44} : Time{4.93, 1.00, 2.38, 1.70, 2.43, 0.45};
+    const double rows = (double)num_tokens * G / batch, keys = (double)maxb * B / 64;
+    const double tiles = (double)batch * Hkv * std::max(1.0, rows / 128 + 0.3);
+    const double out = 1e-6 * num_tokens * G * Hkv * D;
+    double best = 0;
+    for (int n = 1; n <= 64 && (n == 1 || n <= keys); ++n) {
+        const double x = tiles * n / num_sms, rounds = x > 1 ? std::max(x + t.rest, 1.7) : 1.0;
+        const double time = t.start + (n > 1 ? t.join + t.bytes * n * out : 0) + rounds * (keys / n + t.k0) * t.tile;
+        if (n == 1 || time < best) best = time, *splits = n;
+    }
+    return best;
 }
 
 }  // namespace pa

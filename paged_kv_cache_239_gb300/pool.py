@@ -209,7 +209,7 @@ class BlockPool:
         return out
 
     def set_prefill_kernel(self, kind: str) -> None:
-        """'auto' (default), 'mma' or 'tcgen05' (bf16 pools)."""
+        """'auto' (default), 'mma' or 'tcgen05' (bf16 pools; on fp32 ones for trees)."""
         B.pa_pool_set_prefill_kernel(self.handle, _PREFILL_KERNELS[kind])
 
     def prefill_workspace_size(self, batch: int, num_tokens: int, num_heads: int,

@@ -112,6 +112,77 @@ def test_tree_large_scores(cuda_device, dtype, kernel):
     check(out, want, bound)
 
 
+@pytest.mark.parametrize("kernel", ["mma", "tcgen05"])
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 32)])
+def test_tree_f32_infinite_keys_and_queries(cuda_device, kernel, d, block):
+    """A key's infinite component: no weight in rows whose query is negative there (the score is
+    -inf), nothing finite in the others; a query's: nothing finite in its row."""
+    dev, h, hkv, n, ctx = cuda_device, 2, 2, 20, 300
+    tree = T.random_tree(np.random.default_rng(4), n)
+    c = tree_case(5, [n], [ctx], d, block, h, hkv, torch.float32, dev)
+    bits = T.ancestors(tree)
+    for at, value in ((77, float("inf")), (ctx - n + 3, float("inf")), (200, -float("inf"))):
+        c["pool"][int(c["tables"][0, at // block]), 0, 0, :, at % block, 9] = value
+    bt = c["bt"]
+    q = c["q"].clone()
+    q[:, :, 9] = -q[:, :, 9].abs()
+    q[::3, :, 9] *= -1
+    q[10, 0, 4] = float("inf")
+    cache = BlockPool(c["nb"], block, 1, hkv, d, tensor=c["pool"])
+    cache.set_prefill_kernel(kernel)
+    out = cache.tree_attention(q, 0, bt, c["lens"], c["starts"], ints(T.mask_words(bits, 1), dev), d ** -0.5)
+    status_is(0)
+    # key 200 is infinite in the rows whose queries are negative: those of the others are left
+    for i in range(n):
+        assert not bool(torch.isfinite(out[i]).any()) if i % 3 else True
+    # without key 200 the negative rows lose the infinite keys only
+    c["pool"][int(c["tables"][0, 200 // block]), 0, 0, :, 200 % block, 9] = 0.5
+    out = cache.tree_attention(q, 0, bt, c["lens"], c["starts"], ints(T.mask_words(bits, 1), dev), d ** -0.5)
+    status_is(0)
+    plain = c["pool"].clone()
+    plain[int(c["tables"][0, 77 // block]), 0, 0, :, 77 % block] = 0.0
+    plain[int(c["tables"][0, 77 // block]), 1, 0, :, 77 % block] = 0.0
+    at = ctx - n + 3
+    plain[int(c["tables"][0, at // block]), 0, 0, :, at % block, 9] = 0.0
+    for i in range(n):
+        if i % 3 == 0 or i == 10:
+            assert not bool(torch.isfinite(out[i, 0]).any()), i
+            continue
+        # the row by itself: the keys it sees that are finite, in 64 bits
+        keys = [j for j in range(ctx - n) if j != 77] + [ctx - n + j for j in range(n) if bits[i] >> j & 1 and j != 3]
+        kv = torch.stack([plain[int(c["tables"][0, j // block]), :, 0, :, j % block] for j in keys]).double()
+        for head in range(h):
+            s = kv[:, 0, head] @ q[i, head].double() * d ** -0.5
+            want = torch.softmax(s, 0) @ kv[:, 1, head]
+            # a product off by 2^-22, sums of d and of 300 terms off by 2^-24 each time, exponentials by 2^-22
+            size = (kv[:, 0, head].abs() @ q[i, head].double().abs()).max() * d ** -0.5
+            tol = (2.0 ** -21 * (1 + size) * (1 + d / 4) + 300 * 2.0 ** -24) * kv[:, 1, head].abs().max()
+            assert float((out[i, head].double() - want).abs().max()) <= float(tol), (i, head)
+
+
+@pytest.mark.parametrize("kernel", ["mma", "tcgen05"])
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 32)])
+def test_tree_f32_values_at_the_end_of_the_range(cuda_device, kernel, d, block):
+    """Keys, values and queries that bf16 would round to infinity."""
+    dev, h, hkv, n, ctx = cuda_device, 4, 2, 9, 150
+    c = tree_case(6, [n], [ctx], d, block, h, hkv, torch.float32, dev)
+    huge = 3.395e38
+    q = c["q"].clone()
+    q[:, :, 5] = 1e-29 * q[:, :, 5].sign()     # (products of about 3e9, times a scale of 1e-9)
+    q[2, :, 7] = -huge
+    for at in (3, 100, ctx - 2):
+        page, row = int(c["tables"][0, at // block]), at % block
+        c["pool"][page, 0, 0, :, row, 5] = huge
+    c["pool"][:, 0, 0, :, :, 7] = 1e-29
+    c["pool"][int(c["tables"][0, 100 // block]), 1, 0, :, 100 % block, 11] = huge   # (one: weights sum to more than 1)
+    cache = BlockPool(c["nb"], block, 1, hkv, d, tensor=c["pool"])
+    cache.set_prefill_kernel(kernel)
+    out = cache.tree_attention(q, 0, c["bt"], c["lens"], c["starts"], c["masks"], 1e-9)
+    status_is(0)
+    want, bound = T.attention(c["pool"], q, c["tables"], [ctx], [n], c["bits"], 1e-9)
+    check(out, want, bound)
+
+
 def test_far_pages(cuda_device):
     """Pages beyond 2^32 bytes and 2^31 elements of the pool: append at slots, attention on every
     kernel, acceptance."""

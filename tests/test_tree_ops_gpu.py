@@ -311,7 +311,8 @@ SHAPES = [  # new tokens, contexts
 ]
 
 
-@pytest.mark.parametrize("dtype,kernel", [("bf16", "mma"), ("bf16", "tcgen05"), ("bf16", "auto"), ("f32", "auto")])
+@pytest.mark.parametrize("dtype,kernel", [("bf16", "mma"), ("bf16", "tcgen05"), ("bf16", "auto"), ("f32", "auto"), ("f32", "mma"),
+                                          ("f32", "tcgen05")])
 @pytest.mark.parametrize("d,block,h,hkv", [(64, 16, 16, 2), (128, 16, 8, 2), (128, 32, 3, 3), (64, 32, 20, 4), (128, 16, 12, 1)])
 @pytest.mark.parametrize("case", range(len(SHAPES)))
 @pytest.mark.parametrize("shape", ["random", "chain", "any"])
@@ -331,7 +332,7 @@ def test_tree_attention(cuda_device, dtype, kernel, d, block, h, hkv, case, shap
     cache.close()
 
 
-KERNELS = [("bf16", "mma"), ("bf16", "tcgen05"), ("f32", "auto")]
+KERNELS = [("bf16", "mma"), ("bf16", "tcgen05"), ("f32", "auto"), ("f32", "mma"), ("f32", "tcgen05")]
 
 
 @pytest.mark.parametrize("dtype,kernel", KERNELS)
@@ -597,7 +598,7 @@ def test_accept_flags(cuda_device):
 # -------------------------------------------------------- steps of all of them
 
 
-@pytest.mark.parametrize("dtype,kernel", [("bf16", "auto"), ("bf16", "tcgen05"), ("f32", "auto")])
+@pytest.mark.parametrize("dtype,kernel", [("bf16", "auto"), ("bf16", "tcgen05"), ("f32", "auto"), ("f32", "tcgen05")])
 def test_speculation_steps(cuda_device, dtype, kernel):
     """Steps of plan, append, tree attention, acceptance and trim, captured once and replayed:
     after each, the cache holds what appending the accepted tokens one by one gives, and the
