@@ -13,19 +13,22 @@
 // tiles of 64 keys.  Four warps each read K and V (fp32) and write their parts, 128-byte swizzled, to
 // shared memory, two stages of 48 KB each (head_dim 128); q's parts are in tensor memory (in shared
 // memory they took the room of the second stages, and a product of 64 keys reads twice as much of them as
-// of K).  Roles: warps 0 - 3 q, then softmax and O (a row to a thread), 4 - 7 K, 8 - 11 V, 12 the MMAs.
+// of K).  Roles: warps 0 - 3 q, then softmax and O (a row to a thread), 4 - 7 K, 8 - 11 V, 12 the
+// MMAs.
 // Tensor memory: S_0, S_1 (P's parts a and b over them), P's part c twice, P V, q.
 //
-// What bounds it: 128 rows x 64 keys of head_dim 128 take 3.3 us of an SM, of which the products
-// are 1.5; the rest is waiting: K and V of a tile are in registers of the warps that split them, so
-// their loads start when the tile before has been written (without loads in the loop 2.5 us), and a row's
-// softmax, its parts and the addition of P V follow one another.  32 trees of 64 nodes over 4,000
-// keys, 32 heads on 8 of 128: 717 us, 188 TFLOP/s of fp32 products (mma.sync 2,460); 8 of 25 over
-// 2,000: 62 us (211); one of 64 over 1,000: 19 (34); 4 of 8 over 500 - 2,000: 30 (34).
-// Errors are half of the TF32 kernel's.  Slower: q in shared memory and one stage of K and V (79 for the 8 of
-// 25); each chunk's next load right after its split (86: a warp has few counters for loads, and the
-// waits for old ones take the new ones in); tiles' lines brought to L2 two ahead (74).  No change:
-// P V summed in tensor memory over two tiles.
+// What bounds it: latencies.  128 rows x 64 keys of head_dim 128 take 2.8 us of an SM, of which the
+// products are 1.5: K and V of a tile are in registers of the warps that split them, so their loads start
+// when the tile before has been written (without loads in the loop a quarter less), and a row's softmax, its
+// parts and the addition of P V follow one another.  32 trees of 64 nodes over 4,000 keys, 32 heads on
+// 8 of 128: 717 us, 188 TFLOP/s of fp32 products (mma.sync 2,460); 8 of 25 over 2,000: 62 us (211); one
+// of 64 over 1,000: 19 (34); 4 of 8 over 500 - 2,000: 30 (33).  Errors are half of the TF32 kernel's.
+//   Other forms: q in shared memory and one stage of K and V, 79 us for the 8 of 25; each chunk's next
+// load right after its split, 86 (a warp has few counters for loads, and the waits for old ones take the new ones
+// in); the tiles' lines brought to L2 two ahead, 74; P V summed in tensor memory over two tiles, no
+// change.  K and V by cp.async into 64 KB of their own, with one stage of V's parts or of both, 58 for the 8
+// of 25 and 670 for the 32 of 64, but 21 for the one of 64, and 2 us more where a call takes 10: over
+// 62 calls as good on average, at shorter calls worse.
 #include "pa_prefill_mma.cuh"
 #include "pa_prefill_umma.cuh"
 
@@ -51,8 +54,8 @@ struct F32Cfg {
     static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
-// Four numbers' parts: a, b, c of (x, y) in [0 .. 2].x, of (z, w) in .y.  CUT: a cut off instead of
-// rounded (what rounds to infinity).  odd: becomes NaN where an a is not finite.
+// Two numbers' parts, the first's in the low halves.  CUT: a cut off instead of rounded (what
+// rounds to infinity).  odd: becomes NaN where an a is not finite.
 template <bool CUT>
 __device__ __forceinline__ void split3(float x, float y, uint32_t& a, uint32_t& b, uint32_t& c, float& odd) {
     a = CUT ? __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632) : pack_bf16x2(x, y);
