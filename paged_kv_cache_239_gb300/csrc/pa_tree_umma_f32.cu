@@ -21,7 +21,7 @@
 // products are 1.5: K and V of a tile are in registers of the warps that split them, so their loads start
 // when the tile before has been written (without loads in the loop a quarter less), and a row's softmax, its
 // parts and the addition of P V follow one another.  32 trees of 64 nodes over 4,000 keys, 32 heads on
-// 8 of 128: 717 us, 188 TFLOP/s of fp32 products (mma.sync 2,460); 8 of 25 over 2,000: 62 us (211); one
+// 8 of 128: 708 us, 191 TFLOP/s of fp32 products (mma.sync 2,460); 8 of 25 over 2,000: 61 us (211); one
 // of 64 over 1,000: 19 (34); 4 of 8 over 500 - 2,000: 30 (33).  Errors are half of the TF32 kernel's.
 //   Other forms: q in shared memory and one stage of K and V, 79 us for the 8 of 25; each chunk's next
 // load right after its split, 86 (a warp has few counters for loads, and the waits for old ones take the new ones
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(512, 1) pa_tree_umma_f32_kernel(const PrefillP
         }
     } else if (b >= 0 && warp < 12) {
         // ============================================== K (warps 4 - 7), V (8 - 11)
-        regs_dec<104>();
+        regs_dec<112>();
         constexpr int RPP = 128 / CPR, N = C::BN / RPP, PAGES = C::BN / B;
         const bool is_v = warp >= 8;
         const int tid = threadIdx.x - (is_v ? 256 : 128), cr = tid / CPR;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(512, 1) pa_tree_umma_f32_kernel(const PrefillP
         }
         if (!ok) *abort_all = 1;
     } else if (b >= 0) {
-        regs_dec<56>();
+        regs_dec<40>();
         if (warp == 12 && kt0 < kt1) {
             // ======================================================= MMA issuer
             if (elect_one()) {
@@ -409,17 +409,21 @@ __global__ void __launch_bounds__(512, 1) pa_tree_umma_f32_kernel(const PrefillP
                 const uint64_t dK = umma_desc_sw128(sbase, 0, 1024);
                 const uint64_t dV = umma_desc_sw128(sbase + C::OFF_V, 64 * 128, 1024);
                 const int tiles_here = kt1 - kt0;
-                // parts of the factors, the small products first
-                constexpr int LEFT[6] = {2, 0, 1, 1, 0, 0}, RIGHT[6] = {0, 2, 1, 0, 1, 0};
+                // Parts of the factors, two bits each, the small products first.  (A loop, not 72
+                // products in a row: their descriptors spilled.)
+                constexpr unsigned LEFT = 0x052, RIGHT = 0x118;  // 2 0 1 1 0 0, 0 2 1 0 1 0
                 auto score = [&](int i) {
                     const uint64_t k0 = dK + (uint64_t)(((i & 1) * C::STAGE) >> 4);
-#pragma unroll
-                    for (int x = 0; x < 6; ++x)
+#pragma unroll 1
+                    for (int x = 0; x < 6; ++x) {
+                        const uint32_t a = tmem + C::Q_COL + (LEFT >> 2 * x & 3u) * (D / 2);
+                        const uint64_t b = k0 + (uint64_t)((RIGHT >> 2 * x & 3u) * (C::KP >> 4));
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            umma_bf16_ts(tmem + 64 * (i & 1), tmem + C::Q_COL + LEFT[x] * (D / 2) + 8 * k,
-                                         k0 + (uint64_t)((RIGHT[x] * C::KP + (k >> 2) * 64 * 128 + (k & 3) * 32) >> 4),
-                                         IDS, x + k > 0 ? 1u : 0u);
+                            umma_bf16_ts(tmem + 64 * (i & 1), a + 8 * k,
+                                         b + (uint64_t)(((k >> 2) * 64 * 128 + (k & 3) * 32) >> 4), IDS,
+                                         x + k > 0 ? 1u : 0u);
+                    }
                     umma_commit(bar0 + 8 * (C::S_FULL + (i & 1)));
                     umma_commit(bar0 + 8 * (C::K_EMPTY + (i & 1)));
                 };
@@ -440,14 +444,16 @@ __global__ void __launch_bounds__(512, 1) pa_tree_umma_f32_kernel(const PrefillP
                         break;
                     tc_fence_after();
                     const uint64_t v0 = dV + (uint64_t)(((i & 1) * C::STAGE) >> 4);
-                    const uint32_t part[3] = {tmem + 64u * (i & 1), tmem + 64u * (i & 1) + 32u,
-                                              tmem + C::C_COL + 32u * (i & 1)};
-#pragma unroll
-                    for (int x = 0; x < 6; ++x)
+#pragma unroll 1
+                    for (int x = 0; x < 6; ++x) {
+                        const uint32_t left = LEFT >> 2 * x & 3u;
+                        const uint32_t a = tmem + (left == 2 ? C::C_COL + 32u * (i & 1) : 64u * (i & 1) + 32u * left);
+                        const uint64_t v = v0 + (uint64_t)((RIGHT >> 2 * x & 3u) * (C::KP >> 4));
 #pragma unroll
                         for (int k = 0; k < C::BN / 16; ++k)
-                            umma_bf16_ts(tmem + C::O_COL, part[LEFT[x]] + 8 * k,
-                                         v0 + (uint64_t)((RIGHT[x] * C::KP + k * 2048) >> 4), IDV, x + k > 0 ? 1u : 0u);
+                            umma_bf16_ts(tmem + C::O_COL, a + 8 * k, v + (uint64_t)(k * (2048 >> 4)), IDV,
+                                         x + k > 0 ? 1u : 0u);
+                    }
                     umma_commit(bar0 + 8 * C::O_FULL);
                     umma_commit(bar0 + 8 * (C::V_EMPTY + (i & 1)));
                 }
