@@ -648,9 +648,8 @@ PA_API int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens
  * split, take every context to be as long as the table is wide.  With a table much
  * wider than the contexts of a short call, force PA_PREFILL_MMA (one token over 100
  * keys, 16 heads on 2 of 64: 5.0 us in a table of 7 blocks; in one of 8,192 11.1 by
- * choice, 8.2 by force; a tree of 8 nodes over 500 6.5 and 10.2, 8.8 by force).  On fp32
- * pools only a tighter table helps: 8 trees of 25 nodes over 2,000 keys, 32 heads on 8 of
- * 128, 211 us in a table of 126 blocks, 301 in one of 8,192.
+ * choice, 8.2 by force; a tree of 8 nodes over 500 6.5 and 10.2, 8.8 by force; on an
+ * fp32 pool 7.2 and 13.4).
  * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at a prefill call.
  * The workspace size follows the choice.
  * Cites: no counterpart on the pages (a choice among this library's kernels). */

@@ -57,7 +57,9 @@ double tree_umma_time(int G, int Hkv, int batch, int num_tokens, int maxb, int D
 // their bytes, the key tiles of a part and k0 more, times the rounds that the SMs take: beyond one, at
 // least 1.7, for a few CTAs more than there are SMs wait for the others to end.  Least squares over 62
 // calls at 1 to 64 parts; the better of this and mma.sync by estimate takes 2.5 % more than the best
-// (mma.sync for all: 22 %).
+// (mma.sync for all: 22 %).  Four rounds at most: parts without keys, where the table is wider than
+// the contexts, take a microsecond of an SM each (8 trees of 25 nodes over 2,000 keys, 32 heads on 8 of
+// 128, in a table of 8,192 blocks: 61 us, 136 without the limit).
 double tree_umma_f32_plan(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B, int num_sms,
                           int* splits) {
     struct Time {
@@ -68,7 +70,7 @@ double tree_umma_f32_plan(int G, int Hkv, int batch, int num_tokens, int maxb, i
     const double tiles = (double)batch * Hkv * std::max(1.0, rows / 128 + 0.3);
     const double out = 1e-6 * num_tokens * G * Hkv * D;
     double best = 0;
-    for (int n = 1; n <= 64 && (n == 1 || n <= keys); ++n) {
+    for (int n = 1; n <= 64 && (n == 1 || (n <= keys && tiles * n <= 4 * num_sms)); ++n) {
         const double x = tiles * n / num_sms, rounds = x > 1 ? std::max(x + t.rest, 1.7) : 1.0;
         const double time = t.start + (n > 1 ? t.join + t.bytes * n * out : 0) + rounds * (keys / n + t.k0) * t.tile;
         if (n == 1 || time < best) best = time, *splits = n;
