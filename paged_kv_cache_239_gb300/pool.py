@@ -8,6 +8,7 @@ device memory, every operation runs in libpagedattn's kernels.
 """
 from __future__ import annotations
 
+from functools import cached_property
 from typing import Optional
 
 import torch
@@ -37,9 +38,15 @@ class BlockPool:
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
         self.dtype = tensor.dtype
         self._device_index = tensor.get_device()
-        self._calls, self._type = B.calls(), B._dtype_code(tensor.dtype)
+        self._type = B._dtype_code(tensor.dtype)
         self.handle = B.pa_pool_create(tensor, num_blocks, num_layers, num_kv_heads, block_size,
                                        head_dim, tensor.dtype)
+
+    @cached_property
+    def _calls(self):
+        """The module of the speculation calls, which is built for one torch: loaded by the
+        first of them, so that a pool that makes none does not need it."""
+        return B.calls()
 
     # -- allocator ---------------------------------------------------------
     def allocate_block(self) -> int:
