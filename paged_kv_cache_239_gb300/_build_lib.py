@@ -3,14 +3,16 @@
 Each translation unit is compiled in parallel, then linked into one shared
 library under ``paged_kv_cache_239_gb300/_build/``.  Only one ``-gencode``
 (sm_103a) is emitted.  Beside it, for the installed Python and torch, the module
-``pagedcalls`` (``pa_calls.cpp``), which calls the library.
+``pagedcalls`` (``pa_calls.cpp``), which calls the library, and a stamp that names both.
 """
 from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -42,24 +44,64 @@ def _nvcc() -> str:
     return cand
 
 
-def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "pagedattn.h"))
-    return files
+def _older(path: str, files) -> bool:
+    """Whether ``path`` is missing or older than one of the files."""
+    if not os.path.exists(path):
+        return True
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(f) > t for f in files)
+
+
+def _library_stale() -> bool:
+    return _older(LIB_PATH, [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "pa_calls.cpp"]
+                  + [os.path.join(INCLUDE, "pagedattn.h")])
+
+
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _installed_torch() -> str:
+    """The version of the torch on the disk (found without importing torch, which takes
+    longer than the rest of the build on a cold machine)."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return re.search(r"^__version__ = ['\"](.*?)['\"]", f.read(), re.M).group(1)
+
+
+def _python_abi() -> str:
+    return sysconfig.get_config_var("SOABI")
+
+
+def calls_stamp(torch_version: str) -> str:
+    """What the module is bound to, as the file beside it says."""
+    return f"torch {torch_version}, {_python_abi()}"
+
+
+def read_calls_stamp() -> str:
+    try:
+        with open(CALLS_PATH + ".stamp") as f:
+            return f.read()
+    except OSError:
+        return "no known torch"
+
+
+def _calls_stale() -> bool:
+    """Older than its source, or for another torch (on the disk, or in this process) or Python."""
+    if _older(CALLS_PATH, [os.path.join(CSRC, "pa_calls.cpp"), os.path.join(INCLUDE, "pagedattn.h")]):
+        return True
+    stamp = read_calls_stamp()
+    loaded = sys.modules.get("torch")
+    return stamp != calls_stamp(_installed_torch()) or (
+        loaded is not None and stamp != calls_stamp(str(loaded.__version__)))
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _library_stale() or _calls_stale()
 
 
 def _compile_calls() -> str:
-    """The object of the Python module (found without importing torch, which takes
-    longer than the rest of the build on a cold machine)."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
-    inc = os.path.join(torch_dir, "include")
+    """The object of the Python module."""
+    inc = os.path.join(_torch_dir(), "include")
     obj = os.path.join(OUT_DIR, "pa_calls.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-isystem", inc,
@@ -73,7 +115,8 @@ def _compile_calls() -> str:
 
 
 def _link_calls(obj: str) -> None:
-    torch_lib = os.path.join(importlib.util.find_spec("torch").submodule_search_locations[0], "lib")
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    stamp = calls_stamp(_installed_torch())
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lpagedattn", "-Wl,-rpath,$ORIGIN",
            "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
@@ -81,12 +124,18 @@ def _link_calls(obj: str) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    if os.path.exists(CALLS_PATH + ".stamp"):  # (no module is beside another one's)
+        os.remove(CALLS_PATH + ".stamp")
     os.replace(tmp, CALLS_PATH)
+    with open(CALLS_PATH + ".stamp", "w") as f:
+        f.write(stamp)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link the library; returns its path.  Raises on failure."""
-    if not force and not _stale():
+    """Compile and link what is missing or stale of the library and the module; returns the
+    library's path.  Raises on failure."""
+    library, module = force or _library_stale(), force or _calls_stale()
+    if not library and not module:
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -108,20 +157,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls)
-        objs = list(ex.map(compile_one, SOURCES))
-        calls_obj = calls.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl", "-lpthread"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB_PATH)
-    _link_calls(calls_obj)
+        calls = ex.submit(_compile_calls) if module else None
+        objs = list(ex.map(compile_one, SOURCES)) if library else []
+    if library:
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl", "-lpthread"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB_PATH)
+    if calls is not None:
+        _link_calls(calls.result())
     return LIB_PATH
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))

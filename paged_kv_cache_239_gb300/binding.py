@@ -13,6 +13,7 @@ import os
 import re
 from typing import Optional
 
+from . import _build_lib
 from ._build_lib import CALLS_PATH, INCLUDE, LIB_PATH
 
 PA_OK = 0
@@ -165,8 +166,8 @@ _calls = None
 
 def calls():
     """The module that makes a speculation step's calls (``csrc/pa_calls.cpp``): it checks
-    the tensors and calls the library without ctypes.  Raises if it has not been built,
-    or for another torch."""
+    the tensors and calls the library without ctypes.  Raises, before any of it is loaded,
+    if it has not been built, or for another torch or Python."""
     global _calls
     if _calls is None:
         import importlib.util
@@ -174,14 +175,16 @@ def calls():
         import torch
 
         lib()  # (says how to build it)
-        spec = importlib.util.spec_from_file_location("pagedcalls", CALLS_PATH)
+        again = "python -m paged_kv_cache_239_gb300._build_lib"
         if not os.path.exists(CALLS_PATH):
-            raise RuntimeError(f"{CALLS_PATH} is missing: build it as {LIB_PATH}")
+            raise RuntimeError(f"{CALLS_PATH} is missing: build it with `{again}`")
+        built, here = _build_lib.read_calls_stamp(), _build_lib.calls_stamp(str(torch.__version__))
+        if built != here:
+            raise RuntimeError(f"{CALLS_PATH} was built for {built}, not for {here}: "
+                               f"build it again with `{again}`")
+        spec = importlib.util.spec_from_file_location("pagedcalls", CALLS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        if module.torch_version != torch.__version__.split("+")[0]:
-            raise RuntimeError(f"{CALLS_PATH} was built for torch {module.torch_version}, not "
-                               f"{torch.__version__}: build it again")
         _calls = module
     return _calls
 

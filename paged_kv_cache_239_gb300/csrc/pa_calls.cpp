@@ -14,7 +14,6 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include <climits>
 
@@ -292,8 +291,6 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "pagedcalls", nullptr, -1, kMethod
 
 PyMODINIT_FUNC PyInit_pagedcalls() {
     PyObject* m = PyModule_Create(&kModule);
-    if (m && (PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) ||
-              PyModule_AddIntConstant(m, "WRONG_DEVICE", kWrongDevice)))
-        Py_CLEAR(m);
+    if (m && PyModule_AddIntConstant(m, "WRONG_DEVICE", kWrongDevice)) Py_CLEAR(m);
     return m;
 }

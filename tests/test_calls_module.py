@@ -31,3 +31,71 @@ def test_only_the_speculation_calls_need_the_module(pa_lib, monkeypatch):
     with pytest.raises(ValueError, match="device"):
         cache.device_trim_sequences(i32(5), i32(2, 4), i32(2), i32(2))
     cache.close()
+
+
+@pytest.fixture
+def built(tmp_path, monkeypatch):
+    """The build in a folder of its own, its compilers only taken down (they write their output)."""
+    import subprocess
+
+    from paged_kv_cache_239_gb300 import _build_lib as L
+
+    for name in ("LIB_PATH", "CALLS_PATH"):
+        monkeypatch.setattr(L, name, str(tmp_path / getattr(L, name).rsplit("/", 1)[1]))
+    monkeypatch.setattr(L, "OUT_DIR", str(tmp_path))
+    L.commands = []
+
+    def run(cmd, **kw):
+        L.commands.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(L.subprocess, "run", run)
+    yield L
+    del L.commands
+
+
+def test_the_module_is_built_again_for_another_torch_or_python(built, monkeypatch):
+    L = built
+    assert L._stale()
+    L.build()
+    assert not L._stale() and len(L.commands) == len(L.SOURCES) + 3
+    L.commands.clear()
+    L.build()
+    assert not L.commands
+    # another torch on the disk (and in the next process), another Python: the module alone is built again
+    def another(change):
+        with pytest.MonkeyPatch.context() as m:
+            change(m)
+            assert L._stale()
+            L.build()
+            outs = [c[c.index("-o") + 1] for c in L.commands]
+            assert len(outs) == 2 and outs[0].endswith("pa_calls.o") and "pagedcalls" in outs[1]
+            assert not L._stale()
+            L.commands.clear()
+        assert L._stale()
+        L.build()
+        assert not L._stale()
+        L.commands.clear()
+
+    another(lambda m: (m.setattr(L, "_installed_torch", lambda: "9.9.0"), m.setattr(torch, "__version__", "9.9.0")))
+    another(lambda m: m.setattr(L, "_python_abi", lambda: "cpython-399-other"))
+    # another torch in this process than the one on the disk
+    monkeypatch.setattr(torch, "__version__", "9.9.1")
+    assert L._stale()
+
+
+def test_another_torchs_module_is_not_loaded(pa_lib, monkeypatch):
+    """Refused before any of its code is linked, and with what mends it."""
+    import importlib.util
+
+    assert pa_lib.calls() is not None
+    monkeypatch.setattr(pa_lib, "_calls", None)
+    monkeypatch.setattr(importlib.util, "module_from_spec", lambda spec: pytest.fail("loaded"))
+    monkeypatch.setattr(torch, "__version__", "9.9.0")
+    with pytest.raises(RuntimeError, match="9.9.0.*_build_lib"):
+        pa_lib.calls()
+    monkeypatch.setattr(torch, "__version__", torch.version.__version__)
+    monkeypatch.setattr(pa_lib._build_lib, "_python_abi", lambda: "cpython-399-other")
+    with pytest.raises(RuntimeError, match="cpython-399-other.*_build_lib"):
+        pa_lib.calls()
