@@ -15,6 +15,7 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -57,8 +58,23 @@ def _library_stale() -> bool:
                   + [os.path.join(INCLUDE, "pagedattn.h")])
 
 
-def _torch_dir() -> str:
-    return importlib.util.find_spec("torch").submodule_search_locations[0]
+def _torch_dir() -> Optional[str]:
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def calls_need() -> str:
+    """What the module cannot be built without and is not there ("": nothing).  The library, which
+    C programs use by itself, needs none of it."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return "torch"
+    if not (os.path.exists(os.path.join(torch_dir, "include", "c10", "cuda", "CUDAStream.h"))
+            and os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so"))):
+        return "a torch for CUDA, with its headers"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return ""
 
 
 def _installed_torch() -> str:
@@ -86,7 +102,10 @@ def read_calls_stamp() -> str:
 
 
 def _calls_stale() -> bool:
-    """Older than its source, or for another torch (on the disk, or in this process) or Python."""
+    """Older than its source, or for another torch (on the disk, or in this process) or Python;
+    False where it cannot be built."""
+    if calls_need():
+        return False
     if _older(CALLS_PATH, [os.path.join(CSRC, "pa_calls.cpp"), os.path.join(INCLUDE, "pagedattn.h")]):
         return True
     stamp = read_calls_stamp()
@@ -132,9 +151,9 @@ def _link_calls(obj: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link what is missing or stale of the library and the module; returns the
-    library's path.  Raises on failure."""
-    library, module = force or _library_stale(), force or _calls_stale()
+    """Compile and link what is missing or stale of the library and, where it can be built
+    (``calls_need``), the module; returns the library's path.  Raises on failure."""
+    library, module = force or _library_stale(), _calls_stale() or (force and not calls_need())
     if not library and not module:
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -173,3 +192,5 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    if calls_need():
+        print(f"{CALLS_NAME} was not built: it needs {calls_need()}")

@@ -99,3 +99,38 @@ def test_another_torchs_module_is_not_loaded(pa_lib, monkeypatch):
     monkeypatch.setattr(pa_lib._build_lib, "_python_abi", lambda: "cpython-399-other")
     with pytest.raises(RuntimeError, match="cpython-399-other.*_build_lib"):
         pa_lib.calls()
+
+
+@pytest.mark.parametrize("what", ["no torch", "no c10 for CUDA", "no Python headers"])
+def test_the_library_is_built_where_the_module_cannot_be(built, monkeypatch, tmp_path, what):
+    """C programs need neither torch nor Python's headers."""
+    L = built
+    if what == "no torch":
+        find = L.importlib.util.find_spec
+        monkeypatch.setattr(L.importlib.util, "find_spec", lambda name: None if name == "torch" else find(name))
+    elif what == "no c10 for CUDA":
+        (tmp_path / "torch").mkdir()
+        monkeypatch.setattr(L, "_torch_dir", lambda: str(tmp_path / "torch"))
+    else:
+        monkeypatch.setattr(L.sysconfig, "get_paths", lambda: {"include": str(tmp_path / "none")})
+    assert L.build() == L.LIB_PATH and L.os.path.exists(L.LIB_PATH)
+    assert len(L.commands) == len(L.SOURCES) + 1 and not L.os.path.exists(L.CALLS_PATH)
+    L.commands.clear()
+    L.build()
+    assert not L.commands   # (nothing is stale)
+
+
+def test_a_module_that_does_not_compile_fails_the_build_after_the_library(built, monkeypatch):
+    L = built
+    run = L.subprocess.run
+
+    def fail(cmd, **kw):
+        done = run(cmd, **kw)
+        if cmd[0] == "g++":
+            done.returncode, done.stderr = 1, "no such header"
+        return done
+
+    monkeypatch.setattr(L.subprocess, "run", fail)
+    with pytest.raises(RuntimeError, match="pa_calls.cpp"):
+        L.build()
+    assert not L._library_stale() and L._calls_stale()
