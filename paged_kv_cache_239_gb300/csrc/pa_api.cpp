@@ -1065,11 +1065,12 @@ int norm_rope_launch(const pa_pool* pool, const pa::NormRopeParams& p, const cha
     return e == cudaSuccess ? PA_OK : cuda_fail(e, what);
 }
 
-// Attention of new tokens: causal, or (tree_masks) of drafted trees.
-int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const int* block_tables,
-               int max_blocks_per_seq, const int* context_lens, const int* query_starts,
-               const uint32_t* tree_masks, int mask_words, int batch, int num_tokens, int num_heads,
-               float scale, void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+// Attention of new tokens: causal, or of drafted trees (whose masks are NULL where there are no tokens).
+int attend_new(bool tree, void* out, const void* q, const pa_pool* pool, int layer,
+               const int* block_tables, int max_blocks_per_seq, const int* context_lens,
+               const int* query_starts, const uint32_t* tree_masks, int mask_words, int batch,
+               int num_tokens, int num_heads, float scale, void* workspace, size_t workspace_bytes,
+               pa_stream_t stream) {
     if (int rc = check_pool(pool)) return rc;
     if (int rc = check_layer(pool, layer)) return rc;
     const pa::PoolGeom& g = pool->g;
@@ -1077,8 +1078,7 @@ int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const i
     if (!std::isfinite(scale * 1.4426950408889634f))
         return fail(PA_ERR_INVALID_ARG, "scale is not finite (times log2 e)");
     PrefillShape sh;
-    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq,
-                               tree_masks != nullptr, &sh))
+    if (int rc = prefill_shape(pool, batch, num_tokens, num_heads, max_blocks_per_seq, tree, &sh))
         return rc;
     if (batch == 0 || num_tokens == 0) return PA_OK;
     if (!out || !q || !aligned(out, 16) || !aligned(q, 16))
@@ -1124,14 +1124,14 @@ int attend_new(void* out, const void* q, const pa_pool* pool, int layer, const i
         if (int rc = pool_tmaps(pool)) return rc;
         p.slot_blk = pool->tma_slots[0];
         p.slot_layer = pool->tma_slots[1];
-        e = tree_masks ? pa::launch_tree_umma(p, pool->tmaps, g.D, g.B, s)
-                       : pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
+        e = tree ? pa::launch_tree_umma(p, pool->tmaps, g.D, g.B, s)
+                 : pa::launch_prefill_umma(p, pool->tmaps, g.D, g.B, s);
     } else {
         p.row_tile = sh.row_tile;
-        e = !tree_masks      ? pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s)
-            : g.dtype == 1 ? pa::launch_tree_mma_bf16(p, g.D, g.B, s)
+        e = !tree               ? pa::launch_prefill_mma(p, g.dtype, g.D, g.B, s)
+            : g.dtype == 1      ? pa::launch_tree_mma_bf16(p, g.D, g.B, s)
             : p.row_tile == 128 ? pa::launch_tree_umma_f32(p, g.D, g.B, s)
-                           : pa::launch_tree_mma_f32(p, g.D, g.B, s);
+                                : pa::launch_tree_mma_f32(p, g.D, g.B, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
     return PA_OK;
@@ -1279,7 +1279,7 @@ int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, int laye
                          const int* query_starts, int batch, int num_tokens, int num_heads,
                          float scale, void* workspace, size_t workspace_bytes,
                          pa_stream_t stream) {
-    return attend_new(out, q, pool, layer, block_tables, max_blocks_per_seq, context_lens,
+    return attend_new(false, out, q, pool, layer, block_tables, max_blocks_per_seq, context_lens,
                       query_starts, nullptr, 0, batch, num_tokens, num_heads, scale, workspace,
                       workspace_bytes, stream);
 }
@@ -1306,7 +1306,7 @@ int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int layer,
         if (batch > 0 && num_tokens > 0)
             return fail(PA_ERR_INVALID_ARG, "tree_masks must be non-NULL and 4-byte aligned");
     }
-    return attend_new(out, q, pool, layer, block_tables, max_blocks_per_seq, context_lens,
+    return attend_new(true, out, q, pool, layer, block_tables, max_blocks_per_seq, context_lens,
                       query_starts, tree_masks, mask_words, batch, num_tokens, num_heads, scale,
                       workspace, workspace_bytes, stream);
 }

@@ -153,3 +153,17 @@ def test_reference_masks_and_plan():
     assert p.slots == [36, 37, 38, 39, 32, 28, -1] and p.positions == [0, 1, 1, 2, 3, 0, 0]
     tables, stack = T.trim(4, p.tables, p.stack, [5, 1], [2, 0])
     assert stack == [7, 8] and tables.tolist() == [[9, -1, -1], [-1, -1, -1]]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("masks", [None, P + 5 * MB])
+@pytest.mark.parametrize("nothing", [dict(num_tokens=0), dict(batch=0), dict(batch=0, num_tokens=0)])
+def test_trees_of_nothing_on_every_kernel(pa_lib, dtype, kernel, masks, nothing):
+    """An empty tensor's address is NULL: a call without tokens is still a call of trees."""
+    h = pa_lib.pa_pool_create(P, 8, 2, 2, 16, 64, dtype)
+    pa_lib.pa_pool_set_prefill_kernel(h, kernel)
+    args = {**TREE, "tree_masks": masks, **nothing}
+    pa_lib.pa_tree_attention(args.pop("out"), args.pop("q"), h, **args, stream=0)
+    assert pa_lib.pa_tree_workspace_size(h, args["batch"], args["num_tokens"], 4, 4) == 0
+    pa_lib.pa_pool_destroy(h)
