@@ -835,8 +835,8 @@ PA_API int pa_device_trim_sequences(pa_pool* pool, void* dev_stack, int* block_t
  * Device int32, no output overlaps an input or another.  Starts that are no starts, more
  * than 1024 new tokens or more than context_lens[b] set PA_STATUS_BAD_LENGTH: nothing is
  * accepted and the length stays; a parent that is not below its child sets it too, and the
- * node is not accepted.  A slot that is no page's (a dry stack's -1 among them) sets
- * PA_STATUS_BAD_BLOCK_ID and that row does not move.
+ * node is not accepted (token 0 is, being certain: it counts as the root).  A slot that is no
+ * page's (a dry stack's -1 among them) sets PA_STATUS_BAD_BLOCK_ID and that row does not move.
  * Cites: no counterpart on the pages (they draft no tokens).
  */
 PA_API int pa_device_accept_tree(pa_pool* pool, const int64_t* slots, const int* parents,

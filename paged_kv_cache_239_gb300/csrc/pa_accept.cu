@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(kAcceptThreads) pa_accept_kernel(const AcceptP
             s_child[i] = kMaxTreeNodes;
         }
         __syncthreads();
-        if (i > 0 && i < nodes) {
-            if (up < -1 || up >= i) {
+        if (i < nodes) {
+            if (up < -1 || up >= i) {  // (node 0 is the root all the same)
                 if (part == 0) atomicOr(p.g.status, kStatusBadLength);
             } else if (up >= 0 && token == s_target[up]) {
                 atomicMin(s_child + up, i);

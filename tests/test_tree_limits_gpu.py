@@ -425,3 +425,24 @@ def test_trim_frees_what_a_prompt_took(cuda_device):
     status_is(B.PA_STATUS_BAD_BLOCK_ID)
     lost = {int(table[b, j]) for b, j in holes}
     assert stack_ids(stack) == [x for x in stack_ids(before) if x not in lost]
+
+
+def test_accept_flags_a_root_with_a_parent(cuda_device):
+    """Node 0 is the root whatever its parent says, but a parent that is not below it is flagged, as
+    in the plan; the rest of the tree is decided as ever."""
+    dev = cuda_device
+    pool_t = randn((4, 2, 1, 1, 16, 64), torch.bfloat16, dev, 1)
+    before = pool_t.clone()
+    cache = BlockPool(4, 16, 1, 1, 64, tensor=pool_t)
+    args = (ints([9, 5, 6, 9, 7], dev), ints([6, 0, 3, 7, 2], dev), ints([3, 2], dev), ints([0, 3, 5], dev), 3)
+    slots = ints([0, 1, 2, 16, 17], dev, torch.int64)
+    want = [[2, 2], [[0, 2, -1], [0, 1, -1]], [3, 2], [2, 2]]
+    for root, status in ((-1, 0), (0, B.PA_STATUS_BAD_LENGTH), (5, B.PA_STATUS_BAD_LENGTH), (-2, B.PA_STATUS_BAD_LENGTH)):
+        for parents in ([root, 0, 0, -1, 0], [-1, 0, 0, root, 0]):
+            pool_t.copy_(before)
+            out = cache.device_accept_tree(slots, ints(parents, dev), *args)
+            status_is(status)
+            assert [x.tolist() for x in out] == want
+            assert torch.equal(pool_t[0, :, 0, 0, 1], before[0, :, 0, 0, 2])
+            assert torch.equal(pool_t[1], before[1])
+    cache.close()
