@@ -446,3 +446,25 @@ def test_accept_flags_a_root_with_a_parent(cuda_device):
             assert torch.equal(pool_t[0, :, 0, 0, 1], before[0, :, 0, 0, 2])
             assert torch.equal(pool_t[1], before[1])
     cache.close()
+
+
+@pytest.mark.parametrize("dtype,kernel", KERNELS)
+@pytest.mark.parametrize("new,ctx,h,hkv,d", [([8], [508], 16, 2, 64), ([9, 25, 17, 12], [700, 3000, 1500, 2500], 32, 8, 128),
+                                             ([64, 50], [3000, 2000], 8, 2, 128), ([5, 9], [20000, 30011], 8, 2, 64)])
+def test_tree_attention_repeats_itself(cuda_device, dtype, kernel, new, ctx, h, hkv, d):
+    """Equal calls give equal bits, whatever the workspace and the output held before."""
+    dev, dt, block = cuda_device, DT[dtype], 16
+    c = tree_case(17, new, ctx, d, block, h, hkv, dt, dev)
+    cache = BlockPool(c["nb"], block, 1, hkv, d, tensor=c["pool"])
+    cache.set_prefill_kernel(kernel)
+    need = cache.tree_workspace_size(len(new), sum(new), h, c["bt"].shape[1])
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    outs = []
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        out = torch.full(c["q"].shape, float(fill), dtype=dt, device=dev)
+        for _ in range(3):
+            cache.tree_attention(c["q"], 0, c["bt"], c["lens"], c["starts"], c["masks"], d ** -0.5, out=out, workspace=ws)
+            outs.append(out.clone())
+    status_is(0)
+    assert all(torch.equal(outs[0], x) for x in outs[1:])
