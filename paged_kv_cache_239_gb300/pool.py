@@ -8,6 +8,7 @@ device memory, every operation runs in libpagedattn's kernels.
 """
 from __future__ import annotations
 
+import operator
 from functools import cached_property
 from typing import Optional
 
@@ -212,7 +213,8 @@ class BlockPool:
                 self._check_new_rows(q, k, v, q_weight, k_weight, rope),
                 self._check_dense(positions, rows, _I32, "positions"),
                 self._check_dense(slots, rows, _I64, "slots"),
-                self._check_dense(out, rows + (q.shape[1], self.head_dim), self.dtype, "out")))
+                self._check_dense(out, rows + (q.shape[1], self.head_dim), self.dtype, "out")),
+                layer=layer, reals={"eps": eps})
         return out
 
     def set_prefill_kernel(self, kind: str) -> None:
@@ -283,7 +285,8 @@ class BlockPool:
                 self._check_batch(block_tables, context_lens, query_starts),
                 self._check_dense(tree_masks, (q.shape[0], tree_masks.shape[-1]), _I32, "tree_masks"),
                 workspace is None or self._check_dense(workspace, workspace.shape, workspace.dtype,
-                                                       "workspace")))
+                                                       "workspace")),
+                layer=layer, reals={"scale": scale})
         return out
 
     # -- new tokens planned, drafted trees decided --------------------------
@@ -330,7 +333,8 @@ class BlockPool:
                 self._check_dense(slots, rows, _I64, "slots"),
                 self._check_dense(positions, rows, _I32, "positions"),
                 tree_masks is None or self._check_dense(tree_masks, (num_tokens, mask_words), _I32,
-                                                        "tree_masks")))
+                                                        "tree_masks")),
+                num_tokens=num_tokens, mask_words=mask_words)
         return context_lens, query_starts, slots, positions, tree_masks
 
     def device_trim_sequences(self, stack: torch.Tensor, block_tables: torch.Tensor,
@@ -380,7 +384,7 @@ class BlockPool:
                 self._check_dense(nodes, (batch, max_path), _I32, "nodes"),
                 [self._check_dense(t, seqs, _I32, name) for t, name in (
                     (context_lens, "context_lens"), (counts, "counts"), (next_tokens, "next_tokens"),
-                    (next_lens, "next_lens"))]))
+                    (next_lens, "next_lens"))]), max_path=max_path)
         return counts, nodes, next_tokens, next_lens
 
     # -- pages --------------------------------------------------------------
@@ -470,14 +474,24 @@ class BlockPool:
         if self._device_index < 0 or torch.cuda.current_device() != self._device_index:
             raise ValueError(f"the pool is on {self.pool.device}, which is not the current CUDA device")
 
-    def _refused(self, rc: int, name: str, checks) -> None:
-        """A call that did not go through: the library's error, or what is wrong with
-        the tensors (which the call only looked over)."""
+    def _refused(self, rc: int, name: str, checks, reals=None, **ints) -> None:
+        """A call that did not go through: the library's error, or what is wrong with the tensors
+        (which the call only looked over) or the numbers (``ints``; ``reals``: those that need not be whole)."""
         if rc > 0:
             B.check(rc, name)
         if rc == self._calls.WRONG_DEVICE:
             self._check_current()
         checks()
+        for key, value in ints.items():
+            try:
+                fits = -(1 << 31) <= operator.index(value) < 1 << 31
+            except TypeError:
+                raise TypeError(f"{name}: {key} must be an int, not {value!r}") from None
+            if not fits:
+                raise ValueError(f"{name}: {key} {value} does not fit 32 bits")
+        for key, value in (reals or {}).items():
+            if not hasattr(value, "__float__") and not hasattr(value, "__index__"):
+                raise TypeError(f"{name}: {key} must be a number, not {value!r}")
         raise TypeError(f"{name}: an argument is not of the type that the call takes")
 
     def _check_dense(self, t: torch.Tensor, shape, dtype, name: str) -> None:

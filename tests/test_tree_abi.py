@@ -167,3 +167,27 @@ def test_trees_of_nothing_on_every_kernel(pa_lib, dtype, kernel, masks, nothing)
     pa_lib.pa_tree_attention(args.pop("out"), args.pop("q"), h, **args, stream=0)
     assert pa_lib.pa_tree_workspace_size(h, args["batch"], args["num_tokens"], 4, 4) == 0
     pa_lib.pa_pool_destroy(h)
+
+
+def test_refused_numbers_are_named(pa_lib):
+    """A number of the wrong type, or one that the call's 32 bits do not hold, is named."""
+    from paged_kv_cache_239_gb300.pool import BlockPool
+
+    cache = BlockPool(4, 16, 1, 2, 64, tensor=torch.zeros((4, 2, 1, 2, 16, 64), dtype=torch.bfloat16))
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    q, kv = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    bt, lens, starts, stack, slots = i32(2, 4), i32(2), i32(3), i32(5), torch.zeros(3, dtype=torch.int64)
+    ws = torch.zeros(1, dtype=torch.uint8)
+    plan = dict(context_lens=i32(2), query_starts=starts, slots=slots, positions=i32(3))
+    for name, call in (
+        ("layer", lambda: cache.tree_attention(q, "0", bt, lens, starts, i32(3, 1), 1.0, workspace=ws)),
+        ("layer", lambda: cache.tree_attention(q, 1 << 40, bt, lens, starts, i32(3, 1), 1.0, workspace=ws)),
+        ("scale", lambda: cache.tree_attention(q, 0, bt, lens, starts, i32(3, 1), None, workspace=ws)),
+        ("layer", lambda: cache.norm_rope_write_kv_slots(0.5, q, kv, kv, i32(3), slots)),
+        ("eps", lambda: cache.norm_rope_write_kv_slots(0, q, kv, kv, i32(3), slots, eps="small")),
+        ("num_tokens", lambda: cache.device_plan_tokens(stack, bt, lens, lens, 3.0, **plan)),
+        ("mask_words", lambda: cache.device_plan_tokens(stack, bt, lens, lens, 3, tree_masks=i32(3, 1), mask_words=1.0, **plan)),
+        ("max_path", lambda: cache.device_accept_tree(slots, i32(3), i32(3), i32(3), lens, starts, 2.0, nodes=i32(2, 2))),
+    ):
+        with pytest.raises((TypeError, ValueError), match=name):
+            call()
