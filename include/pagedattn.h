@@ -622,9 +622,11 @@ PA_API int pa_prefill_attention(void* out, const void* q, const pa_pool* pool, i
  *   mask_words    1 .. 32.  A sequence of more than 32 * mask_words new tokens sets
  *                 PA_STATUS_BAD_LENGTH and its output rows are zero.
  * The other arguments, the products' rounding (fp32: in two TF32 or three bf16 parts, off by
- * 2^-22 at most either way), bad entries and the choice of the kernel
- * (pa_pool_set_prefill_kernel) as there; the workspace is pa_tree_workspace_size().  What
- * lies in the cache at positions that a row does not see, be it NaN, does not reach it.
+ * 2^-22 at most either way; bf16: the weights in bf16 before their product with V, which makes
+ * outputs' errors 1.9e-3 to 2.3e-3 of their size where rounding them alone makes 1.7e-3), bad
+ * entries and the choice of the kernel (pa_pool_set_prefill_kernel) as there; the workspace is
+ * pa_tree_workspace_size().  Equal calls give equal bits.  What lies in the cache at
+ * positions that a row does not see, be it NaN, does not reach it.
  * Cites: as pa_prefill_attention.
  */
 PA_API int pa_tree_attention(void* out, const void* q, const pa_pool* pool, int layer,
@@ -648,8 +650,8 @@ PA_API int pa_tree_workspace_size(const pa_pool* pool, int batch, int num_tokens
  * split, take every context to be as long as the table is wide.  With a table much
  * wider than the contexts of a short call, force PA_PREFILL_MMA (one token over 100
  * keys, 16 heads on 2 of 64: 5.0 us in a table of 7 blocks; in one of 8,192 11.1 by
- * choice, 8.2 by force; a tree of 8 nodes over 500 6.5 and 10.2, 8.8 by force; on an
- * fp32 pool 7.2 and 13.4).
+ * choice, 8.2 by force; a tree of 8 nodes over 500 6.3 and 9.9, 8.7 by force; on an
+ * fp32 pool 7.4 and 13.1, 11.0 by force).
  * The others force one; tcgen05 on an fp32 pool: PA_ERR_UNSUPPORTED at a prefill call.
  * The workspace size follows the choice.
  * Cites: no counterpart on the pages (a choice among this library's kernels). */
@@ -771,9 +773,10 @@ PA_API int pa_compact_workspace_size(const pa_pool* pool, size_t* bytes);
  *   parents       device int32 [num_tokens], each row's parent as an index within its
  *                 sequence's new tokens, -1 for a root; NULL: each token follows the one
  *                 before it.  A parent that is not below its child sets
- *                 PA_STATUS_BAD_LENGTH and counts as -1.
+ *                 PA_STATUS_BAD_LENGTH and counts as -1.  A row's walk to its root takes a step
+ *                 per ancestor (a chain of 1,024: 58 us), so long chains are given as NULL.
  *   num_tokens    rows of the batch, at least the sum of the counts, at most 2^30.
- *   context_lens  [batch]: cached_lens[b] + n_b.
+ *   context_lens  [batch]: cached_lens[b] + n_b (0 where cached_lens[b] is no length of the table's).
  *   query_starts  [batch + 1]: the prefix sums of n_b.
  *   slots         int64 [num_tokens], 8-byte aligned: page * block_size + row, -1 behind
  *                 the last sequence and where a page is missing.

@@ -1,8 +1,8 @@
-// pa_accept.cu -- drafted trees decided: the longest path of nodes that the model chose itself,
-// and the K and V of its tokens moved up behind the cached ones.
+// pa_accept.cu -- drafted trees decided: the path from the root along the nodes that the model chose
+// itself, and the K and V of its tokens moved up behind the cached ones.
 //
 // A node is accepted where its parent is and its token is the model's choice after the parent
-// (the lowest such node where there are several).  Every node bids for its parent's link with an
+// (the lowest such node where there are several, whose path need not be the longest).  Every node bids for its parent's link with an
 // atomic minimum in shared memory, so the link does not depend on the threads' timing; the path is
 // then one thread's walk from the root.
 //

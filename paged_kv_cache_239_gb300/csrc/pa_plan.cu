@@ -8,13 +8,16 @@
 // is token starts_b + i of the batch (starts: the prefix sums of n) at slot
 // page((c_b + i) / B) * B + (c_b + i) % B.
 //
-// What bounds it: latency (the bytes of 256 trees of 64 nodes would take 0.05 us).  Every CTA of
-// the cluster scans the sequences by itself (a thread each), so that no CTA waits for another
-// but for the stack's height, which is read before it is written; then the tokens are dealt out: a
-// binary search in the starts names the sequence, and four tokens of a thread have their pages on
-// their way at once.  Plan and trim together, on the device: 8 trees of 8 nodes 5.4 us, 256 trees
-// of up to 64 10.9, 16 prompts of 500 to 4,096 tokens 12 (7.0, 11.9 and 13.5 with one token on its
-// way, a scan each for pages and tokens, and the height read first).
+// Every CTA of the cluster scans the sequences by itself (a thread each), so that no CTA waits for
+// another but for the stack's height, which is read before it is written; then the tokens are dealt
+// out: a binary search in the starts names the sequence, and four tokens of a thread have their
+// pages on their way at once.  What bounds it is never the bytes (256 trees of 64 nodes: 0.05 us):
+// small batches wait for a launch and four dependent loads, 2 to 3 us each of plan and trim; many
+// tokens keep the one cluster's eight SMs at work, of whose cycles 53 % issue (256 trees of up to
+// 64), with searches, the ancestors' walks and scattered stores.  On the device, plan / trim: 8
+// trees of 8 nodes 3.1 / 2.5 us, 256 trees of up to 64 7.7 / 3.4, 16 prompts of 500 to 4,096 tokens
+// 7.2 / 4.8; both together 5.3, 11.1 and 12.0 (7.0, 11.9 and 13.5 with one token on its way, a scan
+// each for pages and tokens, and the height read first).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

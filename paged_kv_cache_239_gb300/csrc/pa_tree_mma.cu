@@ -10,9 +10,12 @@ namespace {
 // The time of a call, in us, whose contexts are split in n parts: 2.5 to start, the join of more
 // than eight parts, and the tiles of a part (and k0 more: its start and join) at `tile` each,
 // which changes by `fill` of itself from empty to full row tiles, longer by `share` of the CTAs
-// that an SM has.  Least squares over 43 calls of 1 to 48 trees at every row tile and n; the
-// chosen ones take 5 % more than the best of each (fp32; tiles of 64 rows alone: 27 %) and 3 % (bf16,
-// the choice of tcgen05 included).
+// that an SM has.  Least squares over 43 calls of 1 to 48 trees at every row tile and n, all in
+// tables as wide as the contexts; there the chosen ones take 5 % more than the best of each (fp32;
+// tiles of 64 rows alone: 27 %) and 3 % (bf16, the choice of tcgen05 included).  The width stands
+// for the lengths, so in wider tables the choice is worse: a tree of 8 nodes over 500 in a table of
+// 8,192 blocks takes 9.9 us by choice and 8.7 on mma.sync by force (bf16; 6.3 in a tight table), on
+// fp32 pools 13.1 and 11.0 (7.4).
 struct TreeTime {
     double tile, k0, share, base, fill, join;
 };
@@ -56,8 +59,8 @@ double tree_umma_time(int G, int Hkv, int batch, int num_tokens, int maxb, int D
 // The same for the tcgen05 kernel on fp32 pools (one CTA per SM): start, the join of n parts by
 // their bytes, the key tiles of a part and k0 more, times the rounds that the SMs take: beyond one, at
 // least 1.7, for a few CTAs more than there are SMs wait for the others to end.  Least squares over 62
-// calls at 1 to 64 parts; the better of this and mma.sync by estimate takes 2.5 % more than the best
-// (mma.sync for all: 22 %).  Four rounds at most: parts without keys, where the table is wider than
+// calls at 1 to 64 parts in tight tables; the better of this and mma.sync by estimate takes 2.5 % more
+// than the best (mma.sync for all: 22 %).  Four rounds at most: parts without keys, where the table is wider than
 // the contexts, take a microsecond of an SM each (8 trees of 25 nodes over 2,000 keys, 32 heads on 8 of
 // 128, in a table of 8,192 blocks: 61 us, 136 without the limit).
 double tree_umma_f32_plan(int G, int Hkv, int batch, int num_tokens, int maxb, int D, int B, int num_sms,

@@ -20,9 +20,12 @@
 // What bounds it: latencies.  128 rows x 64 keys of head_dim 128 take 2.8 us of an SM, of which the
 // products are 1.5: K and V of a tile are in registers of the warps that split them, so their loads start
 // when the tile before has been written (without loads in the loop a quarter less), and a row's softmax, its
-// parts and the addition of P V follow one another.  32 trees of 64 nodes over 4,000 keys, 32 heads on
-// 8 of 128: 708 us, 191 TFLOP/s of fp32 products (mma.sync 2,460); 8 of 25 over 2,000: 61 us (211); one
-// of 64 over 1,000: 19 (34); 4 of 8 over 500 - 2,000: 30 (33).  Errors are half of the TF32 kernel's.
+// parts and the addition of P V follow one another.  Nor are K and V split once for all: the two row
+// tiles of 64 nodes of 4 heads are CTAs of their own, and each splits both.  32 trees of 64 nodes over
+// 4,000 keys, 32 heads on 8 of 128: 712 us, 189 TFLOP/s of fp32 products (mma.sync 2,490; elementary fp32
+// operations of torch 6,970; the six products alone 428); 8 of 25 over 2,000: 61 us (212; 1,000; 21); one
+// of 64 over 1,000: 19 (34); 4 of 8 over 500 - 2,000: 30 (33).  Errors are half of the TF32 kernel's
+// (8 of 25: 4.3e-7 of the output's size, 8.8e-7 there, 1.1e-6 in elementary fp32 operations).
 //   Other forms: q in shared memory and one stage of K and V, 79 us for the 8 of 25; each chunk's next
 // load right after its split, 86 (a warp has few counters for loads, and the waits for old ones take the new ones
 // in); the tiles' lines brought to L2 two ahead, 74; P V summed in tensor memory over two tiles, no
