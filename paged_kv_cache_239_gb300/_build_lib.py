@@ -7,6 +7,7 @@ library under ``paged_kv_cache_239_gb300/_build/``.  Only one ``-gencode``
 """
 from __future__ import annotations
 
+import contextlib
 import importlib.util
 import os
 import re
@@ -143,11 +144,16 @@ def _link_calls(obj: str) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    if os.path.exists(CALLS_PATH + ".stamp"):  # (no module is beside another one's)
+    if read_calls_stamp() == stamp:
+        os.replace(tmp, CALLS_PATH)
+        return
+    # no module stands beside another one's stamp
+    with contextlib.suppress(FileNotFoundError):
         os.remove(CALLS_PATH + ".stamp")
     os.replace(tmp, CALLS_PATH)
-    with open(CALLS_PATH + ".stamp", "w") as f:
+    with open(tmp, "w") as f:
         f.write(stamp)
+    os.replace(tmp, CALLS_PATH + ".stamp")
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

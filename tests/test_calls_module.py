@@ -134,3 +134,21 @@ def test_a_module_that_does_not_compile_fails_the_build_after_the_library(built,
     with pytest.raises(RuntimeError, match="pa_calls.cpp"):
         L.build()
     assert not L._library_stale() and L._calls_stale()
+
+
+def test_a_build_for_the_same_torch_leaves_the_stamp_in_its_place(built, monkeypatch):
+    """Processes that build at once do not take the module from one another."""
+    L = built
+    L.build()
+    stamp = L.read_calls_stamp()
+    seen = []
+    replace = L.os.replace
+
+    def watched(a, b):
+        replace(a, b)
+        seen.append(L.read_calls_stamp())
+
+    monkeypatch.setattr(L.os, "replace", watched)
+    monkeypatch.setattr(L.os, "remove", lambda path: pytest.fail("removed"))
+    L.build(force=True)
+    assert seen and all(x == stamp for x in seen)
